@@ -20,6 +20,7 @@ __all__ = [
     "MoEError", "lib", "library_path", "declared_symbols",
     "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3",
     "MOE_OP_DISPATCH_LAYOUT", "MOE_OP_GROUPED_FFN", "MOE_OP_EXPERT_GEMM", "MOE_OP_ROUTER", "MOE_OP_EXPERT_DGRAD",
+    "MOE_OP_BALANCE_LOSS",
     "MOE_LAYOUT_SCRATCH_BYTES", "moe_router_logits", "moe_route", "moe_dispatch_layout",
     "moe_dispatch_layout_noalloc", "moe_permute", "moe_quantize_fp8", "moe_dequantize_fp8", "moe_expert_gate_up",
     "moe_expert_gate_up_gathered", "moe_expert_gate_up_gathered_shared", "moe_expert_down",
@@ -27,6 +28,7 @@ __all__ = [
     "moe_grouped_ffn", "moe_combine", "moe_workspace_bytes", "moe_status_str",
     "moe_version", "moe_combine_backward", "moe_expert_gate_up_preact", "moe_swiglu_backward", "moe_expert_dgrad",
     "moe_expert_wgrad", "moe_router_backward", "moe_router_input_grad", "moe_stream_probe",
+    "moe_balance_loss", "moe_balance_loss_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +36,8 @@ _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = range(3)
-MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD = range(5)
+(MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD,
+ MOE_OP_BALANCE_LOSS) = range(6)
 MOE_LAYOUT_SCRATCH_BYTES = 4 << 20   # the fixed count table of moe_dispatch_layout_noalloc
 
 
@@ -80,6 +83,9 @@ _SIGS = {
     "moe_router_backward": [_P, _P, _I, _I, _P, _P, _I, _I, _P, _I, _I, _P, _P, _I, _P],
     "moe_stream_probe": [_P, _SZ, _I, _P, _P],
     "moe_router_input_grad": [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _I, _P],
+    "moe_balance_loss": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _SZ, _P],
+    "moe_balance_loss_backward": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _I,
+                                  _P],
     "moe_status_str": [_I],
     "moe_version": [],
 }
@@ -157,6 +163,18 @@ def _dt(t: torch.Tensor) -> int:
 
 def _torch_dt(dt: int) -> torch.dtype:
     return {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16, MOE_FP8_E4M3: torch.uint8}[dt]
+
+
+def _expect(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
+    """Raises ValueError unless t (if given) has this shape, one of these dtypes and this device."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -565,3 +583,77 @@ def moe_stream_probe(src: torch.Tensor, ratio: int, dst: Optional[torch.Tensor] 
         dst = torch.empty(n16 * 16, dtype=torch.uint8, device=src.device)
     _check("moe_stream_probe", lib().moe_stream_probe(_ptr(src), n16, ratio, _ptr(dst), _stream(src)))
     return dst
+
+
+# ------------------------------------------------------------------------------------------
+# balance loss
+# ------------------------------------------------------------------------------------------
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_ACT = (torch.float32, torch.bfloat16)
+
+
+def _balance_args(z, topk_idx, bias, seq_start, token_mask):
+    """(N, E, k, S) after the checks that the loss and its gradient share."""
+    if z.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("z must be [N, E] and topk_idx [N, k]")
+    N, E = z.shape
+    k = topk_idx.shape[1]
+    S = 1 if seq_start is None else seq_start.numel() - 1
+    _expect("z", z, (N, E), _F32, z.device)
+    _expect("topk_idx", topk_idx, (N, k), _I32, z.device)
+    _expect("bias", bias, (E,), _F32, z.device)
+    _expect("seq_start", seq_start, (S + 1,), _I32, z.device)
+    _expect("token_mask", token_mask, (N,), (torch.uint8, torch.bool), z.device)
+    return N, E, k, S
+
+
+def moe_balance_loss(z: torch.Tensor, topk_idx: torch.Tensor, alpha: float, bias: Optional[torch.Tensor] = None,
+                     seq_start: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                     out=None, ws: Optional[torch.Tensor] = None):
+    """(loss [1] fp32, counts [S, E] int32, prob_mean [S, E] fp32, tokens [S] int32) of a batch's
+    routes: alpha / S * sum over sequences and experts of (E counts / (k tokens)) prob_mean.
+    seq_start [S + 1] int32 cuts the tokens into sequences (None: one); tokens whose token_mask is
+    0 do not count."""
+    N, E, k, S = _balance_args(z, topk_idx, bias, seq_start, token_mask)
+    dev = z.device
+    if out is None:
+        out = (torch.empty(1, dtype=torch.float32, device=dev), torch.empty((S, E), dtype=torch.int32, device=dev),
+               torch.empty((S, E), dtype=torch.float32, device=dev), torch.empty(S, dtype=torch.int32, device=dev))
+    loss, counts, prob_mean, tokens = out
+    _expect("loss", loss, (1,), _F32, dev)
+    _expect("counts", counts, (S, E), _I32, dev)
+    _expect("prob_mean", prob_mean, (S, E), _F32, dev)
+    _expect("tokens", tokens, (S,), _I32, dev)
+    if ws is None:
+        ws = _workspace(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0), dev)
+    with torch.cuda.device(dev):
+        _check("moe_balance_loss", lib().moe_balance_loss(
+            _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(loss),
+            _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws.numel(), _stream(z)))
+    return loss, counts, prob_mean, tokens
+
+
+def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: float, counts: torch.Tensor,
+                              tokens: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                              seq_start: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
+                              d_loss: Optional[torch.Tensor] = None, topk_gate: Optional[torch.Tensor] = None,
+                              d_gate: Optional[torch.Tensor] = None, dz: Optional[torch.Tensor] = None,
+                              dz_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """dz [N, E]: the balance loss's gradient of the logits times d_loss [1] (None: 1), plus the
+    gates' (topk_gate and d_gate [N, k]) on the selected experts."""
+    N, E, k, S = _balance_args(z, topk_idx, bias, seq_start, token_mask)
+    dev = z.device
+    _expect("counts", counts, (S, E), _I32, dev)
+    _expect("tokens", tokens, (S,), _I32, dev)
+    _expect("d_loss", d_loss, (1,), _F32, dev)
+    _expect("topk_gate", topk_gate, (N, k), _F32, dev)
+    _expect("d_gate", d_gate, (N, k), _F32, dev)
+    if dz is None:
+        dz = torch.empty((N, E), dtype=dz_dtype, device=dev)
+    _expect("dz", dz, (N, E), _ACT, dev)
+    with torch.cuda.device(dev):
+        _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
+            _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(counts),
+            _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz), _dt(dz), _stream(z)))
+    return dz

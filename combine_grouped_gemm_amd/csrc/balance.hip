@@ -1,0 +1,459 @@
+// Balance loss of the router, the experts' counts, and the gradient of the logits
+// ("EP / DeepEP explanation" page, section 4: expert loads n_e and their imbalance; "MoE part 4"
+// page, section 4.2: the router's probabilities and top-k).
+//
+//   p_t     = softmax(z_t + bias)                                  over all E experts
+//   c_s[e]  = slots (t, j) of sequence s with topk_idx[t, j] = e,  P_s[e] = mean of p_t[e]
+//   L       = alpha / S * sum_s sum_e (E c_s[e] / (k T_s)) P_s[e]  T_s: counted tokens of s
+//   dz_t[e] = p_t[e] (a_s[e] - sum_j p_t[j] a_s[j]),  a_s[e] = dL alpha (E c_s[e] - k T_s) / (S k T_s^2)
+//             (+ g_j (dg_j - sum_i g_i dg_i) on a token's selected experts)
+// The counts are piecewise constant in z, so only P carries a gradient.  a_s is written about the
+// even load k T_s / E: a constant in a cancels because p sums to one, and the difference of
+// counts is exact, so nearly even loads lose no digits.
+//
+// A token's E logits are held by a group of G lanes, W V per lane (V runs of W consecutive
+// experts, W = 4 where rows keep 16-byte alignment), so each logit is read once per pass and the
+// softmax never leaves registers.  Sums over tokens are taken in a fixed order: a workgroup
+// covers one chunk of C consecutive tokens and writes one partial sum for each sequence that
+// the chunk meets (slot chunk + sequence: along the tokens every step to the next pair raises
+// one of the two, so slots are distinct and at most chunks + S - 1); a second launch adds a
+// sequence's slots.  Counts are integers, added atomically in LDS: their order does not matter.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "moe_common.h"
+#include "moe_launch.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBalThreads = 256;
+constexpr int kBalWaves = kBalThreads / kWave;
+constexpr int kBalMaxChunks = 512;
+constexpr int kBalEx = 16;    // experts of a second-launch workgroup
+constexpr int kBalRows = kBalThreads / kBalEx;
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  return v;
+}
+
+__device__ __forceinline__ int clamp_token(int t, int N) { return t < 0 ? 0 : (t < N ? t : N); }
+
+// the smallest s with seq_start[s + 1] > t (S: none)
+__device__ __forceinline__ int sequence_of(const int32_t* seq_start, int S, int t) {
+  if (seq_start == nullptr) return 0;
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_start[mid + 1] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// The softmax of one token's biased logits: p[v * W + w] is that of expert (v G + l) W + w (0
+// past E).  A row of -inf has no probabilities: all 0.
+template <int G, int V, int W>
+__device__ __forceinline__ void token_softmax(const float* zr, const float* bias, int E, int l, float (&p)[V * W]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v * G + l) * W;
+    if constexpr (W == 4) {
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < E) {
+        q = *reinterpret_cast<const float4*>(zr + e);
+        if (bias != nullptr) {
+          q.x += bias[e]; q.y += bias[e + 1]; q.z += bias[e + 2]; q.w += bias[e + 3];
+        }
+      }
+      p[4 * v] = q.x; p[4 * v + 1] = q.y; p[4 * v + 2] = q.z; p[4 * v + 3] = q.w;
+    } else {
+      p[v] = e < E ? (bias != nullptr ? zr[e] + bias[e] : zr[e]) : -INFINITY;
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, p[v * W + w]);
+  }
+  m = group_max<G>(m);
+  if (m == -INFINITY) m = 0.0f;   // (every exponential is then 0; a NaN logit stays NaN)
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V * W; ++i) {
+    p[i] = expf(p[i] - m);
+    sum += p[i];
+  }
+  sum = group_sum<G>(sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int i = 0; i < V * W; ++i) p[i] *= inv;
+}
+
+struct BalArgs {
+  const float* z;
+  const float* bias;
+  const int32_t* topk_idx;
+  const int32_t* seq_start;
+  const uint8_t* mask;
+  int N, E, k, S, C, chunks;
+  float alpha;
+  float* part_p;       // [chunks + S, E]
+  int32_t* part_c;     // [chunks + S, E]
+  int32_t* part_t;     // [chunks + S]
+  float* part_l;       // [S, ceil(E / kBalEx)]
+  int32_t* ticket;
+  float* loss;
+  int32_t* counts;
+  float* prob_mean;
+  int32_t* tokens;
+};
+
+template <int G, int V, int W>
+__global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(BalArgs a) {
+  constexpr int kGroups = kBalThreads / G;
+  __shared__ float red[kBalWaves * G * V * W];
+  __shared__ int32_t hist[G * V * W];
+  __shared__ int32_t n_tok;
+  const int tid = threadIdx.x, l = tid % G, grp = tid / G, wave = tid / kWave;
+  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;   // (read by the launch after this one)
+  for (int e = tid; e < G * V * W; e += kBalThreads) hist[e] = 0;
+  if (tid == 0) n_tok = 0;
+  const int t0 = blockIdx.x * a.C, t1 = t0 + a.C < a.N ? t0 + a.C : a.N;
+  for (int s = sequence_of(a.seq_start, a.S, t0); s < a.S; ++s) {
+    int lo = t0, hi = t1;
+    if (a.seq_start != nullptr) {
+      const int b = clamp_token(a.seq_start[s], a.N), e = clamp_token(a.seq_start[s + 1], a.N);
+      if (b >= t1) break;
+      lo = b > t0 ? b : t0;
+      hi = e < t1 ? e : t1;
+    }
+    if (lo >= hi) continue;   // (an empty sequence)
+    __syncthreads();          // hist and n_tok are cleared, red has been read
+    float acc[V * W];
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) acc[i] = 0.0f;
+    int mine = 0;
+    for (int t = lo + grp; t < hi; t += kGroups) {
+      if (a.mask != nullptr && a.mask[t] == 0) continue;
+      float p[V * W];
+      token_softmax<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.bias, a.E, l, p);
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) acc[i] += p[i];
+      for (int j = l; j < a.k; j += G) {
+        const int e = a.topk_idx[static_cast<size_t>(t) * a.k + j];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&hist[e], 1);
+      }
+      ++mine;
+    }
+    if (l == 0 && mine > 0) atomicAdd(&n_tok, mine);
+    // a wave's groups, then the waves, each in a fixed order
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) {
+#pragma unroll
+      for (int off = G; off < kWave; off <<= 1) acc[i] += __shfl_xor(acc[i], off, kWave);
+      if (tid % kWave < G) red[wave * (G * V * W) + ((i / W) * G + l) * W + i % W] = acc[i];
+    }
+    __syncthreads();
+    const size_t slot = static_cast<size_t>(blockIdx.x) + s;
+    for (int e = tid; e < a.E; e += kBalThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kBalWaves; ++w) v += red[w * (G * V * W) + e];
+      a.part_p[slot * a.E + e] = v;
+      a.part_c[slot * a.E + e] = hist[e];
+      hist[e] = 0;
+    }
+    if (tid == 0) {
+      a.part_t[slot] = n_tok;
+      n_tok = 0;
+    }
+    if (hi == t1) break;
+  }
+}
+
+__device__ __forceinline__ int block_sum_int(int v, int32_t* red) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kBalWaves; ++w) v += red[w];
+  return v;
+}
+
+// workgroup (experts of block x, sequence y): the chunks' partial sums, then the sequence's
+// share of the loss; the last workgroup to finish adds the shares in their order
+__global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a) {
+  __shared__ float rp[kBalRows][kBalEx];
+  __shared__ int32_t rc[kBalRows][kBalEx];
+  __shared__ int32_t ri[kBalWaves];
+  __shared__ float share[kBalThreads];
+  __shared__ int last;
+  const int tid = threadIdx.x, el = tid % kBalEx, row = tid / kBalEx;
+  const int e = blockIdx.x * kBalEx + el, s = blockIdx.y;
+  int lo = 0, hi = a.N;
+  if (a.seq_start != nullptr) {
+    lo = clamp_token(a.seq_start[s], a.N);
+    hi = clamp_token(a.seq_start[s + 1], a.N);
+  }
+  const int c0 = lo < hi ? lo / a.C : 0, c1 = lo < hi ? (hi - 1) / a.C + 1 : 0;   // its chunks
+  float p = 0.0f;
+  int c = 0, t = 0;
+  for (int i = c0 + row; i < c1; i += kBalRows) {
+    const size_t o = (static_cast<size_t>(i) + s) * a.E + e;
+    if (e < a.E) {
+      p += a.part_p[o];
+      c += a.part_c[o];
+    }
+  }
+  for (int i = c0 + tid; i < c1; i += kBalThreads) t += a.part_t[i + s];
+  const int T = block_sum_int(t, ri);
+  rp[row][el] = p;
+  rc[row][el] = c;
+  __syncthreads();
+  float part = 0.0f;
+  if (row == 0 && e < a.E) {
+    float ps = 0.0f;
+    int cs = 0;
+#pragma unroll
+    for (int r = 0; r < kBalRows; ++r) {
+      ps += rp[r][el];
+      cs += rc[r][el];
+    }
+    const float mean = T > 0 ? ps / static_cast<float>(T) : 0.0f;
+    a.counts[static_cast<size_t>(s) * a.E + e] = cs;
+    a.prob_mean[static_cast<size_t>(s) * a.E + e] = mean;
+    if (T > 0)
+      part = mean * (static_cast<float>(a.E) * static_cast<float>(cs) / (static_cast<float>(a.k) * static_cast<float>(T)));
+  }
+  if (tid == 0 && blockIdx.x == 0) a.tokens[s] = T;
+  if (tid < kWave) {   // (row 0 lies in wave 0: lanes 0 .. kBalEx - 1)
+    part = group_sum<kBalEx>(part);
+    if (tid == 0) {
+      const int id = s * gridDim.x + blockIdx.x;
+      __hip_atomic_store(a.part_l + id, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const int n = static_cast<int>(gridDim.x * gridDim.y);
+      last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  float sum = 0.0f;
+  const int n = static_cast<int>(gridDim.x * gridDim.y);
+  for (int i = tid; i < n; i += kBalThreads)
+    sum += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  share[tid] = sum;
+  __syncthreads();
+  for (int half = kBalThreads / 2; half > 0; half >>= 1) {
+    if (tid < half) share[tid] += share[tid + half];
+    __syncthreads();
+  }
+  if (tid == 0) *a.loss = a.alpha / static_cast<float>(a.S) * share[0];
+}
+
+struct BalBwdArgs {
+  const float* z;
+  const float* bias;
+  const int32_t* topk_idx;
+  const int32_t* seq_start;
+  const uint8_t* mask;
+  const int32_t* counts;
+  const int32_t* tokens;
+  const float* d_loss;
+  const float* gate;
+  const float* d_gate;
+  void* dz;
+  int N, E, k, S;
+  float alpha;
+};
+
+template <int G, int V, int W, bool F32>
+__global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(BalBwdArgs a) {
+  constexpr int kGroups = kBalThreads / G;
+  const int l = threadIdx.x % G;
+  const float scale = a.alpha * (a.d_loss != nullptr ? *a.d_loss : 1.0f) / (static_cast<float>(a.S) * static_cast<float>(a.k));
+  for (long long t = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / G; t < a.N;
+       t += static_cast<long long>(gridDim.x) * kGroups) {
+    float d[V * W];
+#pragma unroll
+    for (int i = 0; i < V * W; ++i) d[i] = 0.0f;
+    // the token's sequence, if it counts
+    bool on = a.mask == nullptr || a.mask[t] != 0;
+    int s = 0;
+    if (a.seq_start != nullptr) {
+      s = sequence_of(a.seq_start, a.S, static_cast<int>(t));
+      on = on && s < a.S && a.seq_start[s < a.S ? s : 0] <= t;
+    }
+    if (on) {
+      float p[V * W], co[V * W];
+      token_softmax<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.bias, a.E, l, p);
+      const float T = static_cast<float>(a.tokens[s]);
+      const float kT = static_cast<float>(a.k) * T, f = T > 0.0f ? scale / (T * T) : 0.0f;
+      float dot = 0.0f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = (v * G + l) * W;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const int c = e < a.E ? a.counts[static_cast<size_t>(s) * a.E + e + w] : 0;
+          co[v * W + w] = e < a.E ? f * fmaf(static_cast<float>(a.E), static_cast<float>(c), -kT) : 0.0f;
+          dot = fmaf(p[v * W + w], co[v * W + w], dot);
+        }
+      }
+      dot = group_sum<G>(dot);
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) d[i] = p[i] * (co[i] - dot);
+    }
+    if (a.gate != nullptr) {
+      const size_t o = static_cast<size_t>(t) * a.k;
+      float sum = 0.0f;
+      for (int j = 0; j < a.k; ++j) sum = fmaf(a.gate[o + j], a.d_gate[o + j], sum);
+      for (int j = 0; j < a.k; ++j) {
+        const int id = a.topk_idx[o + j];
+        const float dj = a.gate[o + j] * (a.d_gate[o + j] - sum);
+#pragma unroll
+        for (int i = 0; i < V * W; ++i)
+          if (((i / W) * G + l) * W + i % W == id) d[i] += dj;
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = (v * G + l) * W;
+      if (e >= a.E) continue;
+      const size_t o = static_cast<size_t>(t) * a.E + e;
+      if constexpr (F32 && W == 4)
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.dz) + o) =
+            make_float4(d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
+      else if constexpr (F32)
+        reinterpret_cast<float*>(a.dz)[o] = d[v];
+      else if constexpr (W == 4)
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.dz) + o) =
+            make_uint2(pack_bf16x2(d[4 * v], d[4 * v + 1]), pack_bf16x2(d[4 * v + 2], d[4 * v + 3]));
+      else
+        reinterpret_cast<uint16_t*>(a.dz)[o] = f32_to_bf16(d[v]);
+    }
+  }
+}
+
+// lanes of a token's group for E experts, W per lane and run: the smallest power of two that
+// holds them, a whole wave (and V runs) beyond 64 W
+int group_lanes(int E, int W) {
+  int g = W == 4 ? 2 : 8;
+  while (g < kWave && g * W < E) g *= 2;
+  return g;
+}
+
+// f<G, V, W>() for E experts
+template <typename F>
+void with_group(int E, bool vec, F&& f) {
+#define MOE_GROUP(G_, V_, W_) f(std::integral_constant<int, G_>{}, std::integral_constant<int, V_>{}, std::integral_constant<int, W_>{})
+  if (vec) {
+    switch (group_lanes(E, 4)) {
+      case 2: return MOE_GROUP(2, 1, 4);
+      case 4: return MOE_GROUP(4, 1, 4);
+      case 8: return MOE_GROUP(8, 1, 4);
+      case 16: return MOE_GROUP(16, 1, 4);
+      case 32: return MOE_GROUP(32, 1, 4);
+    }
+    if (E <= 256) return MOE_GROUP(64, 1, 4);
+    if (E <= 512) return MOE_GROUP(64, 2, 4);
+    return MOE_GROUP(64, 4, 4);
+  }
+  switch (group_lanes(E, 1)) {
+    case 8: return MOE_GROUP(8, 1, 1);
+    case 16: return MOE_GROUP(16, 1, 1);
+    case 32: return MOE_GROUP(32, 1, 1);
+  }
+  if (E <= 64) return MOE_GROUP(64, 1, 1);
+  if (E <= 128) return MOE_GROUP(64, 2, 1);
+  if (E <= 256) return MOE_GROUP(64, 4, 1);
+  if (E <= 512) return MOE_GROUP(64, 8, 1);
+  return MOE_GROUP(64, 16, 1);
+#undef MOE_GROUP
+}
+
+// tokens of a chunk: at most kBalMaxChunks chunks, and a few tokens per group so that a partial
+// sum is worth its write.  The same for either alignment of z (the workspace depends on it).
+int chunk_tokens(int N, int E) {
+  const int pass = kBalThreads / group_lanes(E, E % 4 == 0 ? 4 : 1);   // tokens the workgroup holds at a time
+  const int need = (N + kBalMaxChunks - 1) / kBalMaxChunks;
+  const int passes = (need + pass - 1) / pass;
+  return pass * (passes > 4 ? passes : 4);
+}
+
+struct BalLayout {
+  int C, chunks;
+  size_t p, c, t, l, ticket, total;   // byte offsets in the workspace
+};
+BalLayout balance_layout(int N, int E, int S) {
+  BalLayout b;
+  b.C = chunk_tokens(N, E);
+  b.chunks = (N + b.C - 1) / b.C;
+  const size_t slots = static_cast<size_t>(b.chunks) + S;
+  b.p = 0;
+  b.c = b.p + slots * E * 4;
+  b.t = b.c + slots * E * 4;
+  b.l = b.t + slots * 4;
+  b.ticket = b.l + static_cast<size_t>(S) * ((E + kBalEx - 1) / kBalEx) * 4;
+  b.total = (b.ticket + 4 + 255) & ~static_cast<size_t>(255);
+  return b;
+}
+
+__global__ void balance_clear_kernel(int32_t* ticket) { *ticket = 0; }
+
+}  // namespace
+
+size_t balance_ws_bytes(int N, int E, int S) { return balance_layout(N, E, S).total; }
+
+hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                               const int32_t* seq_start, int S, const uint8_t* mask, float alpha, float* loss,
+                               int32_t* counts, float* prob_mean, int32_t* tokens, void* ws, hipStream_t s) {
+  const BalLayout b = balance_layout(N, E, S);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  BalArgs a = {z, bias, topk_idx, seq_start, mask, N, E, k, S, b.C, b.chunks, alpha,
+               reinterpret_cast<float*>(w + b.p), reinterpret_cast<int32_t*>(w + b.c),
+               reinterpret_cast<int32_t*>(w + b.t), reinterpret_cast<float*>(w + b.l),
+               reinterpret_cast<int32_t*>(w + b.ticket), loss, counts, prob_mean, tokens};
+  const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0;
+  if (b.chunks > 0)
+    with_group(E, vec, [&](auto g, auto v, auto wd) {
+      hipLaunchKernelGGL((balance_partial_kernel<g(), v(), wd()>), dim3(b.chunks), dim3(kBalThreads), 0, s, a);
+    });
+  else
+    hipLaunchKernelGGL(balance_clear_kernel, dim3(1), dim3(1), 0, s, a.ticket);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(balance_total_kernel, dim3((E + kBalEx - 1) / kBalEx, S), dim3(kBalThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                                        const int32_t* seq_start, int S, const uint8_t* mask, float alpha,
+                                        const int32_t* counts, const int32_t* tokens, const float* d_loss,
+                                        const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s) {
+  const BalBwdArgs a = {z, bias, topk_idx, seq_start, mask, counts, tokens, d_loss, gate, d_gate, dz,
+                        N, E, k, S, alpha};
+  const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0 && reinterpret_cast<uintptr_t>(dz) % 16 == 0;
+  with_group(E, vec, [&](auto g, auto v, auto wd) {
+    const int per = kBalThreads / g();
+    const int blocks = (N + per - 1) / per < 4096 ? (N + per - 1) / per : 4096;
+    if (f32)
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), true>), dim3(blocks), dim3(kBalThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), false>), dim3(blocks), dim3(kBalThreads), 0, s, a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

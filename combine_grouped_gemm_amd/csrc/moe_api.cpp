@@ -47,6 +47,16 @@ moe_status check_gemm(const int32_t* offsets, int E, int rows, int H, int I, voi
   return MOE_OK;
 }
 
+// Checks shared by the balance loss and its gradient.
+moe_status check_balance(int N, int E, int k, const int32_t* seq_start, int S) {
+  if (N < 0 || E < 1 || k < 1 || k > E || S < 1) return MOE_ERR_INVALID_ARG;
+  if (seq_start == nullptr && S != 1) return MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || S > 65535) return MOE_ERR_UNSUPPORTED;
+  if ((static_cast<long long>(N) + S) * E >= (1ll << 31) || static_cast<long long>(N) * k >= (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -82,6 +92,9 @@ size_t moe_workspace_bytes(int op, int N, int H, int I, int E, int k, int a_dt) 
     case MOE_OP_ROUTER:
       if (E < 1 || N == 0 || H <= 0) return 0;
       return moe::router_ws_bytes(N, H, E, a_dt == MOE_BF16);
+    case MOE_OP_BALANCE_LOSS:   // (k: the sequences)
+      if (E < 1 || k < 1) return 0;
+      return moe::balance_ws_bytes(N, E, k);
     default:
       return 0;
   }
@@ -481,6 +494,39 @@ moe_status moe_router_backward(const float* topk_gate, const float* d_gate, int 
   if (x != nullptr && !aligned16(x)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_router_backward(topk_gate, d_gate, N, k, offsets, src_slot, E, rows, x,
                                                 x_dt == MOE_F32, H, dz, dw_r, dw_dt == MOE_F32, stream));
+}
+
+// ---- balance loss
+
+moe_status moe_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                            const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha, float* loss,
+                            int32_t* counts, float* prob_mean, int32_t* tokens, void* ws, size_t ws_bytes,
+                            hipStream_t stream) {
+  const moe_status st = check_balance(N, E, k, seq_start, S);
+  if (st != MOE_OK) return st;
+  if (loss == nullptr || counts == nullptr || prob_mean == nullptr || tokens == nullptr) return MOE_ERR_INVALID_ARG;
+  if (N > 0 && (z == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || ws_bytes < moe::balance_ws_bytes(N, E, S)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_balance_loss(z, bias, topk_idx, N, E, k, seq_start, S, token_mask, alpha, loss,
+                                             counts, prob_mean, tokens, ws, stream));
+}
+
+moe_status moe_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                                     const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha,
+                                     const int32_t* counts, const int32_t* tokens, const float* d_loss,
+                                     const float* topk_gate, const float* d_gate, void* dz, moe_dtype dz_dt,
+                                     hipStream_t stream) {
+  const moe_status st = check_balance(N, E, k, seq_start, S);
+  if (st != MOE_OK) return st;
+  if (dz_dt != MOE_F32 && dz_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if ((topk_gate == nullptr) != (d_gate == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (N == 0) return MOE_OK;
+  if (z == nullptr || topk_idx == nullptr || counts == nullptr || tokens == nullptr || dz == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_balance_loss_backward(z, bias, topk_idx, N, E, k, seq_start, S, token_mask, alpha,
+                                                      counts, tokens, d_loss, topk_gate, d_gate, dz,
+                                                      dz_dt == MOE_F32, stream));
 }
 
 }  // extern "C"

@@ -57,6 +57,17 @@ hipError_t launch_expert_wgrad(const void* a, const void* b, const int32_t* b_ro
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int rows, int tile_rows, int cap, int32_t* prefix,
                               int32_t* tile_expert, int32_t* tile_counter, hipStream_t s);
 
+// balance loss, counts and the logits' gradient (balance.hip); mask, bias, seq_start, d_loss and
+// (gate, d_gate) may be null
+size_t balance_ws_bytes(int N, int E, int S);
+hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                               const int32_t* seq_start, int S, const uint8_t* mask, float alpha, float* loss,
+                               int32_t* counts, float* prob_mean, int32_t* tokens, void* ws, hipStream_t s);
+hipError_t launch_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                                        const int32_t* seq_start, int S, const uint8_t* mask, float alpha,
+                                        const int32_t* counts, const int32_t* tokens, const float* d_loss,
+                                        const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s);
+
 size_t gemm_tile_cap(int rows, int E);
 size_t gemm_schedule_bytes(int rows, int E);
 // the fp8 gate/up's bf16 copy of its activations, kept after the schedule (rows x K)

@@ -69,7 +69,8 @@ typedef enum {
   MOE_OP_GROUPED_FFN = 1, /* includes the [rows, I] intermediate h                      */
   MOE_OP_EXPERT_GEMM = 2, /* moe_expert_gate_up / moe_expert_down: tile schedule (fp8 gate/up: and a bf16 copy of a) */
   MOE_OP_ROUTER = 3,      /* moe_router_logits: fp32 partial sums (N, H, E, a_dt = x_dt) */
-  MOE_OP_EXPERT_DGRAD = 4 /* moe_expert_dgrad: tile schedule (N = rows, E)               */
+  MOE_OP_EXPERT_DGRAD = 4, /* moe_expert_dgrad: tile schedule (N = rows, E)              */
+  MOE_OP_BALANCE_LOSS = 5 /* moe_balance_loss: partial sums (N, E, k = S sequences)      */
 } moe_op;
 
 /* Limits of this implementation. */
@@ -491,6 +492,64 @@ moe_status moe_router_input_grad(const void* w_r, moe_dtype w_dt, int N, int E, 
 moe_status moe_router_backward(const float* topk_gate, const float* d_gate, int N, int k, const int32_t* offsets,
                                const int32_t* src_slot, int E, int rows, const void* x, moe_dtype x_dt, int H,
                                float* dz, void* dw_r, moe_dtype dw_dt, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Balance loss of the router (training).
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * moe_balance_loss -- the load-balancing loss of a batch's routes, with the experts' counts.
+ *
+ * Definition: "EP / DeepEP explanation" page, section 4 (the loads n_e and their imbalance);
+ * "MoE part 4" page, section 4.2 (the router's probabilities and top-k).  With p_t the softmax
+ * of token t's E biased logits, and for each of the S sequences s with T_s counted tokens
+ *
+ *     c_s[e] = slots (t, j) of s with topk_idx[t, j] = e,     P_s[e] = mean over s of p_t[e],
+ *     loss   = alpha / S * sum_s sum_e (E c_s[e] / (k T_s)) P_s[e]       (T_s = 0: no share).
+ *
+ *   z          [N, E] fp32 router logits; bias [E] fp32 as given to moe_route, or NULL.
+ *   topk_idx   [N, k] int32; ids outside [0, E) are not counted.
+ *   seq_start  [S + 1] int32, non-decreasing: sequence s holds tokens seq_start[s] ..
+ *              seq_start[s + 1] - 1 (clamped into [0, N]); tokens before the first and behind
+ *              the last sequence do not count.  NULL (S = 1): all N tokens.
+ *   token_mask [N] bytes, or NULL: tokens with 0 (padding) do not count.
+ *   loss       [1] fp32 out; counts [S, E] int32 out (c_s); prob_mean [S, E] fp32 out (P_s; 0
+ *              for a sequence without tokens); tokens [S] int32 out (T_s).
+ *   ws         workspace of moe_workspace_bytes(MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0) bytes.
+ * Sums are fp32 in a fixed order: the same inputs give the same bits.  Logits of -inf have
+ * probability 0, and a token whose logits are all -inf has none; a NaN or +inf logit of a
+ * counted token makes its sequence's P and the loss NaN, one of an uncounted token does nothing.
+ * N == 0 is valid and writes zeros.  Requires k <= min(E, 32), E <= 1024, S <= 65535,
+ * (N + S) E < 2^31 and N k < 2^31.
+ */
+moe_status moe_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                            const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha, float* loss,
+                            int32_t* counts, float* prob_mean, int32_t* tokens, void* ws, size_t ws_bytes,
+                            hipStream_t stream);
+
+/*
+ * moe_balance_loss_backward -- the logits' gradient: the balance loss's, plus the gates'.
+ *
+ * Definition: the chain rule on moe_balance_loss (the counts are piecewise constant, so only
+ * P carries a gradient) and on moe_route's gates:
+ *
+ *     dz_t[e] = p_t[e] (a[e] - sum_j p_t[j] a[j]),    a[e] = d_loss alpha E c_s[e] / (S k T_s^2)
+ *               + sum over the token's slots j with topk_idx[t, j] = e of
+ *                 g_tj (d_gate_tj - sum_i g_ti d_gate_ti)              (with topk_gate, d_gate)
+ *
+ * An uncounted token gets the gates' part only.
+ *   z, bias, topk_idx, seq_start, token_mask, alpha   as given to moe_balance_loss.
+ *   counts, tokens     as moe_balance_loss wrote them.
+ *   d_loss             [1] fp32: the gradient of what is minimised by the loss, or NULL (1).
+ *   topk_gate, d_gate  [N, k] fp32 (moe_route's gates, moe_combine_backward's gradient), or
+ *                      both NULL.
+ *   dz                 [N, E] of dz_dt (MOE_F32 or MOE_BF16) out, every row written.
+ */
+moe_status moe_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
+                                     const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha,
+                                     const int32_t* counts, const int32_t* tokens, const float* d_loss,
+                                     const float* topk_gate, const float* d_gate, void* dz, moe_dtype dz_dt,
+                                     hipStream_t stream);
 
 /*
  * moe_workspace_bytes -- bytes of workspace `op` needs for these sizes (0 if none).

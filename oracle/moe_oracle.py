@@ -31,7 +31,7 @@ __all__ = [
     "dispatch_layout", "permute", "e4m3_decode", "e4m3_encode", "quantize_blocks",
     "dequantize_blocks", "silu", "expert_ffn", "grouped_ffn", "combine", "imbalance", "moe_layer",
     "combine_backward", "dispatch_backward", "swiglu_backward", "expert_ffn_backward", "gates_backward",
-    "router_backward", "moe_layer_backward",
+    "router_backward", "moe_layer_backward", "balance_loss", "balance_loss_backward",
 ]
 
 E4M3_MAX = 448.0  # largest finite OCP e4m3fn value: 1.75 * 2^8
@@ -517,3 +517,69 @@ def moe_layer_backward(x: np.ndarray, z: np.ndarray, k: int, w13: WeightSource, 
         dx = dx + dx_r
     res["dx"] = dx
     return res
+
+
+# --------------------------------------------------------------------------------------
+# balance loss ([EPX] 4: loads and imbalance; [DGG] 4.2: the router's probabilities)
+# --------------------------------------------------------------------------------------
+
+def _sequence_tokens(N: int, seq_start, mask):
+    """The counted tokens of every sequence."""
+    starts = [0, N] if seq_start is None else [min(max(int(b), 0), N) for b in seq_start]
+    on = np.ones(N, bool) if mask is None else np.asarray(mask) != 0
+    return [np.array([t for t in range(lo, hi) if on[t]], dtype=np.int64) for lo, hi in zip(starts, starts[1:])]
+
+
+def _row_softmax(zb: np.ndarray) -> np.ndarray:
+    """Softmax of every row in float64; a row of -inf has no probabilities (all 0)."""
+    zb = np.asarray(zb, np.float64)
+    m = zb.max(axis=1, keepdims=True)
+    ex = np.exp(zb - np.where(np.isneginf(m), 0.0, m))
+    tot = ex.sum(axis=1, keepdims=True)
+    return ex / np.where(tot == 0, 1.0, tot)
+
+
+def balance_loss(z, topk_idx, alpha, bias=None, seq_start=None, mask=None):
+    """(loss, counts [S, E], mean probabilities [S, E], counted tokens [S]):
+    loss = alpha / S sum_s sum_e (E c_s[e] / (k T_s)) P_s[e]; ids outside [0, E) are not counted."""
+    zb = biased_logits(np.asarray(z, np.float32), bias)
+    N, E = zb.shape
+    k = topk_idx.shape[1]
+    toks = _sequence_tokens(N, seq_start, mask)
+    S = len(toks)
+    counts = np.zeros((S, E), np.int64)
+    prob = np.zeros((S, E))
+    loss = 0.0
+    for s, ts in enumerate(toks):
+        if len(ts) == 0:
+            continue
+        for t in ts:
+            for e in topk_idx[t]:
+                if 0 <= e < E:
+                    counts[s, e] += 1
+        prob[s] = _row_softmax(zb[ts]).mean(axis=0)
+        loss += alpha / S * float((E * counts[s] / (k * len(ts)) * prob[s]).sum())
+    return loss, counts, prob, np.array([len(ts) for ts in toks])
+
+
+def balance_loss_backward(z, topk_idx, alpha, bias=None, seq_start=None, mask=None, d_loss=1.0, gates=None, dg=None):
+    """dz [N, E]: p (a - sum p a) with a = d_loss alpha E c / (S k T^2) on counted tokens, plus the
+    gates' gradient (gates_backward) on the selected experts."""
+    zb = biased_logits(np.asarray(z, np.float32), bias)
+    N, E = zb.shape
+    k = topk_idx.shape[1]
+    _, counts, _, T = balance_loss(z, topk_idx, alpha, bias, seq_start, mask)
+    dz = np.zeros((N, E))
+    for s, ts in enumerate(_sequence_tokens(N, seq_start, mask)):
+        if len(ts) == 0:
+            continue
+        a = d_loss * alpha * E * counts[s] / (len(T) * k * float(T[s]) ** 2)
+        p = _row_softmax(zb[ts])
+        dz[ts] = p * (a[None, :] - (p @ a)[:, None])
+    if gates is not None:
+        sel = gates_backward(gates, dg)
+        for t in range(N):
+            for j, e in enumerate(topk_idx[t]):
+                if 0 <= e < E:
+                    dz[t, e] += sel[t, j]
+    return dz
