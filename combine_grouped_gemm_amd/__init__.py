@@ -28,7 +28,8 @@ __all__ = [
     "moe_grouped_ffn", "moe_combine", "moe_workspace_bytes", "moe_status_str",
     "moe_version", "moe_combine_backward", "moe_expert_gate_up_preact", "moe_swiglu_backward", "moe_expert_dgrad",
     "moe_expert_wgrad", "moe_router_backward", "moe_router_input_grad", "moe_stream_probe",
-    "moe_balance_loss", "moe_balance_loss_backward",
+    "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_mxfp8", "moe_dequantize_mxfp8",
+    "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,6 +39,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = range(3)
 (MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD,
  MOE_OP_BALANCE_LOSS) = range(6)
+MOE_MX_BLOCK = 32                    # columns that share a scale of the kept 8-bit rows
 MOE_LAYOUT_SCRATCH_BYTES = 4 << 20   # the fixed count table of moe_dispatch_layout_noalloc
 
 
@@ -86,6 +88,9 @@ _SIGS = {
     "moe_balance_loss": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _SZ, _P],
     "moe_balance_loss_backward": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _I,
                                   _P],
+    "moe_quantize_mxfp8": [_P, _I, ctypes.c_int64, _I, _P, _P, _P],
+    "moe_dequantize_mxfp8": [_P, _P, ctypes.c_int64, _I, _I, _P, ctypes.c_int64, _P, _I, _P],
+    "moe_swiglu_backward_mxfp8": [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P],
     "moe_status_str": [_I],
     "moe_version": [],
 }
@@ -657,3 +662,83 @@ def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: fl
             _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(counts),
             _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz), _dt(dz), _stream(z)))
     return dz
+
+
+# ------------------------------------------------------------------------------------------
+# activations kept in 8 bits
+# ------------------------------------------------------------------------------------------
+
+_CODES = (torch.uint8,)
+
+
+def moe_quantize_mxfp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
+    """(codes uint8 of x's shape, scale bytes uint8 [..., cols / 32]): e4m3 codes, 32 columns to a
+    power-of-two scale that keeps the block's largest value below 448."""
+    cols = x.shape[-1]
+    if x.dtype not in _ACT:
+        raise ValueError(f"x must be float32 or bfloat16, not {x.dtype}")
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty(tuple(x.shape[:-1]) + (cols // MOE_MX_BLOCK,), dtype=torch.uint8, device=x.device)
+    _expect("q", q, x.shape, _CODES, x.device)
+    _expect("scale", scale, tuple(x.shape[:-1]) + (cols // MOE_MX_BLOCK,), _CODES, x.device)
+    with torch.cuda.device(x.device):
+        _check("moe_quantize_mxfp8", lib().moe_quantize_mxfp8(_ptr(x), _dt(x), x.numel() // max(cols, 1), cols, _ptr(q),
+                                                              _ptr(scale), _stream(x)))
+    return q, scale
+
+
+def moe_dequantize_mxfp8(q: torch.Tensor, scale: torch.Tensor, out: Optional[torch.Tensor] = None,
+                         dtype: torch.dtype = torch.bfloat16, send_pos: Optional[torch.Tensor] = None,
+                         k: int = 1) -> torch.Tensor:
+    """The values of moe_quantize_mxfp8's codes (exact in bf16): as they lie, or with send_pos
+    [rows * k] each row's to its k rows of out [send_pos.numel(), cols] (moe_permute's map)."""
+    cols = q.shape[-1]
+    rows = q.numel() // max(cols, 1)
+    dev = q.device
+    _expect("q", q, q.shape, _CODES, dev)
+    _expect("scale", scale, tuple(q.shape[:-1]) + (cols // MOE_MX_BLOCK,), _CODES, dev)
+    _expect("send_pos", send_pos, (rows * k,), (torch.int32,), dev)
+    if out is None:
+        out = torch.empty(q.shape if send_pos is None else (rows * k, cols), dtype=dtype, device=dev)
+    _expect("out", out, q.shape if send_pos is None else (out.shape[0], cols), _ACT, dev)
+    with torch.cuda.device(dev):
+        _check("moe_dequantize_mxfp8", lib().moe_dequantize_mxfp8(
+            _ptr(q), _ptr(scale), rows, cols, k, _ptr(send_pos), out.shape[0] if out.dim() else 0, _ptr(out), _dt(out),
+            _stream(q)))
+    return out
+
+
+def moe_swiglu_backward_mxfp8(au_q: torch.Tensor, au_scale: torch.Tensor, dh: torch.Tensor,
+                              send_pos: Optional[torch.Tensor] = None, topk_gate: Optional[torch.Tensor] = None,
+                              d_au: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                              d_gate: Optional[torch.Tensor] = None):
+    """(d_au [rows, 2I], h [rows, I], d_gate) from kept 8-bit pre-activations and dh = dy W_down of
+    the ungated upstream gradient.  With send_pos (slot -> row) and topk_gate [N, k] the rows' gates
+    enter d_au and h, and d_gate [N, k] is the gates' gradient; without topk_gate d_gate is None
+    unless given."""
+    rows, I = dh.shape
+    dev = dh.device
+    slots = rows if send_pos is None else send_pos.numel()
+    _expect("dh", dh, (rows, I), _ACT, dev)
+    _expect("au_q", au_q, (rows, 2 * I), _CODES, dev)
+    _expect("au_scale", au_scale, (rows, 2 * I // MOE_MX_BLOCK), _CODES, dev)
+    _expect("send_pos", send_pos, (slots,), (torch.int32,), dev)
+    for name, t in (("topk_gate", topk_gate), ("d_gate", d_gate)):
+        if t is not None and t.numel() != slots:
+            raise ValueError(f"{name} must have one value for each of the {slots} slots")
+        _expect(name, t, t.shape if t is not None else (), (torch.float32,), dev)
+    if d_au is None:
+        d_au = torch.empty((rows, 2 * I), dtype=dh.dtype, device=dev)
+    if h is None:
+        h = torch.empty((rows, I), dtype=dh.dtype, device=dev)
+    if d_gate is None and topk_gate is not None:
+        d_gate = torch.empty_like(topk_gate)
+    _expect("d_au", d_au, (rows, 2 * I), (dh.dtype,), dev)
+    _expect("h", h, (rows, I), (dh.dtype,), dev)
+    with torch.cuda.device(dev):
+        _check("moe_swiglu_backward_mxfp8", lib().moe_swiglu_backward_mxfp8(
+            _ptr(au_q), _ptr(au_scale), _ptr(dh), _dt(dh), rows, I, slots, _ptr(send_pos), _ptr(topk_gate), _ptr(d_au),
+            _ptr(h), _ptr(d_gate), _stream(dh)))
+    return d_au, h, d_gate

@@ -529,4 +529,47 @@ moe_status moe_balance_loss_backward(const float* z, const float* bias, const in
                                                       dz_dt == MOE_F32, stream));
 }
 
+// ---- activations kept in 8 bits
+
+moe_status moe_quantize_mxfp8(const void* x, moe_dtype x_dt, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                              hipStream_t stream) {
+  if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+  if (x_dt != MOE_F32 && x_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (cols % MOE_MX_BLOCK != 0 || rows >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || q == nullptr || scale == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_quantize_mx(x, x_dt == MOE_F32, rows, cols, q, scale, stream));
+}
+
+moe_status moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int k,
+                                const int32_t* send_pos, int64_t out_rows, void* out, moe_dtype out_dt,
+                                hipStream_t stream) {
+  if (rows < 0 || cols <= 0 || k < 1) return MOE_ERR_INVALID_ARG;
+  if (out_dt != MOE_F32 && out_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (cols % MOE_MX_BLOCK != 0 || k > MOE_MAX_TOPK || rows >= (1ll << 40)) return MOE_ERR_UNSUPPORTED;
+  if (send_pos == nullptr ? k != 1 : out_rows < 0) return MOE_ERR_INVALID_ARG;
+  if (send_pos != nullptr && rows >= kMaxRowsPerLaunch) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (q == nullptr || scale == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_dequantize_mx(q, scale, rows, cols, k, send_pos, out_rows, out, out_dt == MOE_F32,
+                                              stream));
+}
+
+moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scale, const void* dh, moe_dtype dt,
+                                     int rows, int I, int slots, const int32_t* send_pos, const float* topk_gate,
+                                     void* d_au, void* h, float* d_gate, hipStream_t stream) {
+  if (rows < 0 || I <= 0 || slots < 0) return MOE_ERR_INVALID_ARG;
+  if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (I % MOE_MX_BLOCK != 0 || slots >= kMaxRowsPerLaunch) return MOE_ERR_UNSUPPORTED;
+  if (send_pos == nullptr && slots != rows) return MOE_ERR_INVALID_ARG;
+  if (slots == 0) return MOE_OK;
+  if (rows > 0 && (au_q == nullptr || au_scale == nullptr || dh == nullptr || d_au == nullptr || h == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(au_q) || !aligned16(dh) || !aligned16(d_au) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_swiglu_backward_mx(au_q, au_scale, dh, dt == MOE_F32, rows, I, slots, send_pos,
+                                                   topk_gate, d_au, h, d_gate, stream));
+}
+
 }  // extern "C"

@@ -68,6 +68,15 @@ hipError_t launch_balance_loss_backward(const float* z, const float* bias, const
                                         const int32_t* counts, const int32_t* tokens, const float* d_loss,
                                         const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s);
 
+// activations kept in 8 bits (checkpoint.hip); send_pos, gate and d_gate may be null
+hipError_t launch_quantize_mx(const void* x, bool f32, long long rows, int cols, uint8_t* q, uint8_t* scale,
+                              hipStream_t s);
+hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, long long rows, int cols, int k,
+                                const int32_t* send_pos, long long out_rows, void* out, bool f32, hipStream_t s);
+hipError_t launch_swiglu_backward_mx(const uint8_t* au, const uint8_t* au_scale, const void* dh, bool f32, int rows,
+                                     int I, int slots, const int32_t* send_pos, const float* gate, void* d_au, void* h,
+                                     float* d_gate, hipStream_t s);
+
 size_t gemm_tile_cap(int rows, int E);
 size_t gemm_schedule_bytes(int rows, int E);
 // the fp8 gate/up's bf16 copy of its activations, kept after the schedule (rows x K)

@@ -78,6 +78,7 @@ typedef enum {
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_GROUPS 64
 #define MOE_FP8_BLOCK 128 /* columns per fp32 scale of an fp8 row */
+#define MOE_MX_BLOCK 32   /* columns per power-of-two scale of a kept 8-bit row */
 
 /*
  * moe_router_logits -- z = x W_r^T, the router's logits for every token and expert.
@@ -550,6 +551,66 @@ moe_status moe_balance_loss_backward(const float* z, const float* bias, const in
                                      const int32_t* counts, const int32_t* tokens, const float* d_loss,
                                      const float* topk_gate, const float* d_gate, void* dz, moe_dtype dz_dt,
                                      hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Activations kept in 8 bits between forward and backward (training).
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * moe_quantize_mxfp8 -- 8-bit codes of rows, 32 columns to a power-of-two scale.
+ *
+ * Definition: microscaling formats (OCP MX): e4m3fn codes q and one scale byte b per 32
+ * consecutive columns; the value is q 2^(b - 127).  Here 2^(b - 127) is the smallest power of
+ * two, at least 2^-117, with amax <= 448 2^(b - 127): nothing saturates, and every value is a
+ * normal number of bf16.  Codes round to nearest even (a finite value above 248 2^120 rounds
+ * past the types' range and reads back as an infinity).  A block holding a NaN or an infinity
+ * gets b = 255 and reads back as NaN.
+ *   x     [rows, cols] of x_dt (MOE_F32 or MOE_BF16).
+ *   q     [rows, cols] uint8 out; scale [rows, cols / 32] uint8 out.
+ * Requires cols % 32 == 0 and 16-byte aligned x and q.
+ */
+moe_status moe_quantize_mxfp8(const void* x, moe_dtype x_dt, int64_t rows, int cols, uint8_t* q, uint8_t* scale,
+                              hipStream_t stream);
+
+/*
+ * moe_dequantize_mxfp8 -- the values of moe_quantize_mxfp8's codes, exact in bf16 and fp32.
+ *
+ *   q, scale   [rows, cols], [rows, cols / 32] as moe_quantize_mxfp8 wrote them.
+ *   send_pos   NULL: out [rows, cols] holds the rows as they lie (k must be 1).  Otherwise
+ *              [rows * k] int32: row t's values go to rows send_pos[t*k+j] of out [out_rows,
+ *              cols] (moe_permute's map); positions outside [0, out_rows) are skipped and rows
+ *              that no slot names are left as they are.
+ *   out        of out_dt (MOE_F32 or MOE_BF16); out_rows is ignored when send_pos is NULL.
+ * Requires cols % 32 == 0 and 16-byte aligned q and out.
+ */
+moe_status moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols, int k,
+                                const int32_t* send_pos, int64_t out_rows, void* out, moe_dtype out_dt,
+                                hipStream_t stream);
+
+/*
+ * moe_swiglu_backward_mxfp8 -- SwiGLU's backward from kept 8-bit pre-activations, with the gates.
+ *
+ * Definition: the chain rule on y_t = sum_j g_tj W_down h ("EP / DeepEP explanation" page,
+ * section 2) and h = silu(a) u, for the kept values a, u and dh = dy W_down of the upstream
+ * gradient BEFORE the gates (moe_expert_dgrad on the permuted dy); s the logistic of a:
+ *
+ *     d_gate = <dh, h>      (= <dy, W_down h>: the expert outputs are not needed)
+ *     da = g dh u s (1 + a (1 - s)),  du = g dh a s,  h_out = g h    (dW_down = dy^T h_out)
+ *
+ *   au_q, au_scale  [rows, 2I] codes and [rows, 2I / 32] scales of the gate (columns 0..I-1) and
+ *                   up pre-activations.
+ *   dh              [rows, I] of dt (MOE_F32 or MOE_BF16).
+ *   send_pos        [slots] int32: slot s is row send_pos[s] (from moe_dispatch_layout; no row
+ *                   named twice); a slot outside [0, rows) has no row and gets d_gate 0.  NULL:
+ *                   slot s is row s (slots == rows).
+ *   topk_gate       [slots] fp32, or NULL (1).
+ *   d_au [rows, 2I], h [rows, I] of dt out: rows that no slot names are left as they are.
+ *   d_gate          [slots] fp32 out, or NULL.
+ * Sums are fp32 in a fixed order.  Requires I % 32 == 0; 16-byte aligned au_q, dh, d_au and h.
+ */
+moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scale, const void* dh, moe_dtype dt,
+                                     int rows, int I, int slots, const int32_t* send_pos, const float* topk_gate,
+                                     void* d_au, void* h, float* d_gate, hipStream_t stream);
 
 /*
  * moe_workspace_bytes -- bytes of workspace `op` needs for these sizes (0 if none).

@@ -32,6 +32,7 @@ __all__ = [
     "dequantize_blocks", "silu", "expert_ffn", "grouped_ffn", "combine", "imbalance", "moe_layer",
     "combine_backward", "dispatch_backward", "swiglu_backward", "expert_ffn_backward", "gates_backward",
     "router_backward", "moe_layer_backward", "balance_loss", "balance_loss_backward",
+    "mx_quantize", "mx_dequantize", "kept_swiglu_backward",
 ]
 
 E4M3_MAX = 448.0  # largest finite OCP e4m3fn value: 1.75 * 2^8
@@ -583,3 +584,53 @@ def balance_loss_backward(z, topk_idx, alpha, bias=None, seq_start=None, mask=No
                 if 0 <= e < E:
                     dz[t, e] += sel[t, j]
     return dz
+
+
+# --------------------------------------------------------------------------------------
+# activations kept in 8 bits (OCP microscaling: e4m3 codes, 32 columns to a power-of-two scale)
+# --------------------------------------------------------------------------------------
+
+MX_BLOCK, MX_MIN_EXP, MX_NAN = 32, -117, 255
+
+
+def mx_quantize(x: np.ndarray):
+    """(codes uint8 [R, C], scale bytes uint8 [R, C / 32]): the scale is the smallest power of two
+    2^e, e >= -117, with amax <= 448 2^e; codes are e4m3 of x / 2^e, ties to even.  A block with a
+    NaN or an infinity gets byte 255 (its codes mean nothing: 0 here)."""
+    x = np.asarray(x, np.float64)
+    R, C = x.shape
+    b = x.reshape(R, C // MX_BLOCK, MX_BLOCK)
+    bad = ~np.isfinite(b).all(axis=2)
+    b = np.where(bad[:, :, None], 0.0, b)
+    amax = np.abs(b).max(axis=2)
+    e = np.full(amax.shape, MX_MIN_EXP)
+    for _ in range(300):   # (2^128 / 448 is below 2^120)
+        e = np.where(amax > 448.0 * np.exp2(e.astype(np.float64)), e + 1, e)
+    codes = e4m3_encode(b / np.exp2(e.astype(np.float64))[:, :, None]).reshape(R, C)
+    return codes, np.where(bad, MX_NAN, e + 127).astype(np.uint8)
+
+
+def mx_dequantize(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """The values, in float64 (NaN where the scale byte is 255)."""
+    R, C = codes.shape
+    s = np.where(scales == MX_NAN, np.nan, np.exp2(scales.astype(np.float64) - 127))
+    return (e4m3_decode(codes).reshape(R, C // MX_BLOCK, MX_BLOCK) * s[:, :, None]).reshape(R, C)
+
+
+def kept_swiglu_backward(au: np.ndarray, dh: np.ndarray, send_pos=None, gates=None):
+    """(d_au, g h, d_gate) of y_t = sum_j g_tj W_down (silu(a) u) for dh = dy W_down before the gates:
+    d_gate = <dh, h>; rows that no slot names are 0, slots without a row have d_gate 0."""
+    rows, I = dh.shape
+    pos = np.arange(rows) if send_pos is None else np.asarray(send_pos).reshape(-1)
+    g = np.ones(len(pos)) if gates is None else np.asarray(gates, np.float64).reshape(-1)
+    d_au, hg, dg = np.zeros((rows, 2 * I)), np.zeros((rows, I)), np.zeros(len(pos))
+    for s, r in enumerate(pos):
+        if not 0 <= r < rows:
+            continue
+        a, u = au[r, :I], au[r, I:]
+        da, du = swiglu_backward(a, u, dh[r])
+        d_au[r] = g[s] * np.concatenate([da, du])
+        h = silu(a) * u
+        hg[r] = g[s] * h
+        dg[s] = float(dh[r] @ h)
+    return d_au, hg, dg
