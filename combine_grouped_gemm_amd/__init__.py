@@ -20,7 +20,7 @@ __all__ = [
     "MoEError", "lib", "library_path", "declared_symbols",
     "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3",
     "MOE_OP_DISPATCH_LAYOUT", "MOE_OP_GROUPED_FFN", "MOE_OP_EXPERT_GEMM", "MOE_OP_ROUTER", "MOE_OP_EXPERT_DGRAD",
-    "MOE_OP_BALANCE_LOSS",
+    "MOE_OP_BALANCE_LOSS", "MOE_OP_ROUTER_WGRAD",
     "MOE_LAYOUT_SCRATCH_BYTES", "moe_router_logits", "moe_route", "moe_dispatch_layout",
     "moe_dispatch_layout_noalloc", "moe_permute", "moe_quantize_fp8", "moe_dequantize_fp8", "moe_expert_gate_up",
     "moe_expert_gate_up_gathered", "moe_expert_gate_up_gathered_shared", "moe_expert_down",
@@ -29,7 +29,7 @@ __all__ = [
     "moe_version", "moe_combine_backward", "moe_expert_gate_up_preact", "moe_swiglu_backward", "moe_expert_dgrad",
     "moe_expert_wgrad", "moe_router_backward", "moe_router_input_grad", "moe_stream_probe",
     "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_mxfp8", "moe_dequantize_mxfp8",
-    "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK",
+    "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK", "moe_router_dense_wgrad", "moe_router_dense_dgrad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +38,7 @@ _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = range(3)
 (MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD,
- MOE_OP_BALANCE_LOSS) = range(6)
+ MOE_OP_BALANCE_LOSS, MOE_OP_ROUTER_WGRAD) = range(7)
 MOE_MX_BLOCK = 32                    # columns that share a scale of the kept 8-bit rows
 MOE_LAYOUT_SCRATCH_BYTES = 4 << 20   # the fixed count table of moe_dispatch_layout_noalloc
 
@@ -88,6 +88,8 @@ _SIGS = {
     "moe_balance_loss": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _SZ, _P],
     "moe_balance_loss_backward": [_P, _P, _P, _I, _I, _I, _P, _I, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _I,
                                   _P],
+    "moe_router_dense_wgrad": [_P, _P, _I, _I, _I, _I, _P, _I, _P, _SZ, _P],
+    "moe_router_dense_dgrad": [_P, _P, _I, _I, _I, _I, _P, _P, _P],
     "moe_quantize_mxfp8": [_P, _I, ctypes.c_int64, _I, _P, _P, _P],
     "moe_dequantize_mxfp8": [_P, _P, ctypes.c_int64, _I, _I, _P, ctypes.c_int64, _P, _I, _P],
     "moe_swiglu_backward_mxfp8": [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P],
@@ -662,6 +664,43 @@ def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: fl
             _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(counts),
             _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz), _dt(dz), _stream(z)))
     return dz
+
+
+def moe_router_dense_wgrad(dz: torch.Tensor, x: torch.Tensor, dw: Optional[torch.Tensor] = None,
+                           dw_dtype: torch.dtype = torch.float32, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW_r [E, H] = dz^T x for a dense logit gradient dz [N, E] (of x's dtype)."""
+    N, H = x.shape
+    E = dz.shape[-1]
+    dev = x.device
+    _expect("x", x, (N, H), _ACT, dev)
+    _expect("dz", dz, (N, E), (x.dtype,), dev)
+    if dw is None:
+        dw = torch.empty((E, H), dtype=dw_dtype, device=dev)
+    _expect("dw", dw, (E, H), _ACT, dev)
+    if ws is None:
+        ws = _workspace(moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, _dt(x)), dev)
+    with torch.cuda.device(dev):
+        _check("moe_router_dense_wgrad", lib().moe_router_dense_wgrad(
+            _ptr(dz), _ptr(x), _dt(x), N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws.numel(), _stream(x)))
+    return dw
+
+
+def moe_router_dense_dgrad(dz: torch.Tensor, w_r: torch.Tensor, rest: Optional[torch.Tensor] = None,
+                           dx: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx [N, H] = dz W_r (+ rest) for a dense logit gradient dz [N, E] (of w_r's dtype)."""
+    E, H = w_r.shape
+    N = dz.shape[0]
+    dev = w_r.device
+    _expect("w_r", w_r, (E, H), _ACT, dev)
+    _expect("dz", dz, (N, E), (w_r.dtype,), dev)
+    _expect("rest", rest, (N, H), (w_r.dtype,), dev)
+    if dx is None:
+        dx = torch.empty((N, H), dtype=w_r.dtype, device=dev)
+    _expect("dx", dx, (N, H), (w_r.dtype,), dev)
+    with torch.cuda.device(dev):
+        _check("moe_router_dense_dgrad", lib().moe_router_dense_dgrad(
+            _ptr(dz), _ptr(w_r), _dt(w_r), N, E, H, _ptr(rest), _ptr(dx), _stream(w_r)))
+    return dx
 
 
 # ------------------------------------------------------------------------------------------

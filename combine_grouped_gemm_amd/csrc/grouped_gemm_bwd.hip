@@ -281,27 +281,6 @@ __device__ __forceinline__ int kc_key(int r) { return (r >> 2) & 3; }
 // k-rows of the strided operands: chunk c of k-row r in slot c ^ 4 (r & 3)
 __device__ __forceinline__ int mc_key(int k) { return 4 * (k & 3); }
 
-// A buffer resource over `bytes` bytes from `base` (raw, stride 0): a load whose offset lies
-// past the end returns zeros instead of touching memory.
-__device__ __forceinline__ u32x4_t buffer_window(const void* base, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4_t{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
-}
-
-// 16 bytes per lane from byte `voff` of a buffer window into LDS at lds_base + 16 * lane
-// (zeros for offsets past the window).  Inline assembly, like dma16, so that the compiler
-// adds no wait of its own before later LDS reads; M0 holds the LDS base, one wait state
-// after its write.
-__device__ __forceinline__ void dma16_window(u32x4_t rsrc, uint32_t voff, uint32_t lds_base) {
-  __asm__ volatile(
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %0, %1, 0 offen lds"
-      :
-      : "v"(voff), "s"(rsrc), "s"(lds_base)
-      : "memory", "m0");
-}
-
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4i16 lds_v4i16;
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;

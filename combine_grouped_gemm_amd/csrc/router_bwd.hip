@@ -1,0 +1,478 @@
+// The router's gradients from a dense logit gradient dz [N, E] ("EP / DeepEP explanation" page,
+// section 2: z = x W_r^T; the balance loss reaches every expert's logit, so its dz has no zeros):
+//
+//   wgrad:  dW_r[e, h] = sum_t dz[t, e] x[t, h]
+//   dgrad:  dx[t, h]   = sum_e dz[t, e] W_r[e, h]  (+ rest[t, h])
+//
+// Both are skinny (E up to 1024 beside thousands of tokens and columns): x, rest and dx are the
+// bytes that count, dz and W_r stay in the caches.
+//
+// bf16 operands (fp32 sums) run on v_mfma_f32_32x32x16_bf16 over tiles of TM rows x 128 columns
+// (rows: experts in wgrad, tokens in dgrad), K (tokens; experts) in stages of 32 through a ring of
+// three LDS slots filled by direct-to-LDS loads: while a stage is multiplied, the one after the
+// next loads.  Every stage of an operand is read through a buffer window that ends after its last
+// valid element, so rows past the data load zeros.  Operands whose K index is the slow one (dz and
+// x in wgrad, W_r in dgrad) lie in LDS as in memory and are read transposed.  A wgrad tile row past E
+// and a column past H hold other elements' products and are not stored.  In dgrad the K tail of a
+// row is the next row's values: fragments past E are cleared, as 0 times their W_r row of zeros would
+// keep a NaN.  dz rows that are not multiples of 16 bytes (E % 8 != 0) come through registers.
+//
+// wgrad has few tiles (E / TM x H / 128), so the tokens are cut into S ranges whose fp32 partial
+// sums a second launch adds in order: the result has the same bits on every run.
+//
+// fp32 operands take a plain LDS-tiled kernel with fp32 FMAs.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_device.h"
+#include "grouped_gemm.h"
+#include "moe_common.h"
+#include "moe_launch.h"
+
+namespace moe {
+namespace {
+
+constexpr int kRbThreads = 256;
+constexpr int kRbTN = 128;   // tile columns
+constexpr int kRbKS = 32;    // K per stage
+constexpr int kRbSlots = 3;
+
+struct RbArgs {
+  const void* dz;     // [N, E]
+  const void* b;      // wgrad: x [N, H]; dgrad: W_r [E, H]
+  const void* rest;   // dgrad: [N, H] or null
+  void* out;          // wgrad: partial sums [S, E, H] fp32, or dW_r when S = 1; dgrad: dx
+  int N, E, H;
+  int S, span;        // wgrad: part s covers tokens s span .. (s + 1) span - 1
+  int out_f32;
+};
+
+template <int TM>
+struct RbCfg {
+  static constexpr int kWM = TM / 64, kWN = 4 / kWM;       // waves along rows, columns
+  static constexpr int kMB = 2, kNB = kRbTN / 32 / kWN;    // 32 x 32 blocks of a wave
+  static constexpr int kABytes = TM * kRbKS * 2, kBBytes = kRbTN * kRbKS * 2;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kAOps = kABytes / 4096, kBOps = kBBytes / 4096;   // 1 KB loads per wave
+};
+
+// Swizzle of the strided operands: 16-byte chunk c of K-row r of `pitch` bytes lies in slot c ^
+// key(r), so that the four rows of a transposing read hit distinct banks
+template <int PITCH>
+__device__ __forceinline__ int strided_key(int r) {
+  if constexpr (PITCH >= 256) return 4 * (r & 3);
+  else return 4 * ((r >> 1) & 1);
+}
+// dgrad's dz rows of 64 bytes
+__device__ __forceinline__ int row_key(int r) { return (r >> 2) & 3; }
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
+typedef __attribute__((address_space(3))) u32x4_t lds_vec16;
+
+// Byte offset of the lane's first transposing read of columns col0 .. col0 + 31: lane i of group g
+// (16 lanes) addresses 8 bytes of K-row 8 (g / 2) + i / 4
+template <int PITCH>
+__device__ __forceinline__ uint32_t strided_off(int col0, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const int row = 8 * (g >> 1) + (i >> 2);
+  const int byte = (col0 + 16 * (g & 1) + 4 * (i & 3)) * 2;
+  return static_cast<uint32_t>(row * PITCH + ((((byte >> 4) ^ strided_key<PITCH>(row)) << 4) | (byte & 15)));
+}
+// Lane l: column col0 + l % 32, K-rows 16 s + 8 (l / 32) + 0..7
+template <int PITCH>
+__device__ __forceinline__ uint4 strided_frag(uint32_t addr, int s) {
+  uint2 h[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+    h[r] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(
+                                         static_cast<uintptr_t>(addr + (16 * s + 4 * r) * PITCH))));
+  return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+}
+
+// DGRAD: dx; otherwise wgrad.  DMA: dz rows are multiples of 16 bytes from a 16-byte base.
+template <bool DGRAD, int TM, bool DMA>
+__global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
+  using C = RbCfg<TM>;
+  constexpr int kMB = C::kMB, kNB = C::kNB, kAOps = C::kAOps, kBOps = C::kBOps;
+  constexpr int kOps = (DMA ? kAOps : 0) + kBOps;
+  constexpr int kPitch = kNB * 32 + 4;   // dgrad epilogue: floats of a staged row
+  constexpr int kLds = DGRAD && 4 * 32 * kPitch * 4 > kRbSlots * C::kStage ? 4 * 32 * kPitch * 4 : kRbSlots * C::kStage;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)lds));
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / C::kWN, wn = wave % C::kWN;
+
+  // ---- the tile: each XCD takes a contiguous range (wgrad: part -> row block -> column block,
+  // so a part's dz stays in one L2; dgrad: token block -> column block)
+  const int nT = (p.H + kRbTN - 1) / kRbTN;
+  const int rowsM = DGRAD ? p.N : p.E;
+  const int mT = (rowsM + TM - 1) / TM;
+  const long long total = static_cast<long long>(mT) * nT * (DGRAD ? 1 : p.S);
+  const long long per_xcd = (total + kNumXcd - 1) / kNumXcd;
+  const long long slot = blockIdx.x / kNumXcd;
+  const long long L = blockIdx.x % kNumXcd * per_xcd + slot;
+  if (slot >= per_xcd || L >= total) return;
+  const int n0 = static_cast<int>(L % nT) * kRbTN;
+  const int m0 = static_cast<int>(L / nT % mT) * TM;
+  const int part = static_cast<int>(L / nT / mT);
+  const int k_lo = DGRAD ? 0 : part * p.span;
+  const int k_hi = DGRAD ? p.E : (k_lo + p.span < p.N ? k_lo + p.span : p.N);
+  const int nk = (k_hi - k_lo + kRbKS - 1) / kRbKS;
+  const int mcount = rowsM - m0 < TM ? rowsM - m0 : TM;
+  const int ncols = p.H - n0 < kRbTN ? p.H - n0 : kRbTN;
+  const uint16_t* dz = reinterpret_cast<const uint16_t*>(p.dz);
+  const uint16_t* bm = reinterpret_cast<const uint16_t*>(p.b);
+
+  // ---- loads: op j of a wave fills 1 KB group wave + 4 j of its operand
+  constexpr int kACh = DGRAD ? 4 : TM / 8;       // 16-byte chunks of a dz row in LDS
+  constexpr int kBCh = kRbTN / 8;
+  auto a_row = [&](int j) { return (wave + 4 * j) * (64 / kACh) + lane / kACh; };
+  auto a_key = [&](int r) { return DGRAD ? row_key(r) : strided_key<DGRAD ? 256 : TM * 2>(r); };
+  uint32_t voff_a[kAOps], voff_b[kBOps];
+#pragma unroll
+  for (int j = 0; j < kAOps; ++j)
+    voff_a[j] = static_cast<uint32_t>(a_row(j)) * p.E * 2 + (((lane % kACh) ^ a_key(a_row(j))) << 4);
+#pragma unroll
+  for (int j = 0; j < kBOps; ++j) {
+    const int r = (wave + 4 * j) * (64 / kBCh) + lane / kBCh;
+    voff_b[j] = static_cast<uint32_t>(r) * p.H * 2 + (((lane % kBCh) ^ strided_key<kRbTN * 2>(r)) << 4);
+  }
+  auto load_stage = [&](int ks, int sl) __attribute__((always_inline)) {
+    const int k0 = k_lo + ks * kRbKS;
+    const int left = k_hi - k0 < kRbKS ? k_hi - k0 : kRbKS;
+    const uint32_t base = lds0 + sl * C::kStage;
+    if constexpr (DMA) {
+      const u32x4_t wa =
+          DGRAD ? buffer_window(dz + static_cast<size_t>(m0) * p.E + k0,
+                                (static_cast<uint32_t>(mcount - 1) * p.E + left) * 2)
+                : buffer_window(dz + static_cast<size_t>(k0) * p.E + m0,
+                                (static_cast<uint32_t>(left - 1) * p.E + mcount) * 2);
+#pragma unroll
+      for (int j = 0; j < kAOps; ++j) dma16_window(wa, voff_a[j], base + (wave + 4 * j) * 1024);
+    }
+    const u32x4_t wb = buffer_window(bm + static_cast<size_t>(k0) * p.H + n0,
+                                     (static_cast<uint32_t>(left - 1) * p.H + ncols) * 2);
+#pragma unroll
+    for (int j = 0; j < kBOps; ++j) dma16_window(wb, voff_b[j], base + C::kABytes + (wave + 4 * j) * 1024);
+  };
+  // (rows that are not multiples of 16 bytes) one 16-byte chunk of 8 elements per op, zeros past
+  // the rows and columns of dz
+  auto read_a = [&](int ks, uint4 (&v)[kAOps]) __attribute__((always_inline)) {
+    const int k0 = k_lo + ks * kRbKS;
+#pragma unroll
+    for (int j = 0; j < kAOps; ++j) {
+      const int r = a_row(j), c = (lane % kACh) ^ a_key(r);
+      const int row = DGRAD ? m0 + r : k0 + r, col = (DGRAD ? k0 : m0) + 8 * c;
+      const bool in = row < (DGRAD ? p.N : k_hi);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = in && col + i < p.E ? dz[static_cast<size_t>(row) * p.E + col + i] : 0u;
+      v[j] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+  };
+  auto put_a = [&](int sl, const uint4 (&v)[kAOps]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kAOps; ++j)
+      *reinterpret_cast<uint4*>(lds + sl * C::kStage + (wave + 4 * j) * 1024 + lane * 16) = v[j];
+  };
+
+  // ---- fragment addresses inside a slot
+  uint32_t fo_a[2], fo_b[kNB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (DGRAD) {   // i: K half; row block 32 further is 2 KB further
+      const int r = wm * 64 + (lane & 31);
+      fo_a[i] = static_cast<uint32_t>(r * 64 + (((2 * i + (lane >> 5)) ^ row_key(r)) << 4));
+    } else {                 // i: row block
+      fo_a[i] = strided_off<TM * 2>(wm * 64 + 32 * i, lane);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kNB; ++j) fo_b[j] = C::kABytes + strided_off<kRbTN * 2>((wn * kNB + j) * 32, lane);
+
+  f32x16_t acc[kMB][kNB];
+#pragma unroll
+  for (int i = 0; i < kMB; ++i)
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) acc[i][j] = f32x16_t{};
+
+  uint4 va[kAOps];
+  load_stage(0, 0);
+  if constexpr (!DMA) {
+    read_a(0, va);
+    put_a(0, va);
+  }
+  if (nk > 1) {
+    load_stage(1, 1);
+    if constexpr (!DMA) {
+      read_a(1, va);
+      put_a(1, va);
+    }
+    wait_vmcnt<kOps>();
+  } else {
+    wait_vmcnt<0>();
+  }
+  wait_lgkmcnt_all();
+  block_barrier();
+  int sl = 0, sl2 = 2;   // ring slots of stages ks and ks + 2
+  for (int ks = 0; ks < nk; ++ks) {
+    const bool more = ks + 2 < nk;
+    if (more) {
+      load_stage(ks + 2, sl2);
+      if constexpr (!DMA) read_a(ks + 2, va);
+    }
+    const uint32_t sb = lds0 + sl * C::kStage;
+#pragma unroll
+    for (int s = 0; s < kRbKS / 16; ++s) {
+      uint4 fa[kMB], fb[kNB];
+#pragma unroll
+      for (int i = 0; i < kMB; ++i) {
+        if constexpr (DGRAD) {
+          fa[i] = __builtin_bit_cast(uint4, *reinterpret_cast<lds_vec16*>(static_cast<uintptr_t>(sb + fo_a[s] + i * 2048)));
+          if (ks == nk - 1 && ks * kRbKS + 16 * s + 8 * (lane >> 5) >= p.E) fa[i] = make_uint4(0, 0, 0, 0);
+        } else {
+          fa[i] = strided_frag<TM * 2>(sb + fo_a[i], s);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) fb[j] = strided_frag<kRbTN * 2>(sb + fo_b[j], s);
+#pragma unroll
+      for (int i = 0; i < kMB; ++i)
+#pragma unroll
+        for (int j = 0; j < kNB; ++j)
+          acc[i][j] = DGRAD ? mma_bf16(fb[j], fa[i], acc[i][j]) : mma_bf16(fa[i], fb[j], acc[i][j]);
+    }
+    if (ks + 1 < nk) {
+      if constexpr (!DMA) {
+        if (more) put_a(sl2, va);
+      }
+      wait_lgkmcnt_all();
+      if (more) wait_vmcnt<kOps>();
+      else wait_vmcnt<0>();
+      block_barrier();
+    }
+    sl = sl + 1 == kRbSlots ? 0 : sl + 1;
+    sl2 = sl2 + 1 == kRbSlots ? 0 : sl2 + 1;
+  }
+
+  if constexpr (!DGRAD) {
+    // lane l holds column l % 32 of a block and, in register v, row 8 (v / 4) + 4 (l / 32) + v % 4:
+    // each store writes two rows' 128 bytes
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) {
+        const int n = n0 + (wn * kNB + j) * 32 + (lane & 31);
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int e = m0 + wm * 64 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+          if (e >= p.E || n >= p.H) continue;
+          const size_t o = (static_cast<size_t>(part) * p.E + e) * p.H + n;
+          if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = acc[i][j][v];
+          else reinterpret_cast<uint16_t*>(p.out)[o] = f32_to_bf16(acc[i][j][v]);
+        }
+      }
+  } else {
+    // lane l holds token l % 32 of a block and runs of 4 columns: a wave's 32 rows go through LDS in
+    // fp32, then 8 columns a lane along the rows, rest added, one rounding
+    wait_lgkmcnt_all();
+    block_barrier();   // every wave is past its last fragment reads
+    float* st = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
+    constexpr int kLanes = kNB * 4;   // lanes along a row
+    const uint16_t* rest = reinterpret_cast<const uint16_t*>(p.rest);
+#pragma unroll
+    for (int i = 0; i < kMB; ++i) {
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& a = acc[i][j];
+          *reinterpret_cast<float4*>(st + (lane & 31) * kPitch + j * 32 + 8 * q + 4 * (lane >> 5)) =
+              make_float4(a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]);
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      wait_lgkmcnt_all();
+#pragma unroll
+      for (int t = 0; t < 32 * kLanes / 64; ++t) {
+        const int r = t * (64 / kLanes) + lane / kLanes, c = 8 * (lane % kLanes);
+        const int row = m0 + wm * 64 + i * 32 + r, col = n0 + wn * kNB * 32 + c;
+        if (row >= p.N || col >= p.H) continue;
+        const float4 x = *reinterpret_cast<const float4*>(st + r * kPitch + c);
+        const float4 y = *reinterpret_cast<const float4*>(st + r * kPitch + c + 4);
+        float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const size_t o = static_cast<size_t>(row) * p.H + col;
+        if (rest != nullptr) {
+          const uint4 q = *reinterpret_cast<const uint4*>(rest + o);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            v[2 * k] += __uint_as_float(w[k] << 16);
+            v[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+          }
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + o) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                       pack_bf16x2(v[6], v[7]));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+}
+
+// fp32: 64 rows x 64 columns per workgroup, thread (ty, tx) of 16 x 16 owns rows ty + 16 i and
+// columns tx + 16 j; K in steps of 16 through LDS
+template <bool DGRAD>
+__global__ __launch_bounds__(kRbThreads) void router_grad_f32_kernel(RbArgs p) {
+  __shared__ float as[16][65];
+  __shared__ float bs[16][65];
+  const float* dz = reinterpret_cast<const float*>(p.dz);
+  const float* b = reinterpret_cast<const float*>(p.b);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64, part = blockIdx.z;
+  const int M = DGRAD ? p.N : p.E;
+  const int k_lo = DGRAD ? 0 : part * p.span;
+  const int k_hi = DGRAD ? p.E : (k_lo + p.span < p.N ? k_lo + p.span : p.N);
+  float acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+  for (int k0 = k_lo; k0 < k_hi; k0 += 16) {
+    for (int i = threadIdx.x; i < 64 * 16; i += kRbThreads) {
+      // (the index that is contiguous in memory runs fastest)
+      const int kk = DGRAD ? i & 15 : i >> 6, r = DGRAD ? i >> 4 : i & 63;
+      const int k = k0 + kk, m = m0 + r;
+      as[kk][r] = k < k_hi && m < M ? dz[DGRAD ? static_cast<size_t>(m) * p.E + k : static_cast<size_t>(k) * p.E + m] : 0.0f;
+      const int kb = i >> 6, n = n0 + (i & 63);
+      bs[kb][i & 63] = k0 + kb < k_hi && n < p.H ? b[static_cast<size_t>(k0 + kb) * p.H + n] : 0.0f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int kk = 0; kk < 16; ++kk) {
+      float a[4], c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = as[kk][ty + 16 * i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) c[j] = bs[kk][tx + 16 * j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], c[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = m0 + ty + 16 * i;
+    if (m >= M) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int n = n0 + tx + 16 * j;
+      if (n >= p.H) continue;
+      float v = acc[i][j];
+      const size_t o = (static_cast<size_t>(DGRAD ? 0 : part) * M + m) * p.H + n;
+      if (DGRAD && p.rest != nullptr) v += reinterpret_cast<const float*>(p.rest)[o];
+      if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = v;
+      else reinterpret_cast<uint16_t*>(p.out)[o] = f32_to_bf16(v);
+    }
+  }
+}
+
+// dW_r = part_0 + part_1 + ... in that order (n4 groups of 4; S = 0: zeros)
+__global__ __launch_bounds__(kRbThreads) void router_wgrad_sum_kernel(const float4* __restrict__ part, int S,
+                                                                      long long n4, void* __restrict__ dw, int f32) {
+  const long long step = static_cast<long long>(gridDim.x) * kRbThreads;
+  for (long long i = static_cast<long long>(blockIdx.x) * kRbThreads + threadIdx.x; i < n4; i += step) {
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < S; ++s) {
+      const float4 b = part[s * n4 + i];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    if (f32) reinterpret_cast<float4*>(dw)[i] = a;
+    else reinterpret_cast<uint2*>(dw)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
+int rb_tile_rows(int rows) { return rows > 128 ? 256 : (rows > 64 ? 128 : 64); }
+
+// token ranges of a wgrad: about two workgroups per CU, ranges of whole stages and at least two
+struct RbSplit {
+  int S, span;
+};
+RbSplit rb_split(int N, int H, int E, bool bf16) {
+  const int tm = bf16 ? rb_tile_rows(E) : 64, tn = bf16 ? kRbTN : 64, step = bf16 ? kRbKS : 16;
+  const long long tiles = static_cast<long long>((E + tm - 1) / tm) * ((H + tn - 1) / tn);
+  long long S = tiles >= 512 ? 1 : 512 / tiles;
+  const long long most = (N + 2 * step - 1) / (2 * step);
+  S = S < most ? S : (most > 1 ? most : 1);
+  const int span = static_cast<int>(((N + S - 1) / S + step - 1) / step) * step;
+  return {(N + span - 1) / span, span};
+}
+
+unsigned rb_grid(long long tiles) {
+  return static_cast<unsigned>((tiles + kNumXcd - 1) / kNumXcd * kNumXcd);
+}
+
+template <bool DGRAD, int TM>
+hipError_t rb_launch(const RbArgs& p, bool dma, long long tiles, hipStream_t s) {
+  if (dma) hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, true>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+  else hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, false>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+template <bool DGRAD>
+hipError_t rb_run(const RbArgs& p, hipStream_t s) {
+  const int rows = DGRAD ? p.N : p.E;
+  const int tm = rb_tile_rows(rows);
+  const long long tiles = static_cast<long long>((rows + tm - 1) / tm) * ((p.H + kRbTN - 1) / kRbTN) * (DGRAD ? 1 : p.S);
+  const bool dma = p.E % 8 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0;
+  if (tm == 256) return rb_launch<DGRAD, 256>(p, dma, tiles, s);
+  if (tm == 128) return rb_launch<DGRAD, 128>(p, dma, tiles, s);
+  return rb_launch<DGRAD, 64>(p, dma, tiles, s);
+}
+
+}  // namespace
+
+size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16) {
+  if (N <= 0) return 0;
+  const RbSplit r = rb_split(N, H, E, bf16);
+  return r.S <= 1 ? 0 : (static_cast<size_t>(r.S) * E * H * sizeof(float) + 255) & ~static_cast<size_t>(255);
+}
+
+hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, int N, int E, int H, void* dw,
+                                     bool dw_f32, void* ws, hipStream_t s) {
+  const RbSplit r = N > 0 ? rb_split(N, H, E, bf16) : RbSplit{0, 0};
+  RbArgs p = {dz, x, nullptr, r.S > 1 ? ws : dw, N, E, H, r.S, r.span, r.S > 1 || dw_f32 ? 1 : 0};
+  if (r.S > 0) {
+    hipError_t err = hipSuccess;
+    if (bf16) {
+      err = rb_run<false>(p, s);
+    } else {
+      hipLaunchKernelGGL(router_grad_f32_kernel<false>, dim3((E + 63) / 64, (H + 63) / 64, r.S), dim3(kRbThreads), 0, s, p);
+      err = hipGetLastError();
+    }
+    if (err != hipSuccess || r.S == 1) return err;
+  }
+  const long long n4 = static_cast<long long>(E) * H / 4;
+  const long long blocks = (n4 + kRbThreads - 1) / kRbThreads;
+  hipLaunchKernelGGL(router_wgrad_sum_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)),
+                     dim3(kRbThreads), 0, s, reinterpret_cast<const float4*>(ws), r.S, n4, dw, dw_f32 ? 1 : 0);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_dense_dgrad(const void* dz, const void* w_r, bool bf16, int N, int E, int H, const void* rest,
+                                     void* dx, hipStream_t s) {
+  const RbArgs p = {dz, w_r, rest, dx, N, E, H, 1, 0, bf16 ? 0 : 1};
+  if (bf16) return rb_run<true>(p, s);
+  hipLaunchKernelGGL(router_grad_f32_kernel<true>, dim3((N + 63) / 64, (H + 63) / 64), dim3(kRbThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -70,7 +70,8 @@ typedef enum {
   MOE_OP_EXPERT_GEMM = 2, /* moe_expert_gate_up / moe_expert_down: tile schedule (fp8 gate/up: and a bf16 copy of a) */
   MOE_OP_ROUTER = 3,      /* moe_router_logits: fp32 partial sums (N, H, E, a_dt = x_dt) */
   MOE_OP_EXPERT_DGRAD = 4, /* moe_expert_dgrad: tile schedule (N = rows, E)              */
-  MOE_OP_BALANCE_LOSS = 5 /* moe_balance_loss: partial sums (N, E, k = S sequences)      */
+  MOE_OP_BALANCE_LOSS = 5, /* moe_balance_loss: partial sums (N, E, k = S sequences)     */
+  MOE_OP_ROUTER_WGRAD = 6 /* moe_router_dense_wgrad: fp32 partial sums (N, H, E, a_dt)   */
 } moe_op;
 
 /* Limits of this implementation. */
@@ -551,6 +552,27 @@ moe_status moe_balance_loss_backward(const float* z, const float* bias, const in
                                      const int32_t* counts, const int32_t* tokens, const float* d_loss,
                                      const float* topk_gate, const float* d_gate, void* dz, moe_dtype dz_dt,
                                      hipStream_t stream);
+
+/*
+ * moe_router_dense_wgrad, moe_router_dense_dgrad -- the router's gradients from a logit gradient
+ * that is non-zero on every expert (moe_balance_loss_backward's; moe_router_backward and
+ * moe_router_input_grad serve the k selected logits).
+ *
+ * Definition: "EP / DeepEP explanation" page, section 2 (z = x W_r^T) and the chain rule:
+ *     dw[e, h] = sum_t dz[t, e] x[t, h],     dx[t, h] = sum_e dz[t, e] W_r[e, h] (+ rest[t, h])
+ *
+ *   dz [N, E], x [N, H], w_r [E, H], rest [N, H] or NULL and dx [N, H] of dt (MOE_F32 or
+ *   MOE_BF16); dw [E, H] of dw_dt (MOE_F32 or MOE_BF16).
+ *   ws  (wgrad) workspace of moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, dt) bytes
+ *       (may be 0: then ws may be NULL).
+ * Sums are fp32 in a fixed order, one rounding at the end.  N == 0 writes dw's zeros.  Requires
+ * H % 8 == 0, E <= 1024 and 16-byte aligned x, w_r, rest, dw, dx and ws; dz may start anywhere (rows
+ * of E % 8 == 0 from a 16-byte boundary load fastest).  dx may be rest.
+ */
+moe_status moe_router_dense_wgrad(const void* dz, const void* x, moe_dtype dt, int N, int E, int H, void* dw,
+                                  moe_dtype dw_dt, void* ws, size_t ws_bytes, hipStream_t stream);
+moe_status moe_router_dense_dgrad(const void* dz, const void* w_r, moe_dtype dt, int N, int E, int H, const void* rest,
+                                  void* dx, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Activations kept in 8 bits between forward and backward (training).

@@ -93,3 +93,44 @@ def test_binding_checks_shapes_and_types():
                 dict(topk_gate=torch.zeros(6, 3)), dict(dz=torch.zeros(6, 4, dtype=torch.float16))):
         with pytest.raises(ValueError):
             moe.moe_balance_loss_backward(**{**dict(z=z, topk_idx=idx, alpha=0.1, counts=c, tokens=t), **bad})
+
+
+def test_dense_router_refusals():
+    L = moe.lib()
+    need = moe.moe_workspace_bytes(moe.MOE_OP_ROUTER_WGRAD, 4096, 512, 0, 16, 0, MOE_BF16)
+    assert need > 0 and need % (16 * 512 * 4) == 0
+    assert moe.moe_workspace_bytes(moe.MOE_OP_ROUTER_WGRAD, 1, 512, 0, 16, 0, MOE_BF16) == 0
+
+    def wgrad(**kw):
+        a = dict(dz=FAKE, x=FAKE, dt=MOE_BF16, N=4096, E=16, H=512, dw=FAKE, dw_dt=MOE_F32, ws=FAKE, ws_bytes=need, s=None)
+        a.update(kw)
+        return L.moe_router_dense_wgrad(*a.values())
+
+    def dgrad(**kw):
+        a = dict(dz=FAKE, w=FAKE, dt=MOE_BF16, N=4096, E=16, H=512, rest=FAKE, dx=FAKE, s=None)
+        a.update(kw)
+        return L.moe_router_dense_dgrad(*a.values())
+
+    for f in (wgrad, dgrad):
+        assert f(N=-1) == MOE_ERR_INVALID_ARG and f(E=0) == MOE_ERR_INVALID_ARG and f(H=0) == MOE_ERR_INVALID_ARG
+        assert f(E=1025) == MOE_ERR_UNSUPPORTED and f(H=516) == MOE_ERR_UNSUPPORTED and f(H=1 << 21) == MOE_ERR_UNSUPPORTED
+        assert f(N=1 << 24) == MOE_ERR_UNSUPPORTED and f(dt=MOE_FP8_E4M3) == MOE_ERR_UNSUPPORTED
+        assert f(dz=None) == MOE_ERR_INVALID_ARG
+    assert wgrad(dw_dt=MOE_FP8_E4M3) == MOE_ERR_UNSUPPORTED
+    assert wgrad(ws_bytes=need - 1) == MOE_ERR_WORKSPACE and wgrad(ws=None) == MOE_ERR_WORKSPACE
+    for name in ("x", "dw"):
+        assert wgrad(**{name: None}) == MOE_ERR_INVALID_ARG and wgrad(**{name: FAKE + 8}) == MOE_ERR_INVALID_ARG
+    for name in ("w", "dx"):
+        assert dgrad(**{name: None}) == MOE_ERR_INVALID_ARG and dgrad(**{name: FAKE + 8}) == MOE_ERR_INVALID_ARG
+    assert dgrad(rest=FAKE + 2) == MOE_ERR_INVALID_ARG and wgrad(ws=FAKE + 8) == MOE_ERR_INVALID_ARG
+    assert dgrad(N=0, dz=None) == MOE_OK
+
+
+def test_dense_router_binding_checks():
+    dz, x, w = torch.zeros(6, 4), torch.zeros(6, 8), torch.zeros(4, 8)
+    for bad in (dict(dz=dz[:5]), dict(dz=dz.bfloat16()), dict(x=x.half()), dict(dw=torch.zeros(4, 16))):
+        with pytest.raises(ValueError):
+            moe.moe_router_dense_wgrad(**{**dict(dz=dz, x=x), **bad})
+    for bad in (dict(dz=dz[:, :3]), dict(w_r=w.bfloat16()), dict(rest=x[:5]), dict(dx=x.bfloat16())):
+        with pytest.raises(ValueError):
+            moe.moe_router_dense_dgrad(**{**dict(dz=dz, w_r=w), **bad})
