@@ -29,7 +29,7 @@ __all__ = [
     "moe_version", "moe_combine_backward", "moe_expert_gate_up_preact", "moe_swiglu_backward", "moe_expert_dgrad",
     "moe_expert_wgrad", "moe_router_backward", "moe_router_input_grad", "moe_stream_probe",
     "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_mxfp8", "moe_dequantize_mxfp8",
-    "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK", "moe_router_dense_wgrad", "moe_router_dense_dgrad",
+    "moe_expert_gate_up_mxfp8", "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK", "moe_router_dense_wgrad", "moe_router_dense_dgrad",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -92,6 +92,7 @@ _SIGS = {
     "moe_router_dense_dgrad": [_P, _P, _I, _I, _I, _I, _P, _P, _P],
     "moe_quantize_mxfp8": [_P, _I, ctypes.c_int64, _I, _P, _P, _P],
     "moe_dequantize_mxfp8": [_P, _P, ctypes.c_int64, _I, _I, _P, ctypes.c_int64, _P, _I, _P],
+    "moe_expert_gate_up_mxfp8": [_P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "moe_swiglu_backward_mxfp8": [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P],
     "moe_status_str": [_I],
     "moe_version": [],
@@ -747,6 +748,47 @@ def moe_dequantize_mxfp8(q: torch.Tensor, scale: torch.Tensor, out: Optional[tor
             _ptr(q), _ptr(scale), rows, cols, k, _ptr(send_pos), out.shape[0] if out.dim() else 0, _ptr(out), _dt(out),
             _stream(q)))
     return out
+
+
+def moe_expert_gate_up_mxfp8(x: torch.Tensor, src_slot: torch.Tensor, k: int, offsets: torch.Tensor, w13: torch.Tensor,
+                             shared_w13: Optional[torch.Tensor] = None, rows: Optional[int] = None,
+                             h: Optional[torch.Tensor] = None, au_q: Optional[torch.Tensor] = None,
+                             au_scale: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """(h [rows (+ N), I], au_q [rows (+ N), 2I], au_scale): moe_expert_gate_up_gathered_shared (without
+    shared_w13: the routed rows only) that keeps the pre-activations as moe_quantize_mxfp8's codes."""
+    N, H = x.shape
+    E, I2, _ = w13.shape
+    I = I2 // 2
+    dev = x.device
+    if rows is None:
+        rows = src_slot.numel()
+    total = rows + (N if shared_w13 is not None else 0)
+    bf = (torch.bfloat16,)
+    _expect("x", x, (N, H), bf, dev)
+    _expect("w13", w13, (E, 2 * I, H), bf, dev)
+    _expect("offsets", offsets, (E + 1,), _I32, dev)
+    _expect("src_slot", src_slot, src_slot.shape, _I32, dev)
+    if src_slot.numel() < rows:
+        raise ValueError(f"src_slot must name {rows} rows")
+    if shared_w13 is not None:
+        _expect("shared_w13", shared_w13.reshape(-1, H), (2 * I, H), bf, dev)
+    if h is None:
+        h = torch.empty((total, I), dtype=torch.bfloat16, device=dev)
+    if au_q is None:
+        au_q = torch.empty((total, 2 * I), dtype=torch.uint8, device=dev)
+    if au_scale is None:
+        au_scale = torch.empty((total, 2 * I // MOE_MX_BLOCK), dtype=torch.uint8, device=dev)
+    _expect("h", h, (total, I), bf, dev)
+    _expect("au_q", au_q, (total, 2 * I), _CODES, dev)
+    _expect("au_scale", au_scale, (total, 2 * I // MOE_MX_BLOCK), _CODES, dev)
+    if ws is None:
+        n_seg = E + (1 if shared_w13 is not None else 0)
+        ws = _workspace(moe_workspace_bytes(MOE_OP_EXPERT_GEMM, total, H, I, n_seg, 1, MOE_BF16), dev)
+    with torch.cuda.device(dev):
+        _check("moe_expert_gate_up_mxfp8", lib().moe_expert_gate_up_mxfp8(
+            _ptr(x), _dt(x), N, _ptr(src_slot), k, _ptr(offsets), E, rows, H, I, _ptr(w13), _ptr(shared_w13), _ptr(h),
+            _ptr(au_q), _ptr(au_scale), _ptr(ws), ws.numel(), _stream(x)))
+    return h, au_q, au_scale
 
 
 def moe_swiglu_backward_mxfp8(au_q: torch.Tensor, au_scale: torch.Tensor, dh: torch.Tensor,

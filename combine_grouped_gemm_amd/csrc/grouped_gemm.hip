@@ -750,6 +750,11 @@ bool grouped_gemm_shared_supported(int mode, int K, int I, int n_out, long long 
          (gathered ? static_cast<long long>(a_nrows) : kWideTileRows) * rbytes < (1LL << 32);
 }
 
+bool grouped_gemm_keep_supported(int K, int I, int rows, int n_seg, int a_nrows) {
+  return grouped_gemm_shared_supported(MODE_GATE_UP, K, I, I, 2ll * I, a_nrows, true) &&
+         wide_tiles_fit(MODE_GATE_UP, rows, n_seg, I, I);
+}
+
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int rows, int tile_rows, int cap, int32_t* prefix,
                               int32_t* tile_expert, int32_t* tile_counter, hipStream_t s) {
   hipLaunchKernelGGL(build_tiles_kernel, dim3(1), dim3(1024), 0, s, offsets, E, rows, tile_rows, cap, prefix,
@@ -808,7 +813,7 @@ hipError_t launch_grouped_gemm(int ct, bool b8, int mode, const void* a, const f
                                long long b_rows, void* sched, hipStream_t s, const int32_t* a_rows,
                                int a_div, int a_nrows, const void* shared_b, int shared_rows,
                                const int32_t* row_slot, const float* row_gate, void* au,
-                               const float* shared_b_scale) {
+                               const float* shared_b_scale, uint8_t* au_scale) {
   // with a shared segment the schedule covers E + 1 segments and rows + shared_rows rows
   const int n_seg = E + (shared_rows > 0 ? 1 : 0);
   int32_t* prefix = reinterpret_cast<int32_t*>(sched);
@@ -893,6 +898,7 @@ hipError_t launch_grouped_gemm(int ct, bool b8, int mode, const void* a, const f
   p.k_split = 1;
   p.au = au;
   p.shared_b_scale = shared_b_scale;
+  p.au_scale = au_scale;
   if (stream) return launch_grouped_gemm_stream(mode, p, s);
   if (wide || wide8) {
     p.tile_counter = tile_counter;

@@ -52,6 +52,7 @@
 #include "gemm_device.h"
 #include "grouped_gemm.h"
 #include "moe_common.h"
+#include "mxfp8.h"
 
 namespace moe {
 namespace {
@@ -114,6 +115,9 @@ __device__ __forceinline__ void store16(buf_rsrc_t w, uint32_t off, uint4 v) {
   typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
   __builtin_amdgcn_raw_buffer_store_b128(u32x4v{v.x, v.y, v.z, v.w}, w, static_cast<int>(off), 0, 0);
 }
+__device__ __forceinline__ void store1(buf_rsrc_t w, uint32_t off, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(v), w, static_cast<int>(off), 0, 0);
+}
 
 // Lanes l and l + 32 hold the same output row: lane l < 32 columns 8 q .. 8 q + 3 of register
 // group q, lane l + 32 columns 8 q + 4 .. 8 q + 7.  Exchanging group 2 u + 1 of lane l with
@@ -125,6 +129,36 @@ __device__ __forceinline__ uint4 lane_pair(uint2 lo, uint2 hi) {
   const u32x2_t a = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
   const u32x2_t b = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
   return make_uint4(a[0], b[0], a[1], b[1]);
+}
+// The 8-bit codes (mxfp8.h) of one 32-column block of an output row, whose 16 values in lane l are
+// columns 8 q + 0..3 (l < 32) or 8 q + 4..7 in register group q, and the other 16 in lane l ^ 32:
+// of the values rounded to bf16, as the quantizer of bf16 rows would read them.  Returns 16 codes
+// in column order, columns 0..15 in lane l < 32 and 16..31 in lane l + 32; byte: the block's scale.
+// Every lane must take part.
+__device__ __forceinline__ uint4 block_codes(const f32x16_t& v, uint32_t& byte) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  uint32_t w[8], m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    const uint32_t lo = (w[i] << 16) & 0x7FFFFFFFu, hi = w[i] & 0x7FFF0000u;
+    m = m > lo ? m : lo;
+    m = m > hi ? m : hi;
+  }
+  const u32x2_t mm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  byte = mx_scale_byte(mm[0] > mm[1] ? mm[0] : mm[1]);
+  const float inv = mx_inverse(byte);
+  uint32_t c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    c[q] = mx_encode4(__uint_as_float(w[2 * q] << 16), __uint_as_float(w[2 * q] & 0xFFFF0000u),
+                      __uint_as_float(w[2 * q + 1] << 16), __uint_as_float(w[2 * q + 1] & 0xFFFF0000u), inv);
+  // (each swap exchanges its second operand in lanes l < 32 with its first in lanes l + 32)
+  const u32x2_t a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);   // columns 0..7 | 8..15
+  const u32x2_t b = __builtin_amdgcn_permlane32_swap(c[2], c[3], false, false);   // 16..23 | 24..31
+  const u32x2_t x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const u32x2_t y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return make_uint4(x[0], y[0], x[1], y[1]);
 }
 // (W8) 64-byte weight rows: chunk c of row r sits in slot c ^ key4(r); a fragment read (32 rows,
 // 8 bytes of one chunk per lane) then spreads over 16 of the 32 eight-byte bank pairs
@@ -139,7 +173,8 @@ __device__ __forceinline__ void static_for(F&& f) {
 
 // The tiles of one shape, from the XCD's counter: G = 0 the schedule's m-tiles (routed, then
 // the shared segment's), G = 1 one tile per listed expert.  lds is the kernel's LDS array.
-template <int MODE, bool W8, int G>
+// KEEP (gate/up): also the pre-activations' 8-bit codes and scales.
+template <int MODE, bool W8, int G, bool KEEP = false>
 __device__ __forceinline__ void run_tiles(const GemmArgs& p, uint8_t* lds) {
   using S = Geo<G, W8>;
   constexpr int kTM = S::TM, kTN = S::TN, kMB = S::MB, kNB = S::NB;
@@ -814,7 +849,7 @@ __device__ __forceinline__ void run_tiles(const GemmArgs& p, uint8_t* lds) {
     // writes nothing), so the next tile's set-up and first loads are issued before them and
     // its wait for stage 0 leaves exactly these stores in flight
     constexpr bool kEarly = MODE != MODE_ROUTER;
-    constexpr int kStores = MODE == MODE_GATE_UP ? kMB * (kNB / 2) * 2 : kMB * kNB * 2;
+    constexpr int kStores = MODE == MODE_GATE_UP ? kMB * (kNB / 2) * (KEEP ? 6 : 2) : kMB * kNB * 2;
     if (kEarly && more) {
       setup(Ln, cur);
       prologue_loads(cur);
@@ -862,7 +897,7 @@ __device__ __forceinline__ void run_tiles(const GemmArgs& p, uint8_t* lds) {
               }
               store16(out_w, in ? static_cast<uint32_t>(ri) * orow + static_cast<uint32_t>(col) * 2 : kNoWrite,
                       lane_pair(hq[0], hq[1]));   // (every lane: the exchange reads both halves)
-              if (p.au != nullptr) {   // the pre-activations, for the backward pass
+              if (!KEEP && p.au != nullptr) {   // the pre-activations, for the backward pass
                 const uint32_t arow = static_cast<uint32_t>(p.I) * 4;
                 const buf_rsrc_t au_w =
                     make_window(reinterpret_cast<uint8_t*>(p.au) + static_cast<size_t>(em0) * arow, nrow * arow);
@@ -890,13 +925,34 @@ __device__ __forceinline__ void run_tiles(const GemmArgs& p, uint8_t* lds) {
             }
           }
         }
+        if constexpr (KEEP) {   // a lane's 16 codes per gate and up block, a scale byte from lanes < 32
+          const uint32_t qrow = static_cast<uint32_t>(p.I) * 2, srow = qrow / 32;
+          const buf_rsrc_t q_w =
+              make_window(reinterpret_cast<uint8_t*>(p.au) + static_cast<size_t>(em0) * qrow, nrow * qrow);
+          const buf_rsrc_t s_w = make_window(p.au_scale + static_cast<size_t>(em0) * srow, nrow * srow);
+#pragma unroll
+          for (int nb = 0; nb < kNB / 2; ++nb) {
+            const int ri = row_in(mb, nb);
+            const int col = ec0 + (lay1 ? wave * 32 : wn * (kNB / 2) * 32 + nb * 32);
+            const bool in = ri < static_cast<int>(nrow) && col < n_cols;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t c0 = static_cast<uint32_t>(col + half * p.I);
+              uint32_t byte;
+              const uint4 codes = block_codes(acc[mb][nb + half * (kNB / 2)], byte);
+              store16(q_w, in ? static_cast<uint32_t>(ri) * qrow + c0 + 16 * ehk : kNoWrite, codes);
+              store1(s_w, in && ehk == 0 ? static_cast<uint32_t>(ri) * srow + c0 / 32 : kNoWrite, byte);
+            }
+          }
+        }
       }
     }
     if (!more) break;
     if constexpr (kEarly) {
       // stage 0 of the next tile has landed once at most its later stages' loads and this
       // tile's stores (issued after them) remain: the stores drain under the next K loop
-      prologue_wait.template operator()<kStores>();
+      // (the count has 6 bits: beyond 40 stores some of them are waited for too)
+      prologue_wait.template operator()<(kStores < 40 ? kStores : 40)>();
     } else {
       setup(Ln, cur);
       prologue_loads(cur);
@@ -912,26 +968,28 @@ __device__ __forceinline__ void run_tiles(const GemmArgs& p, uint8_t* lds) {
 // one 320 x 256 gate/up tile or 320 x 128 down tile per expert and n-block), then the 256 x 256
 // tiles.  A workgroup that runs out of the first shape's tiles moves on to the second's without
 // waiting for the others.
-template <int MODE, bool W8>
+template <int MODE, bool W8, bool KEEP = false>
 __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_wide_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLdsBytes<W8>];
   if constexpr (MODE == MODE_DOWN) {
     if (p.tall_list != nullptr) run_tiles<MODE, W8, 1>(p, lds);
   }
   if constexpr (MODE == MODE_GATE_UP && !W8) {
-    if (p.tall_list != nullptr) run_tiles<MODE, W8, 2>(p, lds);
+    if (p.tall_list != nullptr) run_tiles<MODE, W8, 2, KEEP>(p, lds);
   }
-  run_tiles<MODE, W8, 0>(p, lds);
+  run_tiles<MODE, W8, 0, KEEP>(p, lds);
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm_wide(int mode, const GemmArgs& p, hipStream_t s, bool w8) {
   const dim3 grid(256), block(kThreads);   // persistent: one workgroup per CU, a multiple of the 8 XCDs
-  if (w8 && mode == MODE_ROUTER) return hipErrorNotSupported;
+  if (w8 && (mode == MODE_ROUTER || p.au_scale != nullptr)) return hipErrorNotSupported;
   if (((w8 && mode != MODE_DOWN) || mode == MODE_ROUTER) && p.tall_list != nullptr) return hipErrorNotSupported;
   if (mode == MODE_GATE_UP && w8)
     hipLaunchKernelGGL((grouped_gemm_wide_kernel<MODE_GATE_UP, true>), grid, block, 0, s, p);
+  else if (mode == MODE_GATE_UP && p.au_scale != nullptr)
+    hipLaunchKernelGGL((grouped_gemm_wide_kernel<MODE_GATE_UP, false, true>), grid, block, 0, s, p);
   else if (mode == MODE_GATE_UP)
     hipLaunchKernelGGL((grouped_gemm_wide_kernel<MODE_GATE_UP, false>), grid, block, 0, s, p);
   else if (mode == MODE_DOWN && w8)

@@ -591,6 +591,30 @@ moe_status moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* scale, int64_t 
                                               stream));
 }
 
+moe_status moe_expert_gate_up_mxfp8(const void* x, moe_dtype x_dt, int N, const int32_t* src_slot, int k,
+                                    const int32_t* offsets, int E, int rows, int H, int I, const void* w13,
+                                    const void* shared_w13, void* h, uint8_t* au_q, uint8_t* au_scale, void* ws,
+                                    size_t ws_bytes, hipStream_t stream) {
+  if (x_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (E < 1 || rows < 0 || N < 0 || H <= 0 || I <= 0 || offsets == nullptr) return MOE_ERR_INVALID_ARG;
+  if (k < 1 || k > MOE_MAX_TOPK) return MOE_ERR_INVALID_ARG;
+  if (E >= MOE_MAX_EXPERTS || H % 128 != 0 || I % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  const int n_shared = shared_w13 != nullptr ? N : 0, n_seg = E + (n_shared > 0 ? 1 : 0);
+  if (static_cast<long long>(rows) + n_shared >= (1LL << 31)) return MOE_ERR_UNSUPPORTED;
+  if (rows + n_shared == 0) return MOE_OK;
+  if (!moe::grouped_gemm_keep_supported(H, I, rows + n_shared, n_seg, N)) return MOE_ERR_UNSUPPORTED;
+  if (ws == nullptr || ws_bytes < moe::gemm_schedule_bytes(rows + n_shared, n_seg)) return MOE_ERR_WORKSPACE;
+  if (x == nullptr || N == 0 || h == nullptr || au_q == nullptr || au_scale == nullptr ||
+      (rows > 0 && (w13 == nullptr || src_slot == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(h) || !aligned16(au_q) || (w13 != nullptr && !aligned16(w13)) ||
+      (shared_w13 != nullptr && !aligned16(shared_w13)))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_grouped_gemm(1, false, 0, x, nullptr, w13, nullptr, h, false, offsets, E, rows, H, I, I,
+                                             2ll * I, ws, stream, src_slot, k, N, shared_w13, n_shared, nullptr,
+                                             nullptr, au_q, nullptr, au_scale));
+}
+
 moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scale, const void* dh, moe_dtype dt,
                                      int rows, int I, int slots, const int32_t* send_pos, const float* topk_gate,
                                      void* d_au, void* h, float* d_gate, hipStream_t stream) {

@@ -610,6 +610,27 @@ moe_status moe_dequantize_mxfp8(const uint8_t* q, const uint8_t* scale, int64_t 
                                 hipStream_t stream);
 
 /*
+ * moe_expert_gate_up_mxfp8 -- the gathered gate/up GEMM that keeps its pre-activations in 8 bits.
+ *
+ * Definition: moe_expert_gate_up_gathered_shared, with the pre-activations au = x [W_gate; W_up]^T
+ * written as moe_quantize_mxfp8's codes of their bf16 values, in the same launch: bit for bit
+ * what that call's au and the quantizer give, without the bf16 rows.
+ *   x ... w13, ws      as for moe_expert_gate_up_gathered_shared.
+ *   shared_w13         [2I, H] bf16: the shared expert's weights, its N rows last; or NULL: the
+ *                      routed rows only.
+ *   h                  [rows (+ N), I] bf16 out.
+ *   au_q, au_scale     [rows (+ N), 2I] uint8 and [rows (+ N), 2I / 32] uint8 out (rows from
+ *                      offsets[E] to rows are left as they are).
+ *   ws                 moe_workspace_bytes(MOE_OP_EXPERT_GEMM, rows (+ N), H, I, E (+ 1), 1,
+ *                      MOE_BF16) bytes.
+ * Requires H % 128 == 0 and I % 128 == 0, E < 1024.
+ */
+moe_status moe_expert_gate_up_mxfp8(const void* x, moe_dtype x_dt, int N, const int32_t* src_slot, int k,
+                                    const int32_t* offsets, int E, int rows, int H, int I, const void* w13,
+                                    const void* shared_w13, void* h, uint8_t* au_q, uint8_t* au_scale, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+
+/*
  * moe_swiglu_backward_mxfp8 -- SwiGLU's backward from kept 8-bit pre-activations, with the gates.
  *
  * Definition: the chain rule on y_t = sum_j g_tj W_down h ("EP / DeepEP explanation" page,

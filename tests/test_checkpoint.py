@@ -136,3 +136,32 @@ def test_binding_checks_shapes_and_types():
                 dict(send_pos=torch.zeros(4, dtype=torch.int64)), dict(d_gate=torch.zeros(4, dtype=torch.float64))):
         with pytest.raises(ValueError):
             moe.moe_swiglu_backward_mxfp8(**{**dict(au_q=q, au_scale=s, dh=dh), **bad})
+
+
+def test_gate_up_refusals():
+    L = moe.lib()
+    ws = moe.moe_workspace_bytes(moe.MOE_OP_EXPERT_GEMM, 80 + 40, 256, 128, 9, 1, MOE_BF16)
+
+    def f(**kw):
+        a = dict(x=FAKE, dt=MOE_BF16, N=40, ss=FAKE, k=2, off=FAKE, E=8, rows=80, H=256, I=128, w13=FAKE, sw=FAKE, h=FAKE,
+                 q=FAKE, scale=FAKE, ws=FAKE, ws_bytes=ws, s=None)
+        a.update(kw)
+        return L.moe_expert_gate_up_mxfp8(*a.values())
+
+    assert f(dt=MOE_F32) == MOE_ERR_UNSUPPORTED and f(E=1024) == MOE_ERR_UNSUPPORTED
+    assert f(H=200) == MOE_ERR_UNSUPPORTED and f(I=96) == MOE_ERR_UNSUPPORTED
+    assert f(E=0) == MOE_ERR_INVALID_ARG and f(rows=-1) == MOE_ERR_INVALID_ARG and f(k=0) == MOE_ERR_INVALID_ARG
+    assert f(N=0) == MOE_ERR_INVALID_ARG and f(off=None) == MOE_ERR_INVALID_ARG
+    for name in ("x", "ss", "w13", "h", "q", "scale"):
+        assert f(**{name: None}) == MOE_ERR_INVALID_ARG
+    for name in ("x", "w13", "sw", "h", "q"):
+        assert f(**{name: FAKE + 8}) == MOE_ERR_INVALID_ARG
+    assert f(ws_bytes=ws - 1) == moe.MOE_ERR_WORKSPACE and f(ws=None) == moe.MOE_ERR_WORKSPACE
+    assert f(N=0, rows=0, x=None, h=None) == MOE_OK
+    x, ss, off = torch.zeros(4, 128, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    w = torch.zeros(2, 256, 128, dtype=torch.bfloat16)
+    for bad in (dict(x=x.float()), dict(w13=w.float()), dict(offsets=off[:2]), dict(src_slot=ss.long()), dict(rows=9),
+                dict(shared_w13=w), dict(h=torch.zeros(8, 64, dtype=torch.bfloat16)),
+                dict(au_scale=torch.zeros(8, 4, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            moe.moe_expert_gate_up_mxfp8(**{**dict(x=x, src_slot=ss, k=2, offsets=off, w13=w), **bad})

@@ -214,3 +214,59 @@ def test_captured_and_on_another_stream():
         sync()
         for x, y in ((q, q2), (s, s2), (v, v2), (d_au, d2), (h, h2)):
             assert torch.equal(x, y)
+
+
+def _gate_up_inputs(N, H, E, k, I, seed, hot=False):
+    rng = np.random.default_rng(seed)
+    idx = np.argsort(rng.random((N, E)), axis=1)[:, :k]
+    if hot:   # one expert with every token, one with none
+        idx = np.where(idx == E - 1, 1, idx)
+        idx[:, 0] = 0
+        for t in range(N):
+            if len(set(idx[t])) < k:
+                idx[t] = [0] + [e for e in rng.permutation(E) if e not in (0, E - 1)][:k - 1]
+    n_e, off, sp, ss = oracle.dispatch_layout(idx.astype(np.int32), E)
+    t = lambda *s: torch.from_numpy(rng.normal(size=s)).to(torch.bfloat16).to(DEV)  # noqa: E731
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a).astype(np.int32)).to(DEV)  # noqa: E731
+    std = H ** -0.5
+    return t(N, H), t(E, 2 * I, H) * std, t(1, 2 * I, H) * std, dev(off), dev(ss), n_e
+
+
+# tiles of every shape: one row, 1 x 4 and 2 x 2 layouts, experts of 257..320 rows (320-row tiles), a hot
+# and an empty expert, column blocks that end inside a tile
+@pytest.mark.parametrize("N,H,E,k,I,hot", [(1, 128, 4, 1, 128, False), (5, 256, 3, 2, 128, False),
+                                           (200, 256, 8, 3, 256, False), (300, 512, 4, 2, 384, True),
+                                           (1100, 256, 8, 2, 128, False), (600, 128, 5, 2, 640, True)])
+def test_gate_up_keeps_the_codes_of_its_bf16_rows(N, H, E, k, I, hot):
+    """h and the codes are bit for bit those of the GEMM that writes bf16 pre-activations and the
+    quantizer, with and without the shared expert; rows behind the last are left as they were."""
+    say(f"gate/up with kept codes N={N} H={H} E={E} k={k} I={I} hot={hot}")
+    x, w13, sw, off, ss, n_e = _gate_up_inputs(N, H, E, k, I, N + I, hot)
+    rows = N * k
+    au = torch.empty(rows + N, 2 * I, dtype=torch.bfloat16, device=DEV)
+    h = moe.moe_expert_gate_up_gathered_shared(x, ss, k, off, w13, sw, au=au)
+    q, s = moe.moe_quantize_mxfp8(au)
+    h2, q2, s2 = moe.moe_expert_gate_up_mxfp8(x, ss, k, off, w13, sw)
+    sync()
+    assert torch.equal(h, h2) and torch.equal(q, q2) and torch.equal(s, s2)
+    h3 = torch.full((rows, I), 3.0, dtype=torch.bfloat16, device=DEV)
+    q3 = torch.full((rows, 2 * I), 5, dtype=torch.uint8, device=DEV)
+    s3 = torch.full((rows, 2 * I // 32), 6, dtype=torch.uint8, device=DEV)
+    short = off.clone()
+    last = int(off[-1]) - int(n_e[-1])
+    short[-1] = last            # the last expert's rows count for nobody
+    moe.moe_expert_gate_up_mxfp8(x, ss, k, short, w13, rows=rows, h=h3, au_q=q3, au_scale=s3)
+    sync()
+    assert torch.equal(h3[:last], h[:last]) and torch.equal(q3[:last], q[:last]) and torch.equal(s3[:last], s[:last])
+    assert (h3[last:] == 3).all() and (q3[last:] == 5).all() and (s3[last:] == 6).all()
+
+
+def test_gate_up_kept_codes_not_finite():
+    """A token with a NaN gives NaN blocks in its own rows only."""
+    say("gate/up with kept codes: NaN")
+    x, w13, sw, off, ss, _ = _gate_up_inputs(40, 128, 4, 2, 128, 1)
+    x[7, 3] = float("nan")
+    _, q, s = moe.moe_expert_gate_up_mxfp8(x, ss, 2, off, w13, sw)
+    sync()
+    mine = np.concatenate([ss.cpu().numpy() // 2 == 7, np.arange(40) == 7])
+    assert (s.cpu().numpy()[mine] == 255).all() and (s.cpu().numpy()[~mine] != 255).all()
