@@ -24,13 +24,16 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_OP_DISPATCH_LAYOUT, MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM,
-               MOE_OP_GROUPED_FFN, MOE_OP_ROUTER, moe_combine, moe_combine_backward, moe_dispatch_layout,
-               moe_dequantize_fp8, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
+from . import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_BALANCE_LOSS, MOE_OP_DISPATCH_LAYOUT,
+               MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM, MOE_OP_GROUPED_FFN, MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD,
+               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_backward, moe_dequantize_fp8,
+               moe_dequantize_mxfp8, moe_dispatch_layout, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
                moe_expert_down_shared_e4m3, moe_expert_gate_up, moe_expert_gate_up_gathered,
-               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3, moe_expert_gate_up_preact,
-               moe_expert_wgrad, moe_grouped_ffn, moe_permute, moe_quantize_fp8, moe_route, moe_router_backward,
-               moe_router_input_grad, moe_router_logits, moe_swiglu_backward, moe_workspace_bytes)
+               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3, moe_expert_gate_up_mxfp8,
+               moe_expert_gate_up_preact, moe_expert_wgrad, moe_grouped_ffn, moe_permute, moe_quantize_fp8,
+               moe_quantize_mxfp8, moe_route, moe_router_backward, moe_router_dense_dgrad, moe_router_dense_wgrad,
+               moe_router_input_grad, moe_router_logits, moe_swiglu_backward, moe_swiglu_backward_mxfp8,
+               moe_workspace_bytes)
 
 
 class MoELayer:
@@ -125,6 +128,13 @@ class MoELayer:
         self.save_au = False     # the next forward keeps the gate/up pre-activations (training)
         self.au_saved = False    # the last forward kept them
         self.au_all = None
+        self.keep8 = False       # the last forward kept the tokens and pre-activations in 8 bits
+        self.kept_x = self.kept_au = None   # (codes, scales) of both
+        # the balance loss of the last forward: (loss [1], counts [S, E], mean probabilities [S, E],
+        # counted tokens [S]), or None; what its gradient needs; and its buffers and workspace by S
+        self.balance = None
+        self.balance_args = None
+        self.balance_bufs = {}
 
     _WEIGHTS = ("w13", "w2", "w13_scale", "w2_scale", "sw13", "sw2", "sw13_scale", "sw2_scale", "w_r", "bias")
     _WEIGHT_GRADS = ("dw13", "dw2", "dsw13", "dsw2", "dw_r")
@@ -134,8 +144,8 @@ class MoELayer:
 
         weights: the routed, shared and router weights, fp8 scales included; workspace: the
         library's scratch buffers; activations: the forward's other buffers (logits, routes,
-        layout, permuted rows, h, expert outputs, y; the kept pre-activations once a training
-        forward ran).  After a backward also weight_grads and backward (its intermediates and
+        layout, permuted rows, h, expert outputs, y; the kept pre-activations, or the 8-bit codes
+        of both, once a training forward ran; the balance loss's).  After a backward also weight_grads and backward (its intermediates and
         workspaces).  The caller's input x is not the layer's and is not counted.
         """
         seen, out = set(), {"weights": 0, "activations": 0, "workspace": 0}
@@ -149,6 +159,9 @@ class MoELayer:
         for name, v in vars(self).items():
             if name != "grads":
                 add("weights" if name in self._WEIGHTS else "workspace" if name.endswith("_ws") else "activations", v)
+        for v in self.balance_bufs.values():
+            add("activations", v[:4])
+            add("workspace", v[4])
         for name, v in (getattr(self, "grads", None) or {}).items():
             add("weight_grads" if name in self._WEIGHT_GRADS else "backward", v)
         return out
@@ -203,6 +216,11 @@ class MoELayer:
             return moe_expert_gate_up_gathered_shared_e4m3(self.x_deq, self.layout[3], self.k, self.layout[1],
                                                            self.w13, self.w13_scale, self.sw13, self.sw13_scale,
                                                            h=self.h_all, ws=self.fused_ws)
+        if self.keep8:
+            return moe_expert_gate_up_mxfp8(x, self.layout[3], self.k, self.layout[1], self.w13,
+                                            self.sw13 if self.fuse else None, h=self.h_all if self.fuse else self.h,
+                                            au_q=self.kept_au[0], au_scale=self.kept_au[1],
+                                            ws=self.fused_ws if self.fuse else self.ffn_ws)
         if self.fuse:
             return moe_expert_gate_up_gathered_shared(x, self.layout[3], self.k, self.layout[1], self.w13,
                                                       self.sw13, h=self.h_all, ws=self.fused_ws,
@@ -254,16 +272,56 @@ class MoELayer:
             self.shared_expert(x)
             self.shared_done.record(self.side)
 
-    def forward(self, x: torch.Tensor, z: Optional[torch.Tensor] = None, save_for_backward: bool = False) -> torch.Tensor:
-        """y for tokens x; z: the router logits (computed from W_r when None).  With
-        save_for_backward a bf16 layer that runs the shared expert inside the routed launches
-        also keeps the gate/up pre-activations, which backward then reads instead of
-        recomputing them."""
-        self.save_au = bool(save_for_backward and self.fuse and not self.fp8)
+    def _keep8_buffers(self):
+        """The kept codes and scales of the tokens and of all pre-activation rows."""
+        u8 = dict(dtype=torch.uint8, device=self.device)
+        rows = self.N * self.k + (self.N if self.fuse else 0)
+        self.kept_x = (torch.empty((self.N, self.H), **u8), torch.empty((self.N, self.H // MOE_MX_BLOCK), **u8))
+        self.kept_au = (torch.empty((rows, 2 * self.I), **u8), torch.empty((rows, 2 * self.I // MOE_MX_BLOCK), **u8))
+
+    def balance_step(self, z: torch.Tensor, alpha: float, seq_start: Optional[torch.Tensor] = None,
+                     token_mask: Optional[torch.Tensor] = None):
+        """The balance loss of the routes of z into self.balance (see moe_balance_loss)."""
+        S = 1 if seq_start is None else seq_start.numel() - 1
+        if S not in self.balance_bufs:
+            i32, f32 = dict(dtype=torch.int32, device=self.device), dict(dtype=torch.float32, device=self.device)
+            self.balance_bufs[S] = (
+                torch.empty(1, **f32), torch.empty((S, self.E), **i32), torch.empty((S, self.E), **f32),
+                torch.empty(S, **i32),
+                torch.empty(max(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, self.N, 0, 0, self.E, S, 0), 256),
+                            dtype=torch.uint8, device=self.device))
+        self.balance, ws = self.balance_bufs[S][:4], self.balance_bufs[S][4]
+        self.balance_args = dict(z=z, alpha=alpha, seq_start=seq_start, token_mask=token_mask)
+        return moe_balance_loss(z, self.topk_idx, alpha, bias=self.bias, seq_start=seq_start, token_mask=token_mask,
+                                out=self.balance, ws=ws)
+
+    def forward(self, x: torch.Tensor, z: Optional[torch.Tensor] = None, save_for_backward=False,
+                balance_alpha: Optional[float] = None, seq_start: Optional[torch.Tensor] = None,
+                token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y for tokens x; z: the router logits (computed from W_r when None).
+
+        save_for_backward True: a bf16 layer that runs the shared expert inside the routed
+        launches also keeps the gate/up pre-activations, which backward then reads instead of
+        recomputing them.  "mxfp8": a bf16 layer that gathers its rows keeps x and the
+        pre-activations as 8-bit codes (self.kept_x, self.kept_au); backward then reads nothing
+        else of the forward but the routes, neither x nor the expert outputs.
+        balance_alpha: also the balance loss of the batch's routes, into self.balance, and its
+        gradient in the next backward (seq_start, token_mask: see moe_balance_loss)."""
+        if save_for_backward not in (False, True, "mxfp8"):
+            raise ValueError('save_for_backward is False, True or "mxfp8"')
+        self.keep8 = save_for_backward == "mxfp8"
+        if self.keep8 and (self.dtype != "bf16" or not self.gather or (self.shared and not self.fuse)):
+            raise ValueError("8-bit keeping is built for bf16 layers that gather their rows from x and run a shared "
+                             "expert inside the routed launches")
+        self.save_au = bool(save_for_backward and not self.keep8 and self.fuse and not self.fp8)
         if self.save_au and self.au_all is None:
             self.au_all = torch.empty((self.N * self.k + self.N, 2 * self.I), dtype=torch.bfloat16,
                                       device=self.device)
         self.au_saved = self.save_au
+        if self.keep8:
+            if self.kept_x is None:
+                self._keep8_buffers()
+            moe_quantize_mxfp8(x, *self.kept_x)
         if self.side is not None:
             self.launch_shared_side(x)
         if z is None:
@@ -271,6 +329,10 @@ class MoELayer:
                 raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
             z = self.router(x)
         self.route(z)
+        if balance_alpha is None:
+            self.balance = self.balance_args = None
+        else:
+            self.balance_step(z, balance_alpha, seq_start, token_mask)
         self.dispatch()
         self.permute(x)
         self.experts(x)
@@ -285,63 +347,158 @@ class MoELayer:
     # ---- backward (bf16 layers that gather their rows from x)
 
     def _alloc_backward(self, dw_dtype: torch.dtype):
+        """The backward's buffers, each on the first step that needs it (a buffer is never replaced
+        while dw_dtype stays, so a captured backward keeps its memory)."""
         N, H, E, k, I = self.N, self.H, self.E, self.k, self.I
         rows = N * k
         dev, bf = self.device, torch.bfloat16
-        b = {}
-        b["d_eo"] = torch.empty((rows, H), dtype=bf, device=dev)
-        b["dg"] = torch.empty((N, k), dtype=torch.float32, device=dev)
-        b["au"] = torch.empty((rows, 2 * I), dtype=bf, device=dev)
-        b["dh"] = torch.empty((rows, I), dtype=bf, device=dev)
-        b["d_au"] = torch.empty((rows, 2 * I), dtype=bf, device=dev)
-        b["h"] = torch.empty((rows, I), dtype=bf, device=dev)
-        b["d_perm"] = torch.empty((rows, H), dtype=bf, device=dev)
-        b["x_perm"] = torch.empty((rows, H), dtype=bf, device=dev)
-        b["dw13"] = torch.empty((E, 2 * I, H), dtype=dw_dtype, device=dev)
-        b["dw2"] = torch.empty((E, H, I), dtype=dw_dtype, device=dev)
-        b["gemm_ws"] = torch.empty(max(moe_workspace_bytes(MOE_OP_EXPERT_GEMM, max(rows, N), H, I, E, 1, MOE_BF16),
-                                       256), dtype=torch.uint8, device=dev)
-        b["dgrad_ws"] = torch.empty(max(moe_workspace_bytes(MOE_OP_EXPERT_DGRAD, max(rows, N), 0, 0, E, 0, 0), 256),
-                                    dtype=torch.uint8, device=dev)
+        b = getattr(self, "grads", None)
+        if b is None or b["dw_dtype"] != dw_dtype:
+            b = {"dw_dtype": dw_dtype}
+
+        def need(name, shape, dtype):
+            if name not in b:
+                b[name] = torch.empty(shape, dtype=dtype, device=dev)
+
+        def need_ws(name, nbytes):
+            need(name, (max(nbytes, 256),), torch.uint8)
+
+        need("d_eo", (rows, H), bf)
+        need("dg", (N, k), torch.float32)
+        if not self.keep8:
+            need("au", (rows, 2 * I), bf)
+        elif self.shared or self.w_r is not None:
+            need("x", (N, H), bf)   # the kept tokens' values
+        need("dh", (rows, I), bf)
+        need("d_au", (rows, 2 * I), bf)
+        need("h", (rows, I), bf)
+        need("d_perm", (rows, H), bf)
+        need("x_perm", (rows, H), bf)
+        need("dw13", (E, 2 * I, H), dw_dtype)
+        need("dw2", (E, H, I), dw_dtype)
+        need_ws("gemm_ws", moe_workspace_bytes(MOE_OP_EXPERT_GEMM, max(rows, N), H, I, E, 1, MOE_BF16))
+        need_ws("dgrad_ws", moe_workspace_bytes(MOE_OP_EXPERT_DGRAD, max(rows, N), 0, 0, E, 0, 0))
         if self.shared:
             # (the shared expert's steps have workspaces of their own: they may run on a
             # second stream beside the routed ones)
-            b["gemm_ws_s"] = torch.empty(max(moe_workspace_bytes(MOE_OP_EXPERT_GEMM, N, H, I, 1, 1, MOE_BF16), 256),
-                                         dtype=torch.uint8, device=dev)
-            b["dgrad_ws_s"] = torch.empty(max(moe_workspace_bytes(MOE_OP_EXPERT_DGRAD, N, 0, 0, 1, 0, 0), 256),
-                                          dtype=torch.uint8, device=dev)
-            b["shared_offsets"] = torch.tensor([0, N], dtype=torch.int32, device=dev)
-            b["au_s"] = torch.empty((N, 2 * I), dtype=bf, device=dev)
-            b["dh_s"] = torch.empty((N, I), dtype=bf, device=dev)
-            b["d_au_s"] = torch.empty((N, 2 * I), dtype=bf, device=dev)
-            b["h_s"] = torch.empty((N, I), dtype=bf, device=dev)
-            b["dx_s"] = torch.empty((N, H), dtype=bf, device=dev)
-            b["dsw13"] = torch.empty((1, 2 * I, H), dtype=dw_dtype, device=dev)
-            b["dsw2"] = torch.empty((1, H, I), dtype=dw_dtype, device=dev)
+            need_ws("gemm_ws_s", moe_workspace_bytes(MOE_OP_EXPERT_GEMM, N, H, I, 1, 1, MOE_BF16))
+            need_ws("dgrad_ws_s", moe_workspace_bytes(MOE_OP_EXPERT_DGRAD, N, 0, 0, 1, 0, 0))
+            if "shared_offsets" not in b:
+                b["shared_offsets"] = torch.tensor([0, N], dtype=torch.int32, device=dev)
+            if not self.keep8:
+                need("au_s", (N, 2 * I), bf)
+            need("dh_s", (N, I), bf)
+            need("d_au_s", (N, 2 * I), bf)
+            need("h_s", (N, I), bf)
+            need("dx_s", (N, H), bf)
+            need("dsw13", (1, 2 * I, H), dw_dtype)
+            need("dsw2", (1, H, I), dw_dtype)
+        if self.balance_args is not None:   # the whole logit gradient (fp32 where the caller has the router)
+            need("dz_all", (N, E), bf if self.w_r is not None else torch.float32)
+            need_ws("wgrad_ws", moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, MOE_BF16))
         if self.w_r is not None:
-            b["dz"] = torch.empty((N, k), dtype=torch.float32, device=dev)
-            b["dw_r"] = torch.empty((E, H), dtype=dw_dtype, device=dev)
-            b["dx_r"] = torch.empty((N, H), dtype=bf, device=dev)
-        b["dx"] = torch.empty((N, H), dtype=bf, device=dev)
-        b["dw_dtype"] = dw_dtype
+            if self.balance_args is None:
+                need("dz", (N, k), torch.float32)
+            need("dw_r", (E, H), dw_dtype)
+            need("dx_r", (N, H), bf)
+        need("dx", (N, H), bf)
         self.grads = b
 
-    def backward_steps(self, x: torch.Tensor, dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16) -> list:
+    def _gradients(self) -> dict:
+        """self.grads without the logit gradient of the other kind of forward (an earlier one's)."""
+        stale = "dz_all" if self.balance_args is None else "dz"
+        return {n: t for n, t in self.grads.items() if n != stale} if stale in self.grads else self.grads
+
+    def backward_steps(self, x: Optional[torch.Tensor], dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16,
+                       d_loss: Optional[torch.Tensor] = None) -> list:
         """The backward pass as (name, call) steps in stream order (see backward)."""
         if self.dtype != "bf16" or not self.gather:
             raise ValueError("the backward pass is built for bf16 layers that gather their rows from x")
-        if self.gate_in_down:
+        keep8, dense = self.keep8, self.balance_args is not None
+        if self.gate_in_down and not keep8:
             raise ValueError("backward needs the unscaled expert outputs (gate_in_down=False)")
-        if getattr(self, "grads", None) is None or self.grads["dw_dtype"] != dw_dtype:
-            self._alloc_backward(dw_dtype)
+        if x is None and not keep8:
+            raise ValueError('backward needs x unless the forward kept it (save_for_backward="mxfp8")')
+        self._alloc_backward(dw_dtype)
         b = self.grads
         k, N = self.k, self.N
         rows = N * k
         offsets, send_pos, src_slot = self.layout[1], self.layout[2], self.layout[3]
+        st = []
+        if keep8:
+            # x's values from its codes; the upstream rows before the gates (they enter behind the
+            # down projection, where the gates' own gradient is <dh, h>)
+            kx, (qa, sa) = self.kept_x, self.kept_au
+            x = b.get("x")
+            if x is not None:
+                st.append(("x_values", lambda: moe_dequantize_mxfp8(kx[0], kx[1], out=x)))
+            st += [
+                ("dy_permute", lambda: moe_permute(dy, send_pos, k, None, b["d_eo"])),
+                ("down_dgrad", lambda: moe_expert_dgrad(b["d_eo"], offsets, self.w2, b["dh"], b["dgrad_ws"])),
+                ("swiglu_bwd", lambda: moe_swiglu_backward_mxfp8(qa[:rows], sa[:rows], b["dh"], send_pos,
+                                                                 self.topk_gate, b["d_au"], b["h"], b["dg"])),
+            ]
+        else:
+            st += self._preact_steps(x, dy)
+        xp = ((lambda: moe_dequantize_mxfp8(kx[0], kx[1], out=b["x_perm"], send_pos=send_pos, k=k)) if keep8 else
+              (lambda: moe_permute(x, send_pos, k, None, b["x_perm"])))
+        st += [
+            ("down_wgrad", lambda: moe_expert_wgrad(b["d_eo"], b["h"], offsets, dw=b["dw2"], rows=rows)),
+            # the weight gradient of W13 reads the expert-ordered rows of x (a permuted copy:
+            # the wgrad kernel streams its B operand in layout order)
+            ("x_permute", xp),
+            ("gate_up_wgrad", lambda: moe_expert_wgrad(b["d_au"], b["x_perm"], offsets, dw=b["dw13"], rows=rows)),
+            ("gate_up_dgrad", lambda: moe_expert_dgrad(b["d_au"], offsets, self.w13, b["d_perm"], b["dgrad_ws"])),
+        ]
+        rest = None
+        if self.shared:
+            so = b["shared_offsets"]
+            saved = self.au_saved
+            au_s = self.au_all[rows:] if saved else b.get("au_s")
+            if not saved and not keep8:
+                st.append(("shared_preact", lambda: moe_expert_gate_up_preact(x, so, self.sw13, N, None, 1,
+                                                                              b["au_s"], b["gemm_ws_s"])))
+            swiglu = ((lambda: moe_swiglu_backward_mxfp8(qa[rows:], sa[rows:], b["dh_s"], d_au=b["d_au_s"], h=b["h_s"]))
+                      if keep8 else (lambda: moe_swiglu_backward(au_s, b["dh_s"], b["d_au_s"], b["h_s"])))
+            st += [
+                ("shared_down_dgrad", lambda: moe_expert_dgrad(dy, so, self.sw2, b["dh_s"], b["dgrad_ws_s"])),
+                ("shared_swiglu_bwd", swiglu),
+                ("shared_down_wgrad", lambda: moe_expert_wgrad(dy, b["h_s"], so, dw=b["dsw2"], rows=N)),
+                ("shared_gate_up_wgrad", lambda: moe_expert_wgrad(b["d_au_s"], x, so, dw=b["dsw13"], rows=N)),
+                ("shared_gate_up_dgrad", lambda: moe_expert_dgrad(b["d_au_s"], so, self.sw13, b["dx_s"],
+                                                                  b["dgrad_ws_s"])),
+            ]
+            rest = b["dx_s"]
+        if dense:
+            # the gates' gradient on the selected logits and the balance loss's on all of them
+            ba, (_, counts, _, tokens) = self.balance_args, self.balance
+            st.append(("logit_grad", lambda: moe_balance_loss_backward(
+                ba["z"], self.topk_idx, ba["alpha"], counts, tokens, bias=self.bias, seq_start=ba["seq_start"],
+                token_mask=ba["token_mask"], d_loss=d_loss, topk_gate=self.topk_gate, d_gate=b["dg"], dz=b["dz_all"])))
+        if self.w_r is not None:
+            # sum_j dz_tj W_r[e_tj] (+ the shared expert's input gradient); dense: over all experts
+            rest_r = rest
+            st += [
+                ("router_bwd", lambda: moe_router_dense_wgrad(b["dz_all"], x, dw=b["dw_r"], ws=b["wgrad_ws"])),
+                ("router_dx", lambda: moe_router_dense_dgrad(b["dz_all"], self.w_r, rest=rest_r, dx=b["dx_r"])),
+            ] if dense else [
+                ("router_bwd", lambda: moe_router_backward(self.topk_gate, b["dg"], offsets, src_slot, x, b["dz"],
+                                                           b["dw_r"])),
+                ("router_dx", lambda: moe_router_input_grad(self.w_r, self.topk_idx, b["dz"], rest_r, b["dx_r"])),
+            ]
+            rest = b["dx_r"]
+        rest_x = rest
+        st.append(("dx", lambda: moe_combine(b["d_perm"], send_pos, None, rest_x, b["dx"], k=k)))
+        return st
+
+    def _preact_steps(self, x: torch.Tensor, dy: torch.Tensor) -> list:
+        """Up to the SwiGLU backward, with bf16 pre-activations."""
+        b, k = self.grads, self.k
+        rows = self.N * k
+        offsets, send_pos, src_slot = self.layout[1], self.layout[2], self.layout[3]
         # the pre-activations: kept by the forward, or recomputed here
         saved = self.au_saved
         au = self.au_all[:rows] if saved else b["au"]
-        au_s = self.au_all[rows:] if saved else b.get("au_s")
         st = [
             ("combine_bwd", lambda: moe_combine_backward(dy, send_pos, self.topk_gate, self.expert_out, b["d_eo"],
                                                          b["dg"])),
@@ -352,43 +509,11 @@ class MoELayer:
         st += [
             ("down_dgrad", lambda: moe_expert_dgrad(b["d_eo"], offsets, self.w2, b["dh"], b["dgrad_ws"])),
             ("swiglu_bwd", lambda: moe_swiglu_backward(au, b["dh"], b["d_au"], b["h"])),
-            ("down_wgrad", lambda: moe_expert_wgrad(b["d_eo"], b["h"], offsets, dw=b["dw2"], rows=rows)),
-            # the weight gradient of W13 reads the expert-ordered rows of x (a permuted copy:
-            # the wgrad kernel streams its B operand in layout order)
-            ("x_permute", lambda: moe_permute(x, send_pos, k, None, b["x_perm"])),
-            ("gate_up_wgrad", lambda: moe_expert_wgrad(b["d_au"], b["x_perm"], offsets, dw=b["dw13"], rows=rows)),
-            ("gate_up_dgrad", lambda: moe_expert_dgrad(b["d_au"], offsets, self.w13, b["d_perm"], b["dgrad_ws"])),
         ]
-        rest = None
-        if self.shared:
-            so = b["shared_offsets"]
-            if not saved:
-                st.append(("shared_preact", lambda: moe_expert_gate_up_preact(x, so, self.sw13, N, None, 1,
-                                                                              b["au_s"], b["gemm_ws_s"])))
-            st += [
-                ("shared_down_dgrad", lambda: moe_expert_dgrad(dy, so, self.sw2, b["dh_s"], b["dgrad_ws_s"])),
-                ("shared_swiglu_bwd", lambda: moe_swiglu_backward(au_s, b["dh_s"], b["d_au_s"], b["h_s"])),
-                ("shared_down_wgrad", lambda: moe_expert_wgrad(dy, b["h_s"], so, dw=b["dsw2"], rows=N)),
-                ("shared_gate_up_wgrad", lambda: moe_expert_wgrad(b["d_au_s"], x, so, dw=b["dsw13"], rows=N)),
-                ("shared_gate_up_dgrad", lambda: moe_expert_dgrad(b["d_au_s"], so, self.sw13, b["dx_s"],
-                                                                  b["dgrad_ws_s"])),
-            ]
-            rest = b["dx_s"]
-        if self.w_r is not None:
-            # sum_j dz_tj W_r[e_tj] (+ the shared expert's input gradient)
-            rest_r = rest
-            st += [
-                ("router_bwd", lambda: moe_router_backward(self.topk_gate, b["dg"], offsets, src_slot, x, b["dz"],
-                                                           b["dw_r"])),
-                ("router_dx", lambda: moe_router_input_grad(self.w_r, self.topk_idx, b["dz"], rest_r, b["dx_r"])),
-            ]
-            rest = b["dx_r"]
-        rest_x = rest
-        st.append(("dx", lambda: moe_combine(b["d_perm"], send_pos, None, rest_x, b["dx"], k=k)))
         return st
 
-    def backward(self, x: torch.Tensor, dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16,
-                 overlap_shared: bool = False) -> dict:
+    def backward(self, x: Optional[torch.Tensor], dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16,
+                 overlap_shared: bool = False, d_loss: Optional[torch.Tensor] = None) -> dict:
         """Gradients of the last forward for the upstream gradient dy [N, H] (bf16).
 
         The backward mirrors the forward ("DeepSeek MoE: EP and FSDP guide": dispatch's
@@ -402,17 +527,26 @@ class MoELayer:
         With overlap_shared the shared expert's steps (which need only x, dy and its
         pre-activations) run on a second stream (default priority) beside the routed ones, and
         the input-gradient sum waits for them.
+
+        After a forward with save_for_backward="mxfp8" x may be None: the tokens and
+        pre-activations are the kept codes' values, h and the gates' gradient come from them
+        (d_gate = <dy W_down, h>), and the expert outputs are not read.  After a forward with a
+        balance loss its gradient times d_loss ([1] fp32, None: 1) joins the gates' in the logits'
+        gradient 'dz_all' [N, E], which then gives dW_r and the router's share of dx.
         """
-        steps = self.backward_steps(x, dy, dw_dtype)
+        steps = self.backward_steps(x, dy, dw_dtype, d_loss)
         if not (overlap_shared and self.shared):
             for _, f in steps:
                 f()
-            return self.grads
+            return self._gradients()
         main = torch.cuda.current_stream(self.device)
         if getattr(self, "bwd_side", None) is None:
             self.bwd_side = torch.cuda.Stream(device=self.device)
             self.bwd_side_done = torch.cuda.Event()
         side = self.bwd_side
+        for name, f in steps:
+            if name == "x_values":   # (both streams read them)
+                f()
         side.wait_stream(main)
         with torch.cuda.stream(side):
             for name, f in steps:
@@ -420,7 +554,7 @@ class MoELayer:
                     f()
             self.bwd_side_done.record(side)
         for name, f in steps:
-            if name.startswith("shared_"):
+            if name.startswith("shared_") or name == "x_values":
                 continue
             if name in ("router_dx", "dx") and not getattr(self, "_waited", False):
                 main.wait_event(self.bwd_side_done)   # the shared expert's dx joins here
@@ -428,8 +562,9 @@ class MoELayer:
             f()
         self._waited = False
         for t in (x, dy):
-            t.record_stream(side)
-        return self.grads
+            if t is not None:
+                t.record_stream(side)
+        return self._gradients()
 
 
 class PipelinedMoE:
