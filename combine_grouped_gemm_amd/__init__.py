@@ -156,7 +156,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(t: torch.Tensor):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)   # (current_stream(...).cuda_stream, without its objects)
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -175,14 +175,31 @@ def _torch_dt(dt: int) -> torch.dtype:
 
 def _expect(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None:
     """Raises ValueError unless t (if given) has this shape, one of these dtypes and this device."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype in dtypes and t.device == device):
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _run(fn: str, device: torch.device, *args) -> None:
+    """Calls a C entry point with `device` as the current one."""
+    f = getattr(lib(), fn)
+    if device.index == torch.cuda.current_device():
+        status = f(*args)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args)
+    if status != MOE_OK:
+        raise MoEError(fn, status)
+
+
+def _optional_ws(op: int, N: int, H: int, E: int, k: int, dt: int, device):
+    """(workspace or None, its bytes) for an op that may need none."""
+    nbytes = lib().moe_workspace_bytes(op, N, H, 0, E, k, dt)
+    return (torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None), nbytes
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -626,19 +643,21 @@ def moe_balance_loss(z: torch.Tensor, topk_idx: torch.Tensor, alpha: float, bias
     N, E, k, S = _balance_args(z, topk_idx, bias, seq_start, token_mask)
     dev = z.device
     if out is None:
-        out = (torch.empty(1, dtype=torch.float32, device=dev), torch.empty((S, E), dtype=torch.int32, device=dev),
-               torch.empty((S, E), dtype=torch.float32, device=dev), torch.empty(S, dtype=torch.int32, device=dev))
-    loss, counts, prob_mean, tokens = out
-    _expect("loss", loss, (1,), _F32, dev)
-    _expect("counts", counts, (S, E), _I32, dev)
-    _expect("prob_mean", prob_mean, (S, E), _F32, dev)
-    _expect("tokens", tokens, (S,), _I32, dev)
+        loss, tokens = torch.empty(1, dtype=torch.float32, device=dev), torch.empty(S, dtype=torch.int32, device=dev)
+        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+        prob_mean = torch.empty((S, E), dtype=torch.float32, device=dev)
+    else:
+        loss, counts, prob_mean, tokens = out
+        _expect("loss", loss, (1,), _F32, dev)
+        _expect("counts", counts, (S, E), _I32, dev)
+        _expect("prob_mean", prob_mean, (S, E), _F32, dev)
+        _expect("tokens", tokens, (S,), _I32, dev)
     if ws is None:
-        ws = _workspace(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0), dev)
-    with torch.cuda.device(dev):
-        _check("moe_balance_loss", lib().moe_balance_loss(
-            _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(loss),
-            _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws.numel(), _stream(z)))
+        ws, ws_bytes = _optional_ws(MOE_OP_BALANCE_LOSS, N, 0, E, S, 0, dev)
+    else:
+        ws_bytes = ws.numel()
+    _run("moe_balance_loss", dev, _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask),
+         alpha, _ptr(loss), _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws_bytes, _stream(z))
     return loss, counts, prob_mean, tokens
 
 
@@ -659,11 +678,11 @@ def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: fl
     _expect("d_gate", d_gate, (N, k), _F32, dev)
     if dz is None:
         dz = torch.empty((N, E), dtype=dz_dtype, device=dev)
-    _expect("dz", dz, (N, E), _ACT, dev)
-    with torch.cuda.device(dev):
-        _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-            _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask), alpha, _ptr(counts),
-            _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz), _dt(dz), _stream(z)))
+    else:
+        _expect("dz", dz, (N, E), _ACT, dev)
+    _run("moe_balance_loss_backward", dev, _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S,
+         _ptr(token_mask), alpha, _ptr(counts), _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz),
+         _dt(dz), _stream(z))
     return dz
 
 
@@ -677,12 +696,14 @@ def moe_router_dense_wgrad(dz: torch.Tensor, x: torch.Tensor, dw: Optional[torch
     _expect("dz", dz, (N, E), (x.dtype,), dev)
     if dw is None:
         dw = torch.empty((E, H), dtype=dw_dtype, device=dev)
-    _expect("dw", dw, (E, H), _ACT, dev)
+    else:
+        _expect("dw", dw, (E, H), _ACT, dev)
     if ws is None:
-        ws = _workspace(moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, _dt(x)), dev)
-    with torch.cuda.device(dev):
-        _check("moe_router_dense_wgrad", lib().moe_router_dense_wgrad(
-            _ptr(dz), _ptr(x), _dt(x), N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws.numel(), _stream(x)))
+        ws, ws_bytes = _optional_ws(MOE_OP_ROUTER_WGRAD, N, H, E, 0, _dt(x), dev)
+    else:
+        ws_bytes = ws.numel()
+    _run("moe_router_dense_wgrad", dev, _ptr(dz), _ptr(x), _dt(x), N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws_bytes,
+         _stream(x))
     return dw
 
 
@@ -697,10 +718,9 @@ def moe_router_dense_dgrad(dz: torch.Tensor, w_r: torch.Tensor, rest: Optional[t
     _expect("rest", rest, (N, H), (w_r.dtype,), dev)
     if dx is None:
         dx = torch.empty((N, H), dtype=w_r.dtype, device=dev)
-    _expect("dx", dx, (N, H), (w_r.dtype,), dev)
-    with torch.cuda.device(dev):
-        _check("moe_router_dense_dgrad", lib().moe_router_dense_dgrad(
-            _ptr(dz), _ptr(w_r), _dt(w_r), N, E, H, _ptr(rest), _ptr(dx), _stream(w_r)))
+    else:
+        _expect("dx", dx, (N, H), (w_r.dtype,), dev)
+    _run("moe_router_dense_dgrad", dev, _ptr(dz), _ptr(w_r), _dt(w_r), N, E, H, _ptr(rest), _ptr(dx), _stream(w_r))
     return dx
 
 
@@ -714,18 +734,20 @@ _CODES = (torch.uint8,)
 def moe_quantize_mxfp8(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None):
     """(codes uint8 of x's shape, scale bytes uint8 [..., cols / 32]): e4m3 codes, 32 columns to a
     power-of-two scale that keeps the block's largest value below 448."""
-    cols = x.shape[-1]
+    shape, dev = x.shape, x.device
     if x.dtype not in _ACT:
         raise ValueError(f"x must be float32 or bfloat16, not {x.dtype}")
+    cols = shape[-1]
+    scales = shape[:-1] + (cols // MOE_MX_BLOCK,)
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        q = torch.empty(shape, dtype=torch.uint8, device=dev)
+    else:
+        _expect("q", q, shape, _CODES, dev)
     if scale is None:
-        scale = torch.empty(tuple(x.shape[:-1]) + (cols // MOE_MX_BLOCK,), dtype=torch.uint8, device=x.device)
-    _expect("q", q, x.shape, _CODES, x.device)
-    _expect("scale", scale, tuple(x.shape[:-1]) + (cols // MOE_MX_BLOCK,), _CODES, x.device)
-    with torch.cuda.device(x.device):
-        _check("moe_quantize_mxfp8", lib().moe_quantize_mxfp8(_ptr(x), _dt(x), x.numel() // max(cols, 1), cols, _ptr(q),
-                                                              _ptr(scale), _stream(x)))
+        scale = torch.empty(scales, dtype=torch.uint8, device=dev)
+    else:
+        _expect("scale", scale, scales, _CODES, dev)
+    _run("moe_quantize_mxfp8", dev, _ptr(x), _dt(x), x.numel() // max(cols, 1), cols, _ptr(q), _ptr(scale), _stream(x))
     return q, scale
 
 
@@ -734,19 +756,19 @@ def moe_dequantize_mxfp8(q: torch.Tensor, scale: torch.Tensor, out: Optional[tor
                          k: int = 1) -> torch.Tensor:
     """The values of moe_quantize_mxfp8's codes (exact in bf16): as they lie, or with send_pos
     [rows * k] each row's to its k rows of out [send_pos.numel(), cols] (moe_permute's map)."""
-    cols = q.shape[-1]
+    shape, dev = q.shape, q.device
+    cols = shape[-1]
     rows = q.numel() // max(cols, 1)
-    dev = q.device
-    _expect("q", q, q.shape, _CODES, dev)
-    _expect("scale", scale, tuple(q.shape[:-1]) + (cols // MOE_MX_BLOCK,), _CODES, dev)
-    _expect("send_pos", send_pos, (rows * k,), (torch.int32,), dev)
+    if q.dtype != torch.uint8:
+        raise ValueError(f"q must be uint8, not {q.dtype}")
+    _expect("scale", scale, shape[:-1] + (cols // MOE_MX_BLOCK,), _CODES, dev)
+    _expect("send_pos", send_pos, (rows * k,), _I32, dev)
     if out is None:
-        out = torch.empty(q.shape if send_pos is None else (rows * k, cols), dtype=dtype, device=dev)
-    _expect("out", out, q.shape if send_pos is None else (out.shape[0], cols), _ACT, dev)
-    with torch.cuda.device(dev):
-        _check("moe_dequantize_mxfp8", lib().moe_dequantize_mxfp8(
-            _ptr(q), _ptr(scale), rows, cols, k, _ptr(send_pos), out.shape[0] if out.dim() else 0, _ptr(out), _dt(out),
-            _stream(q)))
+        out = torch.empty(shape if send_pos is None else (rows * k, cols), dtype=dtype, device=dev)
+    else:
+        _expect("out", out, shape if send_pos is None else (out.shape[0], cols), _ACT, dev)
+    _run("moe_dequantize_mxfp8", dev, _ptr(q), _ptr(scale), rows, cols, k, _ptr(send_pos),
+         out.shape[0] if out.dim() else 0, _ptr(out), _dt(out), _stream(q))
     return out
 
 
@@ -772,22 +794,21 @@ def moe_expert_gate_up_mxfp8(x: torch.Tensor, src_slot: torch.Tensor, k: int, of
         raise ValueError(f"src_slot must name {rows} rows")
     if shared_w13 is not None:
         _expect("shared_w13", shared_w13.reshape(-1, H), (2 * I, H), bf, dev)
+    scales = (total, 2 * I // MOE_MX_BLOCK)
+    _expect("h", h, (total, I), bf, dev)
+    _expect("au_q", au_q, (total, 2 * I), _CODES, dev)
+    _expect("au_scale", au_scale, scales, _CODES, dev)
     if h is None:
         h = torch.empty((total, I), dtype=torch.bfloat16, device=dev)
     if au_q is None:
         au_q = torch.empty((total, 2 * I), dtype=torch.uint8, device=dev)
     if au_scale is None:
-        au_scale = torch.empty((total, 2 * I // MOE_MX_BLOCK), dtype=torch.uint8, device=dev)
-    _expect("h", h, (total, I), bf, dev)
-    _expect("au_q", au_q, (total, 2 * I), _CODES, dev)
-    _expect("au_scale", au_scale, (total, 2 * I // MOE_MX_BLOCK), _CODES, dev)
+        au_scale = torch.empty(scales, dtype=torch.uint8, device=dev)
     if ws is None:
         n_seg = E + (1 if shared_w13 is not None else 0)
         ws = _workspace(moe_workspace_bytes(MOE_OP_EXPERT_GEMM, total, H, I, n_seg, 1, MOE_BF16), dev)
-    with torch.cuda.device(dev):
-        _check("moe_expert_gate_up_mxfp8", lib().moe_expert_gate_up_mxfp8(
-            _ptr(x), _dt(x), N, _ptr(src_slot), k, _ptr(offsets), E, rows, H, I, _ptr(w13), _ptr(shared_w13), _ptr(h),
-            _ptr(au_q), _ptr(au_scale), _ptr(ws), ws.numel(), _stream(x)))
+    _run("moe_expert_gate_up_mxfp8", dev, _ptr(x), _dt(x), N, _ptr(src_slot), k, _ptr(offsets), E, rows, H, I,
+         _ptr(w13), _ptr(shared_w13), _ptr(h), _ptr(au_q), _ptr(au_scale), _ptr(ws), ws.numel(), _stream(x))
     return h, au_q, au_scale
 
 
@@ -807,19 +828,18 @@ def moe_swiglu_backward_mxfp8(au_q: torch.Tensor, au_scale: torch.Tensor, dh: to
     _expect("au_scale", au_scale, (rows, 2 * I // MOE_MX_BLOCK), _CODES, dev)
     _expect("send_pos", send_pos, (slots,), (torch.int32,), dev)
     for name, t in (("topk_gate", topk_gate), ("d_gate", d_gate)):
-        if t is not None and t.numel() != slots:
-            raise ValueError(f"{name} must have one value for each of the {slots} slots")
-        _expect(name, t, t.shape if t is not None else (), (torch.float32,), dev)
+        if t is not None:
+            if t.numel() != slots:
+                raise ValueError(f"{name} must have one value for each of the {slots} slots")
+            _expect(name, t, t.shape, _F32, dev)
+    _expect("d_au", d_au, (rows, 2 * I), (dh.dtype,), dev)
+    _expect("h", h, (rows, I), (dh.dtype,), dev)
     if d_au is None:
         d_au = torch.empty((rows, 2 * I), dtype=dh.dtype, device=dev)
     if h is None:
         h = torch.empty((rows, I), dtype=dh.dtype, device=dev)
     if d_gate is None and topk_gate is not None:
         d_gate = torch.empty_like(topk_gate)
-    _expect("d_au", d_au, (rows, 2 * I), (dh.dtype,), dev)
-    _expect("h", h, (rows, I), (dh.dtype,), dev)
-    with torch.cuda.device(dev):
-        _check("moe_swiglu_backward_mxfp8", lib().moe_swiglu_backward_mxfp8(
-            _ptr(au_q), _ptr(au_scale), _ptr(dh), _dt(dh), rows, I, slots, _ptr(send_pos), _ptr(topk_gate), _ptr(d_au),
-            _ptr(h), _ptr(d_gate), _stream(dh)))
+    _run("moe_swiglu_backward_mxfp8", dev, _ptr(au_q), _ptr(au_scale), _ptr(dh), _dt(dh), rows, I, slots,
+         _ptr(send_pos), _ptr(topk_gate), _ptr(d_au), _ptr(h), _ptr(d_gate), _stream(dh))
     return d_au, h, d_gate

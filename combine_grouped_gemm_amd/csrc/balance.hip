@@ -29,23 +29,45 @@
 namespace moe {
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 1024;   // loss: 16 waves, so that a CU's tokens in flight hide their loads
 constexpr int kBalWaves = kBalThreads / kWave;
-constexpr int kBalMaxChunks = 512;
-constexpr int kBalEx = 16;    // experts of a second-launch workgroup
-constexpr int kBalRows = kBalThreads / kBalEx;
+constexpr int kBalMaxChunks = 512;   // two workgroups a CU
+constexpr int kBalEx = 16;    // the fewest experts of a second-launch workgroup
+constexpr int kBalBatch = 8;  // partial sums a thread of it loads together
+constexpr int kBwdThreads = 256;
 
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+// Butterfly reductions over groups of G lanes, every lane ending with the result, without LDS:
+// within 16 lanes by DPP (lane ^ 1, lane ^ 2, then the 8- and 16-lane mirrors, whose partners hold
+// equal values by then), across by gfx950's permlane swaps.  (Shuffles through LDS took about a third
+// of the loss kernel's time at E = 256.)
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int G, typename F>
+__device__ __forceinline__ float group_reduce(float v, F&& f) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  if constexpr (G >= 2) v = f(v, dpp_f32<0xB1>(v));
+  if constexpr (G >= 4) v = f(v, dpp_f32<0x4E>(v));
+  if constexpr (G >= 8) v = f(v, dpp_f32<0x141>(v));
+  if constexpr (G >= 16) v = f(v, dpp_f32<0x140>(v));
+  if constexpr (G >= 32) {
+    const u32x2_t t = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(t[0]), __uint_as_float(t[1]));
+  }
+  if constexpr (G >= 64) {
+    const u32x2_t t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(t[0]), __uint_as_float(t[1]));
+  }
   return v;
 }
 template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int G>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
-  return v;
+  return group_reduce<G>(v, [](float a, float b) { return a + b; });
 }
 
 __device__ __forceinline__ int clamp_token(int t, int N) { return t < 0 ? 0 : (t < N ? t : N); }
@@ -62,39 +84,50 @@ __device__ __forceinline__ int sequence_of(const int32_t* seq_start, int S, int 
   return lo;
 }
 
-// The softmax of one token's biased logits: p[v * W + w] is that of expert (v G + l) W + w (0
-// past E).  A row of -inf has no probabilities: all 0.
+// One token's biased logits: p[v * W + w] is that of expert (v G + l) W + w (-inf past E)
 template <int G, int V, int W>
-__device__ __forceinline__ void token_softmax(const float* zr, const float* bias, int E, int l, float (&p)[V * W]) {
-  float m = -INFINITY;
+__device__ __forceinline__ void load_logits(const float* zr, int E, int l, float (&p)[V * W]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = (v * G + l) * W;
     if constexpr (W == 4) {
       float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (e < E) {
-        q = *reinterpret_cast<const float4*>(zr + e);
-        if (bias != nullptr) {
-          q.x += bias[e]; q.y += bias[e + 1]; q.z += bias[e + 2]; q.w += bias[e + 3];
-        }
-      }
+      if (e < E) q = *reinterpret_cast<const float4*>(zr + e);
       p[4 * v] = q.x; p[4 * v + 1] = q.y; p[4 * v + 2] = q.z; p[4 * v + 3] = q.w;
     } else {
-      p[v] = e < E ? (bias != nullptr ? zr[e] + bias[e] : zr[e]) : -INFINITY;
+      p[v] = e < E ? zr[e] : -INFINITY;
     }
+  }
+}
+// the lane's experts' biases (0 without one: a sum with 0 keeps every logit)
+template <int G, int V, int W>
+__device__ __forceinline__ void load_bias(const float* bias, int E, int l, float (&b)[V * W]) {
 #pragma unroll
-    for (int w = 0; w < W; ++w) m = fmaxf(m, p[v * W + w]);
+  for (int i = 0; i < V * W; ++i) {
+    const int e = ((i / W) * G + l) * W + i % W;
+    b[i] = bias != nullptr && e < E ? bias[e] : 0.0f;
+  }
+}
+// in place: logits plus biases to probabilities.  A row of -inf has none: all 0.
+template <int G, int V, int W>
+__device__ __forceinline__ void softmax_row(float (&p)[V * W], const float (&b)[V * W]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V * W; ++i) {
+    p[i] += b[i];
+    m = fmaxf(m, p[i]);
   }
   m = group_max<G>(m);
   if (m == -INFINITY) m = 0.0f;   // (every exponential is then 0; a NaN logit stays NaN)
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < V * W; ++i) {
-    p[i] = expf(p[i] - m);
+    // e^x = 2^(x log2 e) on the hardware exponential: within |x| + 2 roundings of fp32
+    p[i] = __builtin_amdgcn_exp2f((p[i] - m) * 1.4426950408889634f);
     sum += p[i];
   }
   sum = group_sum<G>(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
   for (int i = 0; i < V * W; ++i) p[i] *= inv;
 }
@@ -110,7 +143,7 @@ struct BalArgs {
   float* part_p;       // [chunks + S, E]
   int32_t* part_c;     // [chunks + S, E]
   int32_t* part_t;     // [chunks + S]
-  float* part_l;       // [S, ceil(E / kBalEx)]
+  float* part_l;       // [S, expert blocks of the second launch]
   int32_t* ticket;
   float* loss;
   int32_t* counts;
@@ -118,38 +151,58 @@ struct BalArgs {
   int32_t* tokens;
 };
 
-template <int G, int V, int W>
+// SINGLE: at most one chunk of the only sequence; the totals and the loss are written here
+template <int G, int V, int W, bool SINGLE>
 __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(BalArgs a) {
   constexpr int kGroups = kBalThreads / G;
   __shared__ float red[kBalWaves * G * V * W];
   __shared__ int32_t hist[G * V * W];
   __shared__ int32_t n_tok;
   const int tid = threadIdx.x, l = tid % G, grp = tid / G, wave = tid / kWave;
-  if (blockIdx.x == 0 && tid == 0) *a.ticket = 0;   // (read by the launch after this one)
+  if (!SINGLE && blockIdx.x == 0 && tid == 0) *a.ticket = 0;   // (read by the launch after this one)
   for (int e = tid; e < G * V * W; e += kBalThreads) hist[e] = 0;
   if (tid == 0) n_tok = 0;
+  float bias[V * W];
+  load_bias<G, V, W>(a.bias, a.E, l, bias);
   const int t0 = blockIdx.x * a.C, t1 = t0 + a.C < a.N ? t0 + a.C : a.N;
-  for (int s = sequence_of(a.seq_start, a.S, t0); s < a.S; ++s) {
+  for (int s = SINGLE ? 0 : sequence_of(a.seq_start, a.S, t0); s < a.S; ++s) {
     int lo = t0, hi = t1;
     if (a.seq_start != nullptr) {
       const int b = clamp_token(a.seq_start[s], a.N), e = clamp_token(a.seq_start[s + 1], a.N);
-      if (b >= t1) break;
+      if (!SINGLE && b >= t1) break;
       lo = b > t0 ? b : t0;
       hi = e < t1 ? e : t1;
     }
-    if (lo >= hi) continue;   // (an empty sequence)
+    if (!SINGLE && lo >= hi) continue;   // (an empty sequence)
     __syncthreads();          // hist and n_tok are cleared, red has been read
     float acc[V * W];
 #pragma unroll
     for (int i = 0; i < V * W; ++i) acc[i] = 0.0f;
     int mine = 0;
+    // a token's logits and first expert id are loaded while the one before it is summed
+    float next[V * W];
+    int next_id = -1;
+    bool next_on = false;
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+      next_on = t < hi && (a.mask == nullptr || a.mask[t] != 0);
+      if (!next_on) return;
+      load_logits<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.E, l, next);
+      if (l < a.k) next_id = a.topk_idx[static_cast<size_t>(t) * a.k + l];
+    };
+    fetch(lo + grp);
     for (int t = lo + grp; t < hi; t += kGroups) {
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
       float p[V * W];
-      token_softmax<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.bias, a.E, l, p);
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) p[i] = next[i];
+      const int id = next_id;
+      const bool on = next_on;
+      fetch(t + kGroups);
+      if (!on) continue;
+      softmax_row<G, V, W>(p, bias);
 #pragma unroll
       for (int i = 0; i < V * W; ++i) acc[i] += p[i];
-      for (int j = l; j < a.k; j += G) {
+      if (l < a.k && static_cast<unsigned>(id) < static_cast<unsigned>(a.E)) atomicAdd(&hist[id], 1);
+      for (int j = l + G; j < a.k; j += G) {
         const int e = a.topk_idx[static_cast<size_t>(t) * a.k + j];
         if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&hist[e], 1);
       }
@@ -165,19 +218,40 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(BalArgs a)
     }
     __syncthreads();
     const size_t slot = static_cast<size_t>(blockIdx.x) + s;
-    for (int e = tid; e < a.E; e += kBalThreads) {
+    float share = 0.0f;   // (E <= kBalThreads: one expert a thread)
+    if (tid < a.E) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kBalWaves; ++w) v += red[w * (G * V * W) + e];
-      a.part_p[slot * a.E + e] = v;
-      a.part_c[slot * a.E + e] = hist[e];
-      hist[e] = 0;
+      for (int w = 0; w < kBalWaves; ++w) v += red[w * (G * V * W) + tid];
+      if constexpr (SINGLE) {
+        const float T = static_cast<float>(n_tok), mean = n_tok > 0 ? v / T : 0.0f;
+        a.counts[tid] = hist[tid];
+        a.prob_mean[tid] = mean;
+        if (n_tok > 0)
+          share = mean * (static_cast<float>(a.E) * static_cast<float>(hist[tid]) / (static_cast<float>(a.k) * T));
+      } else {
+        a.part_p[slot * a.E + tid] = v;
+        a.part_c[slot * a.E + tid] = hist[tid];
+        hist[tid] = 0;
+      }
     }
-    if (tid == 0) {
+    if constexpr (SINGLE) {
+      share = group_sum<kWave>(share);
+      __syncthreads();   // red has been read
+      if (tid % kWave == 0) red[wave] = share;
+      __syncthreads();
+      if (tid == 0) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kBalWaves; ++w) sum += red[w];
+        *a.loss = a.alpha * sum;
+        *a.tokens = n_tok;
+      }
+    } else if (tid == 0) {
       a.part_t[slot] = n_tok;
       n_tok = 0;
     }
-    if (hi == t1) break;
+    if (hi == t1) break;   // (no later sequence has a token here)
   }
 }
 
@@ -192,16 +266,19 @@ __device__ __forceinline__ int block_sum_int(int v, int32_t* red) {
   return v;
 }
 
-// workgroup (experts of block x, sequence y): the chunks' partial sums, then the sequence's
-// share of the loss; the last workgroup to finish adds the shares in their order
-__global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a) {
-  __shared__ float rp[kBalRows][kBalEx];
-  __shared__ int32_t rc[kBalRows][kBalEx];
+// workgroup (`ex` experts of block x, sequence y): the chunks' partial sums, then the sequence's
+// share of the loss; the last workgroup to finish adds the shares in their order.  Every
+// workgroup takes one turn at the ticket, so they are kept to about 64 (610 for 61 sequences of 160
+// experts took 17 us).
+__global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a, int ex) {
+  __shared__ float rp[kBalThreads];
+  __shared__ int32_t rc[kBalThreads];
   __shared__ int32_t ri[kBalWaves];
-  __shared__ float share[kBalThreads];
+  __shared__ float share[kBalWaves];
   __shared__ int last;
-  const int tid = threadIdx.x, el = tid % kBalEx, row = tid / kBalEx;
-  const int e = blockIdx.x * kBalEx + el, s = blockIdx.y;
+  const int rows = kBalThreads / ex;   // (ex is a power of two)
+  const int tid = threadIdx.x, el = tid & (ex - 1), row = tid / ex;
+  const int e = blockIdx.x * ex + el, s = blockIdx.y;
   int lo = 0, hi = a.N;
   if (a.seq_start != nullptr) {
     lo = clamp_token(a.seq_start[s], a.N);
@@ -210,26 +287,34 @@ __global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a) {
   const int c0 = lo < hi ? lo / a.C : 0, c1 = lo < hi ? (hi - 1) / a.C + 1 : 0;   // its chunks
   float p = 0.0f;
   int c = 0, t = 0;
-  for (int i = c0 + row; i < c1; i += kBalRows) {
-    const size_t o = (static_cast<size_t>(i) + s) * a.E + e;
-    if (e < a.E) {
-      p += a.part_p[o];
-      c += a.part_c[o];
+  for (int i = c0 + tid; i < c1; i += kBalThreads) t += a.part_t[i + s];
+  for (int i0 = c0 + row; i0 < c1; i0 += kBalBatch * rows) {
+    float vp[kBalBatch];
+    int vc[kBalBatch];
+#pragma unroll
+    for (int u = 0; u < kBalBatch; ++u) {
+      const int i = i0 + u * rows;
+      const size_t o = (static_cast<size_t>(i) + s) * a.E + e;
+      const bool in = i < c1 && e < a.E;
+      vp[u] = in ? a.part_p[o] : 0.0f;
+      vc[u] = in ? a.part_c[o] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kBalBatch; ++u) {
+      p += vp[u];
+      c += vc[u];
     }
   }
-  for (int i = c0 + tid; i < c1; i += kBalThreads) t += a.part_t[i + s];
-  const int T = block_sum_int(t, ri);
-  rp[row][el] = p;
-  rc[row][el] = c;
-  __syncthreads();
+  rp[tid] = p;
+  rc[tid] = c;
+  const int T = block_sum_int(t, ri);   // (synchronises)
   float part = 0.0f;
   if (row == 0 && e < a.E) {
     float ps = 0.0f;
     int cs = 0;
-#pragma unroll
-    for (int r = 0; r < kBalRows; ++r) {
-      ps += rp[r][el];
-      cs += rc[r][el];
+    for (int r = 0; r < rows; ++r) {
+      ps += rp[r * ex + el];
+      cs += rc[r * ex + el];
     }
     const float mean = T > 0 ? ps / static_cast<float>(T) : 0.0f;
     a.counts[static_cast<size_t>(s) * a.E + e] = cs;
@@ -238,28 +323,32 @@ __global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a) {
       part = mean * (static_cast<float>(a.E) * static_cast<float>(cs) / (static_cast<float>(a.k) * static_cast<float>(T)));
   }
   if (tid == 0 && blockIdx.x == 0) a.tokens[s] = T;
-  if (tid < kWave) {   // (row 0 lies in wave 0: lanes 0 .. kBalEx - 1)
-    part = group_sum<kBalEx>(part);
-    if (tid == 0) {
-      const int id = s * gridDim.x + blockIdx.x;
-      __hip_atomic_store(a.part_l + id, part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      const int n = static_cast<int>(gridDim.x * gridDim.y);
-      last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-    }
+  part = group_sum<kWave>(part);
+  if (tid % kWave == 0) share[tid / kWave] = part;
+  __syncthreads();
+  const int n = static_cast<int>(gridDim.x * gridDim.y);
+  if (tid == 0) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBalWaves; ++w) sum += share[w];
+    const int id = s * gridDim.x + blockIdx.x;
+    __hip_atomic_store(a.part_l + id, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
   }
   __syncthreads();
   if (!last) return;
   float sum = 0.0f;
-  const int n = static_cast<int>(gridDim.x * gridDim.y);
   for (int i = tid; i < n; i += kBalThreads)
     sum += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  share[tid] = sum;
+  sum = group_sum<kWave>(sum);
+  if (tid % kWave == 0) share[tid / kWave] = sum;
   __syncthreads();
-  for (int half = kBalThreads / 2; half > 0; half >>= 1) {
-    if (tid < half) share[tid] += share[tid + half];
-    __syncthreads();
+  if (tid == 0) {
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kBalWaves; ++w) sum += share[w];
+    *a.loss = a.alpha / static_cast<float>(a.S) * sum;
   }
-  if (tid == 0) *a.loss = a.alpha / static_cast<float>(a.S) * share[0];
 }
 
 struct BalBwdArgs {
@@ -275,56 +364,92 @@ struct BalBwdArgs {
   const float* d_gate;
   void* dz;
   int N, E, k, S;
+  int per;             // tokens of a workgroup
   float alpha;
 };
 
+// a workgroup takes `per` consecutive tokens, a group every kGroups-th of them
 template <int G, int V, int W, bool F32>
-__global__ __launch_bounds__(kBalThreads) void balance_backward_kernel(BalBwdArgs a) {
-  constexpr int kGroups = kBalThreads / G;
-  const int l = threadIdx.x % G;
+__global__ __launch_bounds__(kBwdThreads) void balance_backward_kernel(BalBwdArgs a) {
+  constexpr int kGroups = kBwdThreads / G;
+  const int l = threadIdx.x % G, lane = threadIdx.x % kWave;
   const float scale = a.alpha * (a.d_loss != nullptr ? *a.d_loss : 1.0f) / (static_cast<float>(a.S) * static_cast<float>(a.k));
-  for (long long t = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / G; t < a.N;
-       t += static_cast<long long>(gridDim.x) * kGroups) {
+  float bias[V * W], co[V * W];
+  load_bias<G, V, W>(a.bias, a.E, l, bias);
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.per;
+  const long long t1 = t0 + a.per < a.N ? t0 + a.per : a.N;
+  int s = -1, s_hi = 0;   // the sequence whose coefficients co holds, and its end
+  for (long long t = t0 + threadIdx.x / G; t < t1; t += kGroups) {
     float d[V * W];
-#pragma unroll
-    for (int i = 0; i < V * W; ++i) d[i] = 0.0f;
+    load_logits<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.E, l, d);
+    // (slot l of the token, if it has one: its expert, gate and gate gradient)
+    const size_t o = static_cast<size_t>(t) * a.k;
+    int id = -1;
+    float g = 0.0f, dg = 0.0f;
+    if (a.gate != nullptr && l < a.k) {
+      id = a.topk_idx[o + l];
+      g = a.gate[o + l];
+      dg = a.d_gate[o + l];
+    }
     // the token's sequence, if it counts
     bool on = a.mask == nullptr || a.mask[t] != 0;
-    int s = 0;
-    if (a.seq_start != nullptr) {
+    if (s < 0 || t >= s_hi) {   // (tokens come in order: a sequence's coefficients are loaded once)
       s = sequence_of(a.seq_start, a.S, static_cast<int>(t));
-      on = on && s < a.S && a.seq_start[s < a.S ? s : 0] <= t;
-    }
-    if (on) {
-      float p[V * W], co[V * W];
-      token_softmax<G, V, W>(a.z + static_cast<size_t>(t) * a.E, a.bias, a.E, l, p);
-      const float T = static_cast<float>(a.tokens[s]);
-      const float kT = static_cast<float>(a.k) * T, f = T > 0.0f ? scale / (T * T) : 0.0f;
-      float dot = 0.0f;
+      s_hi = a.N;
+      if (a.seq_start != nullptr) s_hi = s < a.S ? a.seq_start[s + 1] : a.N;
+      if (s < a.S) {
+        const float T = static_cast<float>(a.tokens[s]);
+        const float kT = static_cast<float>(a.k) * T, f = T > 0.0f ? scale / (T * T) : 0.0f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = (v * G + l) * W;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const int c = e < a.E ? a.counts[static_cast<size_t>(s) * a.E + e + w] : 0;
-          co[v * W + w] = e < a.E ? f * fmaf(static_cast<float>(a.E), static_cast<float>(c), -kT) : 0.0f;
-          dot = fmaf(p[v * W + w], co[v * W + w], dot);
+        for (int i = 0; i < V * W; ++i) {
+          const int e = ((i / W) * G + l) * W + i % W;
+          const int c = e < a.E ? a.counts[static_cast<size_t>(s) * a.E + e] : 0;
+          co[i] = e < a.E ? f * fmaf(static_cast<float>(a.E), static_cast<float>(c), -kT) : 0.0f;
         }
       }
+    }
+    if (a.seq_start != nullptr) on = on && s < a.S && a.seq_start[s < a.S ? s : 0] <= t;
+    if (on) {
+      softmax_row<G, V, W>(d, bias);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) dot = fmaf(d[i], co[i], dot);
       dot = group_sum<G>(dot);
 #pragma unroll
-      for (int i = 0; i < V * W; ++i) d[i] = p[i] * (co[i] - dot);
+      for (int i = 0; i < V * W; ++i) d[i] *= co[i] - dot;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V * W; ++i) d[i] = 0.0f;
     }
     if (a.gate != nullptr) {
-      const size_t o = static_cast<size_t>(t) * a.k;
-      float sum = 0.0f;
-      for (int j = 0; j < a.k; ++j) sum = fmaf(a.gate[o + j], a.d_gate[o + j], sum);
-      for (int j = 0; j < a.k; ++j) {
-        const int id = a.topk_idx[o + j];
-        const float dj = a.gate[o + j] * (a.d_gate[o + j] - sum);
+      float sum = g * dg;
+      for (int j = l + G; j < a.k; j += G) sum = fmaf(a.gate[o + j], a.d_gate[o + j], sum);
+      sum = group_sum<G>(sum);
+      for (int j0 = 0; j0 < a.k; j0 += G) {   // (more slots than lanes only with few experts)
+        if (j0 > 0) {
+          id = -1;
+          if (j0 + l < a.k) {
+            id = a.topk_idx[o + j0 + l];
+            g = a.gate[o + j0 + l];
+            dg = a.d_gate[o + j0 + l];
+          }
+        }
+        const float mine = g * (dg - sum);
+        const int n = a.k - j0 < G ? a.k - j0 : G;
+        for (int j = 0; j < n; ++j) {
+          int idj;
+          float dj;
+          if constexpr (G == kWave) {
+            idj = __builtin_amdgcn_readlane(id, j);
+            dj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), j));
+          } else {
+            idj = __shfl(id, lane - l + j, kWave);
+            dj = __shfl(mine, lane - l + j, kWave);
+          }
 #pragma unroll
-        for (int i = 0; i < V * W; ++i)
-          if (((i / W) * G + l) * W + i % W == id) d[i] += dj;
+          for (int i = 0; i < V * W; ++i)
+            if (((i / W) * G + l) * W + i % W == idj) d[i] += dj;
+        }
       }
     }
 #pragma unroll
@@ -389,7 +514,7 @@ int chunk_tokens(int N, int E) {
   const int pass = kBalThreads / group_lanes(E, E % 4 == 0 ? 4 : 1);   // tokens the workgroup holds at a time
   const int need = (N + kBalMaxChunks - 1) / kBalMaxChunks;
   const int passes = (need + pass - 1) / pass;
-  return pass * (passes > 4 ? passes : 4);
+  return pass * (passes > 2 ? passes : 2);
 }
 
 struct BalLayout {
@@ -414,7 +539,13 @@ __global__ void balance_clear_kernel(int32_t* ticket) { *ticket = 0; }
 
 }  // namespace
 
-size_t balance_ws_bytes(int N, int E, int S) { return balance_layout(N, E, S).total; }
+// one launch that needs no workspace
+static bool balance_single(const BalLayout& b, int S) { return b.chunks <= 1 && S == 1; }
+
+size_t balance_ws_bytes(int N, int E, int S) {
+  const BalLayout b = balance_layout(N, E, S);
+  return balance_single(b, S) ? 0 : b.total;
+}
 
 hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
                                const int32_t* seq_start, int S, const uint8_t* mask, float alpha, float* loss,
@@ -426,15 +557,21 @@ hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t*
                reinterpret_cast<int32_t*>(w + b.t), reinterpret_cast<float*>(w + b.l),
                reinterpret_cast<int32_t*>(w + b.ticket), loss, counts, prob_mean, tokens};
   const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0;
-  if (b.chunks > 0)
+  const bool single = balance_single(b, S);
+  if (single || b.chunks > 0)
     with_group(E, vec, [&](auto g, auto v, auto wd) {
-      hipLaunchKernelGGL((balance_partial_kernel<g(), v(), wd()>), dim3(b.chunks), dim3(kBalThreads), 0, s, a);
+      if (single)
+        hipLaunchKernelGGL((balance_partial_kernel<g(), v(), wd(), true>), dim3(1), dim3(kBalThreads), 0, s, a);
+      else
+        hipLaunchKernelGGL((balance_partial_kernel<g(), v(), wd(), false>), dim3(b.chunks), dim3(kBalThreads), 0, s, a);
     });
   else
     hipLaunchKernelGGL(balance_clear_kernel, dim3(1), dim3(1), 0, s, a.ticket);
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(balance_total_kernel, dim3((E + kBalEx - 1) / kBalEx, S), dim3(kBalThreads), 0, s, a);
+  if (err != hipSuccess || single) return err;
+  int ex = kBalEx;
+  while (ex < E && static_cast<long long>((E + ex - 1) / ex) * S > 64) ex *= 2;
+  hipLaunchKernelGGL(balance_total_kernel, dim3((E + ex - 1) / ex, S), dim3(kBalThreads), 0, s, a, ex);
   return hipGetLastError();
 }
 
@@ -442,16 +579,19 @@ hipError_t launch_balance_loss_backward(const float* z, const float* bias, const
                                         const int32_t* seq_start, int S, const uint8_t* mask, float alpha,
                                         const int32_t* counts, const int32_t* tokens, const float* d_loss,
                                         const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s) {
-  const BalBwdArgs a = {z, bias, topk_idx, seq_start, mask, counts, tokens, d_loss, gate, d_gate, dz,
-                        N, E, k, S, alpha};
+  BalBwdArgs a = {z, bias, topk_idx, seq_start, mask, counts, tokens, d_loss, gate, d_gate, dz,
+                  N, E, k, S, 0, alpha};
   const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0 && reinterpret_cast<uintptr_t>(dz) % 16 == 0;
   with_group(E, vec, [&](auto g, auto v, auto wd) {
-    const int per = kBalThreads / g();
-    const int blocks = (N + per - 1) / per < 4096 ? (N + per - 1) / per : 4096;
+    // about 2048 workgroups (8 waves a SIMD), each of whole passes
+    const int pass = kBwdThreads / g();
+    const int passes = ((N + pass - 1) / pass + 2047) / 2048;
+    a.per = pass * passes;
+    const int blocks = (N + a.per - 1) / a.per;
     if (f32)
-      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), true>), dim3(blocks), dim3(kBalThreads), 0, s, a);
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), true>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
     else
-      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), false>), dim3(blocks), dim3(kBalThreads), 0, s, a);
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), false>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
   });
   return hipGetLastError();
 }

@@ -517,8 +517,9 @@ moe_status moe_balance_loss(const float* z, const float* bias, const int32_t* to
   if (st != MOE_OK) return st;
   if (loss == nullptr || counts == nullptr || prob_mean == nullptr || tokens == nullptr) return MOE_ERR_INVALID_ARG;
   if (N > 0 && (z == nullptr || topk_idx == nullptr)) return MOE_ERR_INVALID_ARG;
-  if (ws == nullptr || ws_bytes < moe::balance_ws_bytes(N, E, S)) return MOE_ERR_WORKSPACE;
-  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::balance_ws_bytes(N, E, S);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_balance_loss(z, bias, topk_idx, N, E, k, seq_start, S, token_mask, alpha, loss,
                                              counts, prob_mean, tokens, ws, stream));
 }

@@ -9,8 +9,8 @@
 //
 // bf16 operands (fp32 sums) run on v_mfma_f32_32x32x16_bf16 over tiles of TM rows x 128 columns
 // (rows: experts in wgrad, tokens in dgrad), K (tokens; experts) in stages of 32 through a ring of
-// three LDS slots filled by direct-to-LDS loads: while a stage is multiplied, the one after the
-// next loads.  Every stage of an operand is read through a buffer window that ends after its last
+// three LDS slots filled by direct-to-LDS loads two and a half stages ahead, fragments one K step
+// ahead of their MFMAs.  Every stage of an operand is read through a buffer window that ends after its last
 // valid element, so rows past the data load zeros.  Operands whose K index is the slow one (dz and
 // x in wgrad, W_r in dgrad) lie in LDS as in memory and are read transposed.  A wgrad tile row past E
 // and a column past H hold other elements' products and are not stored.  In dgrad the K tail of a
@@ -22,6 +22,7 @@
 //
 // fp32 operands take a plain LDS-tiled kernel with fp32 FMAs.
 #include <hip/hip_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include "gemm_device.h"
@@ -142,7 +143,7 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   auto load_stage = [&](int ks, int sl) __attribute__((always_inline)) {
     const int k0 = k_lo + ks * kRbKS;
     const int left = k_hi - k0 < kRbKS ? k_hi - k0 : kRbKS;
-    const uint32_t base = lds0 + sl * C::kStage;
+    const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + sl * C::kStage);
     if constexpr (DMA) {
       const u32x4_t wa =
           DGRAD ? buffer_window(dz + static_cast<size_t>(m0) * p.E + k0,
@@ -198,80 +199,119 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
 #pragma unroll
     for (int j = 0; j < kNB; ++j) acc[i][j] = f32x16_t{};
 
-  uint4 va[kAOps];
-  load_stage(0, 0);
-  if constexpr (!DMA) {
-    read_a(0, va);
-    put_a(0, va);
-  }
-  if (nk > 1) {
-    load_stage(1, 1);
-    if constexpr (!DMA) {
-      read_a(1, va);
-      put_a(1, va);
-    }
-    wait_vmcnt<kOps>();
-  } else {
-    wait_vmcnt<0>();
-  }
-  wait_lgkmcnt_all();
-  block_barrier();
-  int sl = 0, sl2 = 2;   // ring slots of stages ks and ks + 2
-  for (int ks = 0; ks < nk; ++ks) {
-    const bool more = ks + 2 < nk;
-    if (more) {
-      load_stage(ks + 2, sl2);
-      if constexpr (!DMA) read_a(ks + 2, va);
-    }
+  // ---- K loop.  Stage ks, two K steps of 16, fragments one step ahead of their MFMAs:
+  //   read step 1; multiply step 0; wait for stage ks + 1 and synchronise (every wave has now read
+  //   all of stage ks); load stage ks + 3 into its slot; read step 0 of stage ks + 1; multiply step 1
+  struct Frags {
+    uint4 a[kMB], b[kNB];
+  };
+  auto read_frags = [&](int sl, int s, Frags& f) __attribute__((always_inline)) {
     const uint32_t sb = lds0 + sl * C::kStage;
 #pragma unroll
-    for (int s = 0; s < kRbKS / 16; ++s) {
-      uint4 fa[kMB], fb[kNB];
-#pragma unroll
-      for (int i = 0; i < kMB; ++i) {
-        if constexpr (DGRAD) {
-          fa[i] = __builtin_bit_cast(uint4, *reinterpret_cast<lds_vec16*>(static_cast<uintptr_t>(sb + fo_a[s] + i * 2048)));
-          if (ks == nk - 1 && ks * kRbKS + 16 * s + 8 * (lane >> 5) >= p.E) fa[i] = make_uint4(0, 0, 0, 0);
-        } else {
-          fa[i] = strided_frag<TM * 2>(sb + fo_a[i], s);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kNB; ++j) fb[j] = strided_frag<kRbTN * 2>(sb + fo_b[j], s);
-#pragma unroll
-      for (int i = 0; i < kMB; ++i)
-#pragma unroll
-        for (int j = 0; j < kNB; ++j)
-          acc[i][j] = DGRAD ? mma_bf16(fb[j], fa[i], acc[i][j]) : mma_bf16(fa[i], fb[j], acc[i][j]);
+    for (int i = 0; i < kMB; ++i) {
+      if constexpr (DGRAD)
+        f.a[i] = __builtin_bit_cast(uint4, *reinterpret_cast<lds_vec16*>(static_cast<uintptr_t>(sb + fo_a[s] + i * 2048)));
+      else
+        f.a[i] = strided_frag<TM * 2>(sb + fo_a[i], s);
     }
-    if (ks + 1 < nk) {
-      if constexpr (!DMA) {
-        if (more) put_a(sl2, va);
+#pragma unroll
+    for (int j = 0; j < kNB; ++j) f.b[j] = strided_frag<kRbTN * 2>(sb + fo_b[j], s);
+  };
+  auto multiply = [&](int ks, int s, Frags& f) __attribute__((always_inline)) {
+    if constexpr (DGRAD) {
+      if (ks == nk - 1) {   // dz past the row's end: the next row's values
+        const bool past = ks * kRbKS + 16 * s + 8 * (lane >> 5) >= p.E;
+#pragma unroll
+        for (int i = 0; i < kMB; ++i)
+          if (past) f.a[i] = make_uint4(0, 0, 0, 0);
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j)
+        acc[i][j] = DGRAD ? mma_bf16(f.b[j], f.a[i], acc[i][j]) : mma_bf16(f.a[i], f.b[j], acc[i][j]);
+  };
+  uint4 va[kAOps];
+  auto first_stage = [&](int st) __attribute__((always_inline)) {
+    load_stage(st, st);
+    if constexpr (!DMA) {
+      read_a(st, va);
+      put_a(st, va);
+    }
+  };
+  first_stage(0);
+  if (nk > 1) first_stage(1);
+  if (nk > 2) first_stage(2);
+  if (nk > 2) wait_vmcnt<2 * kOps>();
+  else if (nk > 1) wait_vmcnt<kOps>();
+  else wait_vmcnt<0>();
+  wait_lgkmcnt_all();
+  block_barrier();
+  constexpr int kLanes = kNB * 4;                    // dgrad epilogue: lanes along a row, 8 columns each
+  constexpr int kRest = DGRAD ? 32 * kLanes / 64 : 1;   // and the 16-byte words of rest they add
+  uint4 rest_w[kMB][kRest];
+  const uint16_t* rest = reinterpret_cast<const uint16_t*>(p.rest);
+  auto load_rest = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < kRest; ++t) {
+      const int row = m0 + wm * 64 + i * 32 + t * (64 / kLanes) + lane / kLanes;
+      const int col = n0 + wn * kNB * 32 + 8 * (lane % kLanes);
+      rest_w[i][t] = rest != nullptr && row < p.N && col < p.H
+                         ? *reinterpret_cast<const uint4*>(rest + static_cast<size_t>(row) * p.H + col)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  Frags f0, f1;
+  read_frags(0, 0, f0);
+  int sl = 0;   // ring slot of stage ks
+  for (int ks = 0; ks < nk; ++ks) {
+    const bool next = ks + 1 < nk, load = ks + kRbSlots < nk;
+    if constexpr (!DMA) {
+      if (load) read_a(ks + kRbSlots, va);
+    }
+    read_frags(sl, 1, f1);
+    if constexpr (DGRAD) {
+      if (!next) load_rest(0);   // (no load to LDS is in flight: nothing waits for these early)
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(ks, 0, f0);
+    const int sl1 = sl + 1 == kRbSlots ? 0 : sl + 1;
+    if (next) {
       wait_lgkmcnt_all();
-      if (more) wait_vmcnt<kOps>();
+      if (ks + 2 < nk) wait_vmcnt<kOps>();
       else wait_vmcnt<0>();
       block_barrier();
+      if (load) {
+        load_stage(ks + kRbSlots, sl);
+        if constexpr (!DMA) put_a(sl, va);
+      }
+      read_frags(sl1, 0, f0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    sl = sl + 1 == kRbSlots ? 0 : sl + 1;
-    sl2 = sl2 + 1 == kRbSlots ? 0 : sl2 + 1;
+    multiply(ks, 1, f1);
+    sl = sl1;
   }
 
   if constexpr (!DGRAD) {
     // lane l holds column l % 32 of a block and, in register v, row 8 (v / 4) + 4 (l / 32) + v % 4:
-    // each store writes two rows' 128 bytes
+    // each store writes two rows' 128 bytes, through a window that ends with the tile's last
+    // element (lanes past the columns take an offset behind it)
+    const uint32_t esz = p.out_f32 ? 4 : 2;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(p.out) + ((static_cast<size_t>(part) * p.E + m0) * p.H + n0) * esz;
+    const __amdgpu_buffer_rsrc_t win = __builtin_amdgcn_make_buffer_rsrc(
+        base, 0, static_cast<int>((static_cast<uint32_t>(mcount - 1) * p.H + ncols) * esz), 0x00020000);
 #pragma unroll
     for (int i = 0; i < kMB; ++i)
 #pragma unroll
       for (int j = 0; j < kNB; ++j) {
-        const int n = n0 + (wn * kNB + j) * 32 + (lane & 31);
+        const int n = (wn * kNB + j) * 32 + (lane & 31);
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-          const int e = m0 + wm * 64 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-          if (e >= p.E || n >= p.H) continue;
-          const size_t o = (static_cast<size_t>(part) * p.E + e) * p.H + n;
-          if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = acc[i][j][v];
-          else reinterpret_cast<uint16_t*>(p.out)[o] = f32_to_bf16(acc[i][j][v]);
+          const int r = wm * 64 + i * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+          const int off = n < ncols ? static_cast<int>((static_cast<uint32_t>(r) * p.H + n) * esz) : INT_MIN;
+          if (p.out_f32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][v]), win, off, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(acc[i][j][v]), win, off, 0, 0);
         }
       }
   } else {
@@ -280,10 +320,9 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
     wait_lgkmcnt_all();
     block_barrier();   // every wave is past its last fragment reads
     float* st = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
-    constexpr int kLanes = kNB * 4;   // lanes along a row
-    const uint16_t* rest = reinterpret_cast<const uint16_t*>(p.rest);
 #pragma unroll
     for (int i = 0; i < kMB; ++i) {
+      if (i + 1 < kMB) load_rest(i + 1);
 #pragma unroll
       for (int j = 0; j < kNB; ++j)
 #pragma unroll
@@ -296,7 +335,7 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
       __builtin_amdgcn_wave_barrier();
       wait_lgkmcnt_all();
 #pragma unroll
-      for (int t = 0; t < 32 * kLanes / 64; ++t) {
+      for (int t = 0; t < kRest; ++t) {
         const int r = t * (64 / kLanes) + lane / kLanes, c = 8 * (lane % kLanes);
         const int row = m0 + wm * 64 + i * 32 + r, col = n0 + wn * kNB * 32 + c;
         if (row >= p.N || col >= p.H) continue;
@@ -304,14 +343,12 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
         const float4 y = *reinterpret_cast<const float4*>(st + r * kPitch + c + 4);
         float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         const size_t o = static_cast<size_t>(row) * p.H + col;
-        if (rest != nullptr) {
-          const uint4 q = *reinterpret_cast<const uint4*>(rest + o);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        const uint4 q = rest_w[i][t];
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[2 * k] += __uint_as_float(w[k] << 16);
-            v[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-          }
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] += __uint_as_float(w[k] << 16);
+          v[2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
         }
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + o) =
             make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
@@ -341,16 +378,30 @@ __global__ __launch_bounds__(kRbThreads) void router_grad_f32_kernel(RbArgs p) {
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  for (int k0 = k_lo; k0 < k_hi; k0 += 16) {
-    for (int i = threadIdx.x; i < 64 * 16; i += kRbThreads) {
+  // the next step's elements are loaded while this one is multiplied
+  float ra[4], rb[4];
+  auto load = [&](int k0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = threadIdx.x + u * kRbThreads;
       // (the index that is contiguous in memory runs fastest)
       const int kk = DGRAD ? i & 15 : i >> 6, r = DGRAD ? i >> 4 : i & 63;
       const int k = k0 + kk, m = m0 + r;
-      as[kk][r] = k < k_hi && m < M ? dz[DGRAD ? static_cast<size_t>(m) * p.E + k : static_cast<size_t>(k) * p.E + m] : 0.0f;
-      const int kb = i >> 6, n = n0 + (i & 63);
-      bs[kb][i & 63] = k0 + kb < k_hi && n < p.H ? b[static_cast<size_t>(k0 + kb) * p.H + n] : 0.0f;
+      ra[u] = k < k_hi && m < M ? dz[DGRAD ? static_cast<size_t>(m) * p.E + k : static_cast<size_t>(k) * p.E + m] : 0.0f;
+      const int kb = k0 + (i >> 6), n = n0 + (i & 63);
+      rb[u] = kb < k_hi && n < p.H ? b[static_cast<size_t>(kb) * p.H + n] : 0.0f;
+    }
+  };
+  load(k_lo);
+  for (int k0 = k_lo; k0 < k_hi; k0 += 16) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = threadIdx.x + u * kRbThreads;
+      as[DGRAD ? i & 15 : i >> 6][DGRAD ? i >> 4 : i & 63] = ra[u];
+      bs[i >> 6][i & 63] = rb[u];
     }
     __syncthreads();
+    if (k0 + 16 < k_hi) load(k0 + 16);
 #pragma unroll
     for (int kk = 0; kk < 16; ++kk) {
       float a[4], c[4];
@@ -388,12 +439,18 @@ __global__ __launch_bounds__(kRbThreads) void router_wgrad_sum_kernel(const floa
   const long long step = static_cast<long long>(gridDim.x) * kRbThreads;
   for (long long i = static_cast<long long>(blockIdx.x) * kRbThreads + threadIdx.x; i < n4; i += step) {
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < S; ++s) {
-      const float4 b = part[s * n4 + i];
-      a.x += b.x;
-      a.y += b.y;
-      a.z += b.z;
-      a.w += b.w;
+    for (int s0 = 0; s0 < S; s0 += 8) {   // (eight parts' loads together)
+      float4 b[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        b[u] = s0 + u < S ? part[(s0 + u) * n4 + i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        a.x += b[u].x;
+        a.y += b[u].y;
+        a.z += b[u].z;
+        a.w += b[u].w;
+      }
     }
     if (f32) reinterpret_cast<float4*>(dw)[i] = a;
     else reinterpret_cast<uint2*>(dw)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));

@@ -517,7 +517,8 @@ moe_status moe_router_backward(const float* topk_gate, const float* d_gate, int 
  *   token_mask [N] bytes, or NULL: tokens with 0 (padding) do not count.
  *   loss       [1] fp32 out; counts [S, E] int32 out (c_s); prob_mean [S, E] fp32 out (P_s; 0
  *              for a sequence without tokens); tokens [S] int32 out (T_s).
- *   ws         workspace of moe_workspace_bytes(MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0) bytes.
+ *   ws         workspace of moe_workspace_bytes(MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0) bytes (may
+ *              be 0: then ws may be NULL).
  * Sums are fp32 in a fixed order: the same inputs give the same bits.  Logits of -inf have
  * probability 0, and a token whose logits are all -inf has none; a NaN or +inf logit of a
  * counted token makes its sequence's P and the loss NaN, one of an uncounted token does nothing.

@@ -67,8 +67,8 @@ def _check(c, alpha=0.03, d_loss=1.7, dz_dtype=torch.float32, gates=False):
     rl, rc, rp, rt = oracle.balance_loss(alpha=alpha, **c)
     assert np.array_equal(counts.cpu().numpy(), rc) and np.array_equal(tokens.cpu().numpy(), rt)
     rel = _prob_rel(c)
-    # a mean: at most N / 512 + 4 passes of a chunk, 512 / 16 partials a row, and trees of 6, 4 and
-    # 16 adds, each rounding once; all terms are positive
+    # a mean of positive terms: at most N / 512 + 2 passes of a chunk, 5 steps across a wave's groups,
+    # 16 waves, 8 partials a row and 64 rows, each adding once: N / 512 + 95 roundings
     mean_rel = rel + 2 * U32 * (N / 512 + 4 + 32 + 26)
     assert np.all(np.abs(f64(prob) - rp) <= mean_rel * rp + 1e-37)
     # the loss adds at most 2^16 positive shares: 256 a thread and an 8-step tree, 6 products
@@ -78,7 +78,7 @@ def _check(c, alpha=0.03, d_loss=1.7, dz_dtype=torch.float32, gates=False):
     # products within rel + a 22-step sum
     zb = oracle.biased_logits(c["z"], c["bias"])
     bound = np.zeros((N, E))
-    starts = [0, N] if c["seq_start"] is None else c["seq_start"]
+    starts = [0, N] if c["seq_start"] is None else np.clip(c["seq_start"], 0, N)
     for s, (lo, hi) in enumerate(zip(starts, starts[1:])):
         if rt[s] == 0 or lo >= hi:
             continue
@@ -220,3 +220,18 @@ def test_two_streams_and_a_captured_graph():
         want = _loss(n, 0.1)
         assert all(torch.equal(x, y) for x, y in zip(want, out))
         assert torch.equal(dz, _grad(n, 0.1, want[1], want[3]))
+
+
+def test_one_chunk_of_one_listed_sequence():
+    """A batch small enough for one launch whose only sequence is listed: a part of the batch, all of
+    it, none of it, and outside it."""
+    say("balance: one listed sequence")
+    for lo, hi in ((3, 20), (0, 25), (9, 9), (40, 50), (-5, 7), (20, 3)):
+        c = _case(25, 60, 4, seed=30)
+        c["seq_start"] = np.array([lo, hi], np.int32)
+        if lo <= hi:
+            _check(c, gates=True)
+        else:   # (not a valid list: no token)
+            loss, counts, _, tokens = _loss(c, 0.1)
+            sync()
+            assert float(loss) == 0 and not counts.any() and not tokens.any()
