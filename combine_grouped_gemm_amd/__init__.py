@@ -186,8 +186,8 @@ def _expect(name: str, t: Optional[torch.Tensor], shape, dtypes, device) -> None
 
 def _run(fn: str, device: torch.device, *args) -> None:
     """Calls a C entry point with `device` as the current one."""
-    f = getattr(lib(), fn)
-    if device.index == torch.cuda.current_device():
+    f = getattr(_LIB or lib(), fn)
+    if device.index == torch._C._cuda_getDevice():
         status = f(*args)
     else:
         with torch.cuda.device(device):
@@ -643,9 +643,8 @@ def moe_balance_loss(z: torch.Tensor, topk_idx: torch.Tensor, alpha: float, bias
     N, E, k, S = _balance_args(z, topk_idx, bias, seq_start, token_mask)
     dev = z.device
     if out is None:
-        loss, tokens = torch.empty(1, dtype=torch.float32, device=dev), torch.empty(S, dtype=torch.int32, device=dev)
-        counts = torch.empty((S, E), dtype=torch.int32, device=dev)
-        prob_mean = torch.empty((S, E), dtype=torch.float32, device=dev)
+        loss, prob_mean = z.new_empty(1), z.new_empty((S, E))
+        tokens, counts = topk_idx.new_empty(S), topk_idx.new_empty((S, E))
     else:
         loss, counts, prob_mean, tokens = out
         _expect("loss", loss, (1,), _F32, dev)

@@ -20,7 +20,7 @@
 // wgrad has few tiles (E / TM x H / 128), so the tokens are cut into S ranges whose fp32 partial
 // sums a second launch adds in order: the result has the same bits on every run.
 //
-// fp32 operands take a plain LDS-tiled kernel with fp32 FMAs.
+// fp32 operands run on v_mfma_f32_32x32x2_f32 (products and sums in fp32).
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -360,75 +360,89 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   }
 }
 
-// fp32: 64 rows x 64 columns per workgroup, thread (ty, tx) of 16 x 16 owns rows ty + 16 i and
-// columns tx + 16 j; K in steps of 16 through LDS
+// fp32: tiles of 64 rows x 128 columns on v_mfma_f32_32x32x2_f32 (4 waves of 32 x 64; lane l supplies
+// row l % 32 at k = l / 32 of both operands), K in steps of 16 through two LDS buffers, the next
+// step's elements in registers meanwhile.  Both operands lie k-row after k-row, rows padded so that
+// the two k-rows of a fragment read fall into different halves of the banks.
+constexpr int kF32TM = 64, kF32TN = 128, kF32KS = 16;
+constexpr int kF32APitch = kF32TM + 32, kF32BPitch = kF32TN + 32;
+static_assert(kF32APitch % 64 == 32 && kF32BPitch % 64 == 32, "k-rows alternate between the bank halves");
+
 template <bool DGRAD>
 __global__ __launch_bounds__(kRbThreads) void router_grad_f32_kernel(RbArgs p) {
-  __shared__ float as[16][65];
-  __shared__ float bs[16][65];
+  __shared__ float as[2][kF32KS][kF32APitch];
+  __shared__ __attribute__((aligned(16))) float bs[2][kF32KS][kF32BPitch];
   const float* dz = reinterpret_cast<const float*>(p.dz);
   const float* b = reinterpret_cast<const float*>(p.b);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.x * 64, n0 = blockIdx.y * 64, part = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 63, wm = tid >> 7, wn = (tid >> 6) & 1;
+  const int m0 = blockIdx.x * kF32TM, n0 = blockIdx.y * kF32TN, part = blockIdx.z;
   const int M = DGRAD ? p.N : p.E;
   const int k_lo = DGRAD ? 0 : part * p.span;
   const int k_hi = DGRAD ? p.E : (k_lo + p.span < p.N ? k_lo + p.span : p.N);
-  float acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  // the next step's elements are loaded while this one is multiplied
-  float ra[4], rb[4];
+  const bool vec = p.E % 4 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0;   // dz rows by 16 bytes
+  // A: 4 elements a thread, contiguous in memory: wgrad expert run 4 (tid % 16) of token tid / 16;
+  // dgrad expert run 4 (tid / 64) of token tid % 64
+  const int ak = DGRAD ? 4 * (tid >> 6) : tid >> 4, am = DGRAD ? tid & 63 : 4 * (tid & 15);
+  // B: columns 4 (tid % 32) .. + 3 of k-rows tid / 32 and tid / 32 + 8
+  const int bk = tid >> 5, bn = 4 * (tid & 31);
+  float ra[4];
+  float4 rb[2];
   auto load = [&](int k0) __attribute__((always_inline)) {
+    const int row = DGRAD ? m0 + am : k0 + ak, col = DGRAD ? k0 + ak : m0 + am;   // of dz
+    const bool in = row < (DGRAD ? M : k_hi);
+    const float* at = dz + static_cast<size_t>(row) * p.E + col;
+    if (vec) {
+      const float4 q = in && col < p.E ? *reinterpret_cast<const float4*>(at) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ra[0] = q.x; ra[1] = q.y; ra[2] = q.z; ra[3] = q.w;
+    } else {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = threadIdx.x + u * kRbThreads;
-      // (the index that is contiguous in memory runs fastest)
-      const int kk = DGRAD ? i & 15 : i >> 6, r = DGRAD ? i >> 4 : i & 63;
-      const int k = k0 + kk, m = m0 + r;
-      ra[u] = k < k_hi && m < M ? dz[DGRAD ? static_cast<size_t>(m) * p.E + k : static_cast<size_t>(k) * p.E + m] : 0.0f;
-      const int kb = k0 + (i >> 6), n = n0 + (i & 63);
-      rb[u] = kb < k_hi && n < p.H ? b[static_cast<size_t>(kb) * p.H + n] : 0.0f;
+      for (int i = 0; i < 4; ++i) ra[i] = in && col + i < p.E ? at[i] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int k = k0 + bk + 8 * u, n = n0 + bn;
+      rb[u] = k < k_hi && n < p.H ? *reinterpret_cast<const float4*>(b + static_cast<size_t>(k) * p.H + n)
+                                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // (H % 4 == 0)
     }
   };
+  auto store = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) as[buf][DGRAD ? ak + i : ak][DGRAD ? am : am + i] = ra[i];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) *reinterpret_cast<float4*>(&bs[buf][bk + 8 * u][bn]) = rb[u];
+  };
+  f32x16_t acc[2] = {};
   load(k_lo);
-  for (int k0 = k_lo; k0 < k_hi; k0 += 16) {
+  store(0);
+  __syncthreads();
+  int buf = 0;
+  for (int k0 = k_lo; k0 < k_hi; k0 += kF32KS) {
+    const bool next = k0 + kF32KS < k_hi;
+    if (next) load(k0 + kF32KS);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = threadIdx.x + u * kRbThreads;
-      as[DGRAD ? i & 15 : i >> 6][DGRAD ? i >> 4 : i & 63] = ra[u];
-      bs[i >> 6][i & 63] = rb[u];
+    for (int s = 0; s < kF32KS / 2; ++s) {
+      const int k = 2 * s + (lane >> 5);
+      const float fa = as[buf][k][wm * 32 + (lane & 31)];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa, bs[buf][k][wn * 64 + j * 32 + (lane & 31)], acc[j], 0, 0, 0);
     }
+    if (next) store(buf ^ 1);
     __syncthreads();
-    if (k0 + 16 < k_hi) load(k0 + 16);
-#pragma unroll
-    for (int kk = 0; kk < 16; ++kk) {
-      float a[4], c[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = as[kk][ty + 16 * i];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) c[j] = bs[kk][tx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], c[j], acc[i][j]);
-    }
-    __syncthreads();
+    buf ^= 1;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + ty + 16 * i;
-    if (m >= M) continue;
+  for (int j = 0; j < 2; ++j) {
+    const int n = n0 + wn * 64 + j * 32 + (lane & 31);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 16 * j;
-      if (n >= p.H) continue;
-      float v = acc[i][j];
+    for (int v = 0; v < 16; ++v) {
+      const int m = m0 + wm * 32 + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+      if (m >= M || n >= p.H) continue;
+      float x = acc[j][v];
       const size_t o = (static_cast<size_t>(DGRAD ? 0 : part) * M + m) * p.H + n;
-      if (DGRAD && p.rest != nullptr) v += reinterpret_cast<const float*>(p.rest)[o];
-      if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = v;
-      else reinterpret_cast<uint16_t*>(p.out)[o] = f32_to_bf16(v);
+      if (DGRAD && p.rest != nullptr) x += reinterpret_cast<const float*>(p.rest)[o];
+      if (p.out_f32) reinterpret_cast<float*>(p.out)[o] = x;
+      else reinterpret_cast<uint16_t*>(p.out)[o] = f32_to_bf16(x);
     }
   }
 }
@@ -464,7 +478,7 @@ struct RbSplit {
   int S, span;
 };
 RbSplit rb_split(int N, int H, int E, bool bf16) {
-  const int tm = bf16 ? rb_tile_rows(E) : 64, tn = bf16 ? kRbTN : 64, step = bf16 ? kRbKS : 16;
+  const int tm = bf16 ? rb_tile_rows(E) : kF32TM, tn = bf16 ? kRbTN : kF32TN, step = bf16 ? kRbKS : kF32KS;
   const long long tiles = static_cast<long long>((E + tm - 1) / tm) * ((H + tn - 1) / tn);
   long long S = tiles >= 512 ? 1 : 512 / tiles;
   const long long most = (N + 2 * step - 1) / (2 * step);
@@ -512,7 +526,8 @@ hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, i
     if (bf16) {
       err = rb_run<false>(p, s);
     } else {
-      hipLaunchKernelGGL(router_grad_f32_kernel<false>, dim3((E + 63) / 64, (H + 63) / 64, r.S), dim3(kRbThreads), 0, s, p);
+      hipLaunchKernelGGL(router_grad_f32_kernel<false>,
+                         dim3((E + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN, r.S), dim3(kRbThreads), 0, s, p);
       err = hipGetLastError();
     }
     if (err != hipSuccess || r.S == 1) return err;
@@ -528,7 +543,8 @@ hipError_t launch_router_dense_dgrad(const void* dz, const void* w_r, bool bf16,
                                      void* dx, hipStream_t s) {
   const RbArgs p = {dz, w_r, rest, dx, N, E, H, 1, 0, bf16 ? 0 : 1};
   if (bf16) return rb_run<true>(p, s);
-  hipLaunchKernelGGL(router_grad_f32_kernel<true>, dim3((N + 63) / 64, (H + 63) / 64), dim3(kRbThreads), 0, s, p);
+  hipLaunchKernelGGL(router_grad_f32_kernel<true>, dim3((N + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN),
+                     dim3(kRbThreads), 0, s, p);
   return hipGetLastError();
 }
 
