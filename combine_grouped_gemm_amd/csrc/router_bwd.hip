@@ -232,6 +232,28 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
       for (int j = 0; j < kNB; ++j)
         acc[i][j] = DGRAD ? mma_bf16(f.b[j], f.a[i], acc[i][j]) : mma_bf16(f.a[i], f.b[j], acc[i][j]);
   };
+  constexpr int kLanes = kNB * 4;                    // dgrad epilogue: lanes along a row, 8 columns each
+  constexpr int kRest = DGRAD ? 32 * kLanes / 64 : 1;   // and the 16-byte words of rest they add
+  uint4 rest_w[kMB][kRest];
+  const uint16_t* rest = reinterpret_cast<const uint16_t*>(p.rest);
+  auto load_rest = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < kRest; ++t) {
+      const int row = m0 + wm * 64 + i * 32 + t * (64 / kLanes) + lane / kLanes;
+      const int col = n0 + wn * kNB * 32 + 8 * (lane % kLanes);
+      rest_w[i][t] = rest != nullptr && row < p.N && col < p.H
+                         ? *reinterpret_cast<const uint4*>(rest + static_cast<size_t>(row) * p.H + col)
+                         : make_uint4(0, 0, 0, 0);
+    }
+  };
+  // rest is read ahead of everything else, as far as registers go (256-row tiles: the first of the
+  // wave's two row blocks, the second in the epilogue); read where it is added it cost 7 us of 60
+  // at N 8192, E 8, H 7168
+  constexpr int kEarly = TM < 256 ? kMB : 1;
+  if constexpr (DGRAD) {
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i) load_rest(i);
+  }
   uint4 va[kAOps];
   auto first_stage = [&](int st) __attribute__((always_inline)) {
     load_stage(st, st);
@@ -248,20 +270,6 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   else wait_vmcnt<0>();
   wait_lgkmcnt_all();
   block_barrier();
-  constexpr int kLanes = kNB * 4;                    // dgrad epilogue: lanes along a row, 8 columns each
-  constexpr int kRest = DGRAD ? 32 * kLanes / 64 : 1;   // and the 16-byte words of rest they add
-  uint4 rest_w[kMB][kRest];
-  const uint16_t* rest = reinterpret_cast<const uint16_t*>(p.rest);
-  auto load_rest = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < kRest; ++t) {
-      const int row = m0 + wm * 64 + i * 32 + t * (64 / kLanes) + lane / kLanes;
-      const int col = n0 + wn * kNB * 32 + 8 * (lane % kLanes);
-      rest_w[i][t] = rest != nullptr && row < p.N && col < p.H
-                         ? *reinterpret_cast<const uint4*>(rest + static_cast<size_t>(row) * p.H + col)
-                         : make_uint4(0, 0, 0, 0);
-    }
-  };
   Frags f0, f1;
   read_frags(0, 0, f0);
   int sl = 0;   // ring slot of stage ks
@@ -271,9 +279,6 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
       if (load) read_a(ks + kRbSlots, va);
     }
     read_frags(sl, 1, f1);
-    if constexpr (DGRAD) {
-      if (!next) load_rest(0);   // (no load to LDS is in flight: nothing waits for these early)
-    }
     __builtin_amdgcn_sched_barrier(0);
     multiply(ks, 0, f0);
     const int sl1 = sl + 1 == kRbSlots ? 0 : sl + 1;
@@ -322,7 +327,7 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
     float* st = reinterpret_cast<float*>(lds) + wave * 32 * kPitch;
 #pragma unroll
     for (int i = 0; i < kMB; ++i) {
-      if (i + 1 < kMB) load_rest(i + 1);
+      if (i + 1 < kMB && i + 1 >= kEarly) load_rest(i + 1);
 #pragma unroll
       for (int j = 0; j < kNB; ++j)
 #pragma unroll
@@ -472,6 +477,10 @@ __global__ __launch_bounds__(kRbThreads) void router_wgrad_sum_kernel(const floa
 }
 
 int rb_tile_rows(int rows) { return rows > 128 ? 256 : (rows > 64 ? 128 : 64); }
+// dgrad: 256 tokens halve the reads of W_r, but two workgroups fit a CU; up to 128 experts the reads and
+// writes of rest and dx count for more, and three workgroups of 128 tokens keep more of them in
+// flight (N 8192, H 7168, E 64: 57 us against 59; E 256: 85 against 81)
+int rb_dgrad_rows(int N, int E) { return E <= 128 && N > 64 ? 128 : rb_tile_rows(N); }
 
 // token ranges of a wgrad: about two workgroups per CU, ranges of whole stages and at least two
 struct RbSplit {
@@ -501,7 +510,7 @@ hipError_t rb_launch(const RbArgs& p, bool dma, long long tiles, hipStream_t s) 
 template <bool DGRAD>
 hipError_t rb_run(const RbArgs& p, hipStream_t s) {
   const int rows = DGRAD ? p.N : p.E;
-  const int tm = rb_tile_rows(rows);
+  const int tm = DGRAD ? rb_dgrad_rows(p.N, p.E) : rb_tile_rows(p.E);
   const long long tiles = static_cast<long long>((rows + tm - 1) / tm) * ((p.H + kRbTN - 1) / kRbTN) * (DGRAD ? 1 : p.S);
   const bool dma = p.E % 8 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0;
   if (tm == 256) return rb_launch<DGRAD, 256>(p, dma, tiles, s);
