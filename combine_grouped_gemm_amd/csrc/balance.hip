@@ -18,6 +18,10 @@
 // the chunk meets (slot chunk + sequence: along the tokens every step to the next pair raises
 // one of the two, so slots are distinct and at most chunks + S - 1); a second launch adds a
 // sequence's slots.  Counts are integers, added atomically in LDS: their order does not matter.
+//
+// Measured: N 8192, E 256, k 8: 5.0 us (8.4 MB of logits) + 6.4 us and, with the gates, 8.6 us
+// backward: latencies (loads, the ticket).  N 32768, E 160, 61 sequences: 13.4 + 5.9 and 15.6 us: the
+// softmax's vector instructions (24 of 64 lanes hold no expert there).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -10,8 +10,11 @@
 // The gates' gradient needs no expert outputs: <dy, W_down h> = <W_down^T dy, h>.  With g folded
 // into h_out the weight gradient is dW_down = dy^T (g h) over the plain permuted dy.
 //
-// All three move each byte once; a lane takes 8 adjacent columns (8 bytes of codes, 16 of bf16), four
-// lanes a block, and a wave's accesses are contiguous.
+// All three move each byte once and are bound by memory; a lane takes 8 adjacent columns (8 bytes of
+// codes, 16 of bf16), four lanes a block, so that a wave's accesses are contiguous, and every stream
+// is touched once (non-temporal).  Measured, bf16: 8191 x 7168 quantized in 31 us (5.8 TB/s) and
+// written to 8 expert-ordered rows each in 178 us (5.6 TB/s); SwiGLU backward of 65536 slots of I
+// 2048 with gates in 266 us (5.06 TB/s; a 1 GiB copy on the card: 5.15).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -228,8 +231,11 @@ static hipError_t swiglu_mx(const uint8_t* au, const uint8_t* au_scale, const vo
   hipLaunchKernelGGL((swiglu_backward_mx_kernel<F32, TPR_>),                                                      \
                      dim3(static_cast<unsigned>((static_cast<long long>(slots) * TPR_ + kCkThreads - 1) / kCkThreads)), \
                      dim3(kCkThreads), 0, s, au, au_scale, dh, rows, I, slots, send_pos, gate, d_au, h, d_gate)
+  // lanes of a slot by its width (us with 16 / 64 / 256 lanes):
+  //   65536 slots of I 64: 10 / 24 / 53, of I 256: 31 / 31 / 64, of I 512: 62 / 56 / 69,
+  //   of I 2048: 257 / 224 / 226; 256 slots of I 2048: 11 / 4.6 / 3.1, of I 14336: 93 / 28 / 12
   if (I <= 256) MOE_SWIGLU_MX(16);
-  else if (slots >= 4096) MOE_SWIGLU_MX(64);
+  else if (I < 2048) MOE_SWIGLU_MX(64);
   else MOE_SWIGLU_MX(256);
 #undef MOE_SWIGLU_MX
   return hipGetLastError();

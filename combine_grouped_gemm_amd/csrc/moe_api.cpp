@@ -52,7 +52,8 @@ moe_status check_balance(int N, int E, int k, const int32_t* seq_start, int S) {
   if (N < 0 || E < 1 || k < 1 || k > E || S < 1) return MOE_ERR_INVALID_ARG;
   if (seq_start == nullptr && S != 1) return MOE_ERR_INVALID_ARG;
   if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || S > 65535) return MOE_ERR_UNSUPPORTED;
-  if ((static_cast<long long>(N) + S) * E >= (1ll << 31) || static_cast<long long>(N) * k >= (1ll << 31))
+  if ((static_cast<long long>(N) + S) * E >= (1ll << 31) || static_cast<long long>(N) * k >= (1ll << 31) ||
+      N >= (1 << 30))   // (token numbers plus a chunk stay below 2^31)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -21,6 +21,10 @@
 // sums a second launch adds in order: the result has the same bits on every run.
 //
 // fp32 operands run on v_mfma_f32_32x32x2_f32 (products and sums in fp32).
+//
+// Measured, bf16, N 8192, E 256, H 7168: wgrad 54 us + 11 us for the sum of 9 parts (bound by the
+// 66 MB of partial sums behind the 117 MB of x); dgrad with rest 75 us (60 us of it are rest and dx, as
+// with E = 8; the rest grows by 0.11 us an expert with the direct-to-LDS loads).
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <stdint.h>
@@ -483,6 +487,8 @@ int rb_tile_rows(int rows) { return rows > 128 ? 256 : (rows > 64 ? 128 : 64); }
 int rb_dgrad_rows(int N, int E) { return E <= 128 && N > 64 ? 128 : rb_tile_rows(N); }
 
 // token ranges of a wgrad: about two workgroups per CU, ranges of whole stages and at least two
+// (bf16, N 8192, E 256, H 7168, sum included: 4 / 8 / 9 / 16 ranges 53 / 51 / 50 / 68 us; fp32, N 2048, E 128,
+// H 8192, 256 / 512 / 1024 workgroups: 84 / 59 / 57 us, E 64, H 4096: 28 / 24 / 27)
 struct RbSplit {
   int S, span;
 };

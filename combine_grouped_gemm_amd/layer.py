@@ -306,10 +306,13 @@ class MoELayer:
         pre-activations as 8-bit codes (self.kept_x, self.kept_au); backward then reads nothing
         else of the forward but the routes, neither x nor the expert outputs.
         balance_alpha: also the balance loss of the batch's routes, into self.balance, and its
-        gradient in the next backward (seq_start, token_mask: see moe_balance_loss)."""
-        if save_for_backward not in (False, True, "mxfp8"):
+        gradient in the next backward (seq_start, token_mask: see moe_balance_loss; they, and z
+        if it was passed, stay as they are until then)."""
+        if isinstance(save_for_backward, str) and save_for_backward != "mxfp8":
             raise ValueError('save_for_backward is False, True or "mxfp8"')
-        self.keep8 = save_for_backward == "mxfp8"
+        if balance_alpha is None and (seq_start is not None or token_mask is not None):
+            raise ValueError("seq_start and token_mask belong to a balance loss (balance_alpha)")
+        self.keep8 = isinstance(save_for_backward, str)
         if self.keep8 and (self.dtype != "bf16" or not self.gather or (self.shared and not self.fuse)):
             raise ValueError("8-bit keeping is built for bf16 layers that gather their rows from x and run a shared "
                              "expert inside the routed launches")
@@ -417,6 +420,8 @@ class MoELayer:
         keep8, dense = self.keep8, self.balance_args is not None
         if self.gate_in_down and not keep8:
             raise ValueError("backward needs the unscaled expert outputs (gate_in_down=False)")
+        if d_loss is not None and not dense:
+            raise ValueError("d_loss is the gradient of a balance loss, and the forward had none (balance_alpha)")
         if x is None and not keep8:
             raise ValueError('backward needs x unless the forward kept it (save_for_backward="mxfp8")')
         self._alloc_backward(dw_dtype)

@@ -523,7 +523,7 @@ moe_status moe_router_backward(const float* topk_gate, const float* d_gate, int 
  * probability 0, and a token whose logits are all -inf has none; a NaN or +inf logit of a
  * counted token makes its sequence's P and the loss NaN, one of an uncounted token does nothing.
  * N == 0 is valid and writes zeros.  Requires k <= min(E, 32), E <= 1024, S <= 65535,
- * (N + S) E < 2^31 and N k < 2^31.
+ * N < 2^30, (N + S) E < 2^31 and N k < 2^31.
  */
 moe_status moe_balance_loss(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
                             const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha, float* loss,

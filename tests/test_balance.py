@@ -69,6 +69,7 @@ def test_refusals():
         assert f(seq=None) == MOE_ERR_INVALID_ARG                      # three sequences, no starts
         assert f(E=2000) == MOE_ERR_UNSUPPORTED and f(E=64, k=33) == MOE_ERR_UNSUPPORTED
         assert f(S=70000) == MOE_ERR_UNSUPPORTED and f(N=1 << 28) == MOE_ERR_UNSUPPORTED
+        assert f(N=1 << 30, E=1, k=1) == MOE_ERR_UNSUPPORTED
         assert f(z=None) == MOE_ERR_INVALID_ARG and f(idx=None) == MOE_ERR_INVALID_ARG
     for name in ("loss", "counts", "prob", "tokens"):
         assert fwd(**{name: None}) == MOE_ERR_INVALID_ARG

@@ -226,9 +226,13 @@ def test_refusals():
     with pytest.raises(ValueError):
         layer.forward(inp["x"], save_for_backward="mxfp8")
     inp, layer, dy = _layer(cfg)
-    layer.forward(inp["x"])
+    layer.forward(inp["x"], save_for_backward=None)   # (any false value)
     with pytest.raises(ValueError):
         layer.backward(None, dy)
+    with pytest.raises(ValueError):
+        layer.backward(inp["x"], dy, d_loss=torch.ones(1, device=DEV))
+    with pytest.raises(ValueError):
+        layer.forward(inp["x"], token_mask=torch.ones(cfg.N, dtype=torch.uint8, device=DEV))
     # gates inside the down projection: the kept backward does not need the unscaled outputs
     inp, layer, dy = _layer(cfg, gate_in_down=True)
     layer.forward(inp["x"], inp["z"], save_for_backward="mxfp8")
