@@ -96,6 +96,18 @@ __device__ __forceinline__ void dma16_window(u32x4_t rsrc, uint32_t voff, uint32
       : "memory", "m0");
 }
 
+// Lanes l and l + 32 hold the same output row: lane l < 32 columns 8 q .. 8 q + 3 of register
+// group q, lane l + 32 columns 8 q + 4 .. 8 q + 7.  Exchanging group 2 u + 1 of lane l with
+// group 2 u of lane l + 32 (gfx950's v_permlane32_swap) leaves lane l with columns 16 u .. 16 u + 7
+// and lane l + 32 with 16 u + 8 .. 16 u + 15, in order: one 16-byte store per lane.  lo and hi
+// are this lane's groups 2 u and 2 u + 1 as packed bf16; every lane must take part.
+__device__ __forceinline__ uint4 lane_pair(uint2 lo, uint2 hi) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  const u32x2_t a = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
+  const u32x2_t b = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
+  return make_uint4(a[0], b[0], a[1], b[1]);
+}
+
 // D += A * B^T on one 32x32 block over 16 k: lane l supplies row l % 32, k 8 * (l / 32) ..
 // + 7 of both operands (any permutation of k applied to both operands alike is allowed)
 __device__ __forceinline__ f32x16_t mma_bf16(uint4 a, uint4 b, f32x16_t c) {

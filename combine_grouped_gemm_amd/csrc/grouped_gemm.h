@@ -41,7 +41,7 @@ struct GemmArgs {
                                // prefix gives no m-tiles and which run as one 320-row tile; or null
   int32_t* tall_counter = nullptr;      // [kNumXcd] the counters of those tiles (zeroed by the prologue)
   const float* shared_b_scale = nullptr;  // (B8) the shared expert's block scales [b_rows, K / 128]
-  uint8_t* au_scale = nullptr;          // gate/up (256 x 256 kernel, bf16): au holds the pre-activations'
+  uint8_t* au_scale = nullptr;          // gate/up (bf16, gathered): au holds the pre-activations'
                                         // 8-bit codes [rows, 2I] and this their scales [rows, 2I / 32]
 };
 

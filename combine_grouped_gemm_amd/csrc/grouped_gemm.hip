@@ -34,6 +34,7 @@
 #include "gemm_device.h"
 #include "grouped_gemm.h"
 #include "moe_common.h"
+#include "mxfp8.h"
 #include "moe_launch.h"
 
 namespace moe {
@@ -455,7 +456,13 @@ struct DmaCfg {
   }
 };
 
-template <int MODE, int BN, int ROWB, int STAGES, int WM, int WN>
+// KEEP (gate/up): also the pre-activations' 8-bit codes and scales, and the shared expert's rows as
+// segment E.  The operands of the MFMAs are exchanged, so that a lane holds 16 columns of one row and
+// a code block's scale needs one exchange.  Tiles of 128 rows x 64 or 128 weight rows, five stages in
+// LDS: H 1024, I 512, 16 experts of 127 rows and 509 shared rows take 18 us with the schedule's launch
+// (the 256 x 256 tiles 37), bound by one tile's 16 stages on 224 of 256 CUs; 32 experts of 64 rows
+// with H 2048, I 4096 take 222 us, 4.8 TB/s of weights.
+template <int MODE, int BN, int ROWB, int STAGES, int WM, int WN, bool KEEP = false>
 __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel(GemmArgs p) {
   using C = DmaCfg<BN, ROWB, STAGES, WM, WN>;
   constexpr int KSTEPS = C::kKSteps;
@@ -486,7 +493,8 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
   const int n_cols = MODE == MODE_GATE_UP ? p.I : p.n_out;
   const int tile_cols = MODE == MODE_GATE_UP ? BN / 2 : BN;
   const int nN = (n_cols + tile_cols - 1) / tile_cols;
-  const long long total = static_cast<long long>(p.tile_prefix[p.E]) * nN;
+  const int n_seg = KEEP && p.shared_rows > 0 ? p.E + 1 : p.E;
+  const long long total = static_cast<long long>(p.tile_prefix[n_seg]) * nN;
   const int xcd = blockIdx.x % kNumXcd;
   const int slot = blockIdx.x / kNumXcd;
   const int per_xcd = gridDim.x / kNumXcd;
@@ -520,9 +528,14 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
     const long long local = L - static_cast<long long>(pe) * nN;
     const int nblk = static_cast<int>(local / mt_e);
     const int mtile = static_cast<int>(local % mt_e);
-    int seg_lo = p.offsets[e], seg_hi = p.offsets[e + 1];
-    seg_lo = seg_lo < 0 ? 0 : (seg_lo > p.rows ? p.rows : seg_lo);
-    seg_hi = seg_hi < seg_lo ? seg_lo : (seg_hi > p.rows ? p.rows : seg_hi);
+    const bool shared = KEEP && e == p.E;
+    int seg_lo, seg_hi;
+    if (shared) {
+      seg_lo = p.rows;
+      seg_hi = p.rows + p.shared_rows;
+    } else {
+      expert_segment(p, e, seg_lo, seg_hi);
+    }
     // the expert's rows are split into mt_e tiles of equal size (a multiple of 32 rows):
     // the tiles that share a weight panel do equal work and stream it together, which
     // keeps more of the panel's second and third reads in L2
@@ -536,7 +549,7 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
     // gathered operand: tile row r is row a_rows[m0 + r] / a_div of a (the launcher checks
     // that a_nrows * rb fits in 32 bits)
     const uint8_t* a_tile = p.a_rows ? p.a : p.a + static_cast<size_t>(m0) * rb;
-    const uint8_t* b_tile = p.b + static_cast<size_t>(e) * p.b_rows * rb;
+    const uint8_t* b_tile = shared ? p.shared_b : p.b + static_cast<size_t>(e) * p.b_rows * rb;
 
     // this lane's source offsets; wave w fills groups w, w + waves, ... (A groups first).
     // Rows past the segment (A) or past the matrix (B) re-read the last valid one.
@@ -548,7 +561,7 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
         int r = g * C::kRowsPerGroup + lrow;
         r = r < mlast ? r : mlast;
         if (p.a_rows) {
-          int t = p.a_rows[m0 + r] / p.a_div;
+          int t = shared ? m0 + r - p.rows : p.a_rows[m0 + r] / p.a_div;
           t = t < 0 ? 0 : (t < p.a_nrows ? t : p.a_nrows - 1);
           r = t;
         }
@@ -596,7 +609,9 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
         __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < MB * NB; ++i) {
-        if (i / NB < ACT) acc[i / NB][i % NB] = mma(fa[i / NB], fb[i % NB], acc[i / NB][i % NB]);
+        if (i / NB < ACT)
+          acc[i / NB][i % NB] = KEEP ? mma(fb[i % NB], fa[i / NB], acc[i / NB][i % NB])
+                                     : mma(fa[i / NB], fb[i % NB], acc[i / NB][i % NB]);
         __builtin_amdgcn_sched_barrier(0);
         between(i);
         __builtin_amdgcn_sched_barrier(0);
@@ -689,6 +704,40 @@ __global__ __launch_bounds__(WM * WN * 64, kDmaOcc) void grouped_gemm_dma_kernel
     }(std::make_integer_sequence<int, MB + 1>{});
 
     // ---- epilogue
+    if constexpr (KEEP) {   // (I % 128 == 0: every column of the tile is one of the output's)
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const int r = m0 + (mb * WM + wm) * 32 + (lane & 31);
+#pragma unroll
+        for (int nb = 0; nb < NB / 2; ++nb) {
+          const int col = c0 + wn * (BN / (2 * WN)) + nb * 32;
+          const f32x16_t& ga = acc[mb][nb];
+          const f32x16_t& ua = acc[mb][nb + NB / 2];
+          uint8_t* out = static_cast<uint8_t*>(p.out) + (static_cast<size_t>(r) * p.I + col) * 2;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // 8 adjacent columns a lane (every lane takes part in the exchange)
+            uint2 hq[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int b0 = 8 * u + 4 * g;
+              hq[g] = make_uint2(pack_bf16x2(silu_f32(ga[b0]) * ua[b0], silu_f32(ga[b0 + 1]) * ua[b0 + 1]),
+                                 pack_bf16x2(silu_f32(ga[b0 + 2]) * ua[b0 + 2], silu_f32(ga[b0 + 3]) * ua[b0 + 3]));
+            }
+            const uint4 o = lane_pair(hq[0], hq[1]);
+            if (r < mend) *reinterpret_cast<uint4*>(out + (16 * u + 8 * h) * 2) = o;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t byte;
+            const uint4 codes = block_codes(acc[mb][nb + half * (NB / 2)], byte);
+            const size_t o = static_cast<size_t>(r) * p.I * 2 + static_cast<size_t>(half) * p.I + col;
+            if (r < mend) *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.au) + o + 16 * h) = codes;
+            if (r < mend && h == 0) p.au_scale[o / 32] = static_cast<uint8_t>(byte);
+          }
+        }
+      }
+      continue;
+    }
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) {
 #pragma unroll
@@ -748,6 +797,33 @@ bool grouped_gemm_shared_supported(int mode, int K, int I, int n_out, long long 
   return K % 128 == 0 && (mode == MODE_GATE_UP ? I : n_out) % 8 == 0 && wide_out_fits(mode, I, n_out) &&
          b_rows * rbytes < (1LL << 32) &&
          (gathered ? static_cast<long long>(a_nrows) : kWideTileRows) * rbytes < (1LL << 32);
+}
+
+// Weight rows (gate and up) of a 128-row tile of the gate/up with kept codes, 0: 256 x 256 tiles.
+// The wide kernel has the better rate once its tiles fill the CUs and their own rows; before that
+// smaller tiles put the work on more CUs and read the weights through more of them, and with few
+// rows per expert the deeper ring of a 128 x 128 tile streams the weights better.  The rows of each
+// expert are on the device, so the rule takes the even case: an expert's last tile half full on
+// average, no more experts than slots (uneven rows cost up to 1.4x, and no result changes: every
+// shape sums K in the same order).  Measured (us on 256 x 256 / 128 x 128 / 128 x 64 tiles; the
+// count of 128-weight-row tiles the rule computes; with the schedule's launch):
+//   H 1024, I 512, 8 experts of 64 rows                29 / 15 / 13     64 tiles of 64 columns
+//   H 4096, I 1024, 8 experts of 64 rows               58 / 34 / 28    128
+//   H 4096, I 1024, 8 experts of 128 rows              62 / 38 / 48    192
+//   H 1024, I 512, 16 of 128 rows, 512 shared          37 / 18 / 23    224
+//   H 4096, I 1024, 8 experts of 256 rows             114 / 69 / 75    320
+//   H 4096, I 1024, 16 of 128 rows, 512 shared         94 / 91 / 112   448
+//   H 1024, I 512, 8 experts of 1024 rows              42 / 42 / 50    544
+//   H 4096, I 1024, 8 experts of 512 rows              89 / 111 / 127  576
+//   H 4096, I 1024, 32 experts of 64 rows             151 / 124 / 124  512, 64 rows an expert
+//   H 2048, I 4096, 32 experts of 64 rows             244 / 222 / 266  2048, 64 rows
+//   H 4096, I 1024, 64 experts of 128 rows            241 / 269 / 330  1536, 128 rows
+static int keep_weight_rows(int E, int rows, int shared_rows, int I) {
+  const long long total = static_cast<long long>(rows) + shared_rows;
+  const long long seg = (E < rows ? E : rows) + (shared_rows > 0 ? 1 : 0);
+  const long long even = total / kDM + seg / 2, m = seg > even ? seg : even;
+  if (m * (I / 32) <= 256) return 64;
+  return m * (I / 64) <= 480 || total <= 96 * seg ? 128 : 0;
 }
 
 bool grouped_gemm_keep_supported(int K, int I, int rows, int n_seg, int a_nrows) {
@@ -863,10 +939,11 @@ hipError_t launch_grouped_gemm(int ct, bool b8, int mode, const void* a, const f
     return hipErrorNotSupported;   // (callers check first)
   const bool wide = wide_ok && (shared_rows > 0 || row_gate != nullptr || au != nullptr ||
                                 mode == MODE_GATE_UP || E > 1);
-  const int tile_rows = stream ? kStreamTileRows : (wide || wide8 ? kWideTileRows : (dma ? kDM : GBM));
+  const int keep_rows = au_scale != nullptr ? keep_weight_rows(E, rows, shared_rows, I) : 0;
+  const int tile_rows = keep_rows != 0 ? kDM : stream ? kStreamTileRows : (wide || wide8 ? kWideTileRows : (dma ? kDM : GBM));
   // bf16 GEMMs on the 256 x 256 kernel: experts of 257..320 rows as one tile (down: 320 x 128,
   // gate/up: 320 x 256); the down GEMM on e4m3 weights as well (320 x 128)
-  const bool tall = wide || (wide8 && mode == MODE_DOWN);
+  const bool tall = (wide && keep_rows == 0) || (wide8 && mode == MODE_DOWN);
   hipLaunchKernelGGL(build_tiles_kernel, dim3(1), dim3(1024), 0, s, offsets, E, rows, tile_rows, cap,
                      prefix, tile_expert, tile_counter, shared_rows, kWideTallRows,
                      tall ? tall_list : nullptr, kNumXcd + 1);
@@ -900,6 +977,14 @@ hipError_t launch_grouped_gemm(int ct, bool b8, int mode, const void* a, const f
   p.shared_b_scale = shared_b_scale;
   p.au_scale = au_scale;
   if (stream) return launch_grouped_gemm_stream(mode, p, s);
+  if (keep_rows != 0) {
+    const dim3 grid(persistent_grid());
+    if (keep_rows == 64)
+      hipLaunchKernelGGL((grouped_gemm_dma_kernel<MODE_GATE_UP, 64, kDmaRowB, 5, 4, 1, true>), grid, dim3(256), 0, s, p);
+    else
+      hipLaunchKernelGGL((grouped_gemm_dma_kernel<MODE_GATE_UP, 128, kDmaRowB, 5, 4, 2, true>), grid, dim3(512), 0, s, p);
+    return hipGetLastError();
+  }
   if (wide || wide8) {
     p.tile_counter = tile_counter;
     if (tall) {

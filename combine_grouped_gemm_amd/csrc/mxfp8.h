@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_device.h"
 #include "moe_common.h"
 
 namespace moe {
@@ -41,6 +42,36 @@ __device__ __forceinline__ uint32_t mx_encode4(float a, float b, float c, float 
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, w, true);
   return static_cast<uint32_t>(w);
+}
+// The 8-bit codes of one 32-column block of an output row, whose 16 values in lane l are
+// columns 8 q + 0..3 (l < 32) or 8 q + 4..7 in register group q, and the other 16 in lane l ^ 32:
+// of the values rounded to bf16, as the quantizer of bf16 rows would read them.  Returns 16 codes
+// in column order, columns 0..15 in lane l < 32 and 16..31 in lane l + 32; byte: the block's scale.
+// Every lane must take part.
+__device__ __forceinline__ uint4 block_codes(const f32x16_t& v, uint32_t& byte) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  uint32_t w[8], m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    const uint32_t lo = (w[i] << 16) & 0x7FFFFFFFu, hi = w[i] & 0x7FFF0000u;
+    m = m > lo ? m : lo;
+    m = m > hi ? m : hi;
+  }
+  const u32x2_t mm = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  byte = mx_scale_byte(mm[0] > mm[1] ? mm[0] : mm[1]);
+  const float inv = mx_inverse(byte);
+  uint32_t c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    c[q] = mx_encode4(__uint_as_float(w[2 * q] << 16), __uint_as_float(w[2 * q] & 0xFFFF0000u),
+                      __uint_as_float(w[2 * q + 1] << 16), __uint_as_float(w[2 * q + 1] & 0xFFFF0000u), inv);
+  // (each swap exchanges its second operand in lanes l < 32 with its first in lanes l + 32)
+  const u32x2_t a = __builtin_amdgcn_permlane32_swap(c[0], c[1], false, false);   // columns 0..7 | 8..15
+  const u32x2_t b = __builtin_amdgcn_permlane32_swap(c[2], c[3], false, false);   // 16..23 | 24..31
+  const u32x2_t x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const u32x2_t y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return make_uint4(x[0], y[0], x[1], y[1]);
 }
 // the values of the 8 codes of two words
 __device__ __forceinline__ void mx_decode8(uint2 q, float s, float (&v)[8]) {

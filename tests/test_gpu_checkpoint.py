@@ -261,6 +261,30 @@ def test_gate_up_keeps_the_codes_of_its_bf16_rows(N, H, E, k, I, hot):
     assert (h3[last:] == 3).all() and (q3[last:] == 5).all() and (s3[last:] == 6).all()
 
 
+# the same on sizes that take each tile shape: 64 weight rows (one round of tiles), 128 (few tiles; many tiles with few
+# rows an expert), and 256 (even experts, experts of 257..320 rows, a hot and an empty one)
+@pytest.mark.parametrize("N,H,E,k,I,hot", [(97, 1152, 6, 2, 384, False), (161, 384, 3, 2, 128, True),
+                                           (513, 640, 16, 4, 512, False), (450, 256, 8, 2, 1024, True),
+                                           (90, 512, 33, 4, 1152, False), (2, 256, 200, 8, 2176, False),
+                                           (1100, 256, 8, 2, 2048, False), (600, 128, 5, 2, 2560, True),
+                                           (300, 512, 4, 2, 4096, True), (200, 256, 3, 3, 8192, False)])
+def test_gate_up_kept_codes_of_every_tile_shape(N, H, E, k, I, hot):
+    test_gate_up_keeps_the_codes_of_its_bf16_rows(N, H, E, k, I, hot)
+
+
+def test_gate_up_kept_codes_shared_rows_only():
+    """No routed rows: the shared expert's alone, without a slot table."""
+    say("gate/up with kept codes: shared rows only")
+    for N, I in ((70, 256), (700, 4096)):
+        x, w13, sw, off, ss, _ = _gate_up_inputs(N, 256, 2, 1, I, 7)
+        au = torch.empty(2 * N, 2 * I, dtype=torch.bfloat16, device=DEV)
+        h = moe.moe_expert_gate_up_gathered_shared(x, ss, 1, off, w13, sw, au=au)
+        q, s = moe.moe_quantize_mxfp8(au)
+        h2, q2, s2 = moe.moe_expert_gate_up_mxfp8(x, ss[:0], 1, torch.zeros_like(off), w13, sw, rows=0)
+        sync()
+        assert torch.equal(h[N:], h2) and torch.equal(q[N:], q2) and torch.equal(s[N:], s2)
+
+
 def test_gate_up_kept_codes_not_finite():
     """A token with a NaN gives NaN blocks in its own rows only."""
     say("gate/up with kept codes: NaN")
