@@ -9,6 +9,14 @@ from tests.gpu_util import f64, say, sync
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _return_cached_blocks():
+    """The allocator's cached blocks go back afterwards: a test elsewhere counts the bytes it hands out, and
+    an unsplit block of these sizes would count as more."""
+    yield
+    torch.cuda.empty_cache()
 U32 = 2.0 ** -24
 
 
