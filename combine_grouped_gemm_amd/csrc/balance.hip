@@ -20,8 +20,9 @@
 // sequence's slots.  Counts are integers, added atomically in LDS: their order does not matter.
 //
 // Measured: N 8192, E 256, k 8: 5.0 us (8.4 MB of logits) + 6.4 us and, with the gates, 8.6 us
-// backward: latencies (loads, the ticket).  N 32768, E 160, 61 sequences: 13.4 + 5.9 and 15.6 us: the
-// softmax's vector instructions (24 of 64 lanes hold no expert there).
+// backward: latencies (loads, the ticket).  N 32768, E 160, 61 sequences: 13.4 + 5.9 and 15.6 us: still
+// latencies (groups of 16 lanes with three runs each, a third of the instructions a token, take 15.1
+// and 14.6 us in a row of calls against 15.7 and 13.9).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
