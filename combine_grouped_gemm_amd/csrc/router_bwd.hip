@@ -22,11 +22,12 @@
 //
 // fp32 operands run on v_mfma_f32_32x32x2_f32 (products and sums in fp32).
 //
-// Measured, bf16, N 8192, E 256, H 7168: wgrad 54 us + 11 us for the sum of 9 parts (bound by the
-// 66 MB of partial sums behind the 117 MB of x); dgrad with rest 75 us (60 us of it are rest and dx, as
+// Measured, bf16, N 8192, E 256, H 7168: wgrad 55 us with the sum of its 4 parts (117 MB of x, 29 MB of
+// partial sums out and back); dgrad with rest 75 us (60 us of it are rest and dx, as
 // with E = 8; the rest grows by 0.11 us an expert with the direct-to-LDS loads).
 #include <hip/hip_runtime.h>
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "gemm_device.h"
@@ -162,19 +163,36 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
 #pragma unroll
     for (int j = 0; j < kBOps; ++j) dma16_window(wb, voff_b[j], base + C::kABytes + (wave + 4 * j) * 1024);
   };
-  // (rows that are not multiples of 16 bytes) one 16-byte chunk of 8 elements per op, zeros past
-  // the rows and columns of dz
+  // (rows that are not multiples of 16 bytes) one 16-byte chunk of 8 elements per op: a load of 2-byte
+  // alignment while all 8 lie in dz, element by element at its end.  Zeros past the rows and, in
+  // dgrad, past the columns of dz.
+  const size_t dz_n = static_cast<size_t>(p.N) * p.E;
   auto read_a = [&](int ks, uint4 (&v)[kAOps]) __attribute__((always_inline)) {
+    struct __attribute__((packed, aligned(2))) Chunk {
+      uint32_t w[4];
+    };
     const int k0 = k_lo + ks * kRbKS;
 #pragma unroll
     for (int j = 0; j < kAOps; ++j) {
       const int r = a_row(j), c = (lane % kACh) ^ a_key(r);
       const int row = DGRAD ? m0 + r : k0 + r, col = (DGRAD ? k0 : m0) + 8 * c;
-      const bool in = row < (DGRAD ? p.N : k_hi);
-      uint32_t w[8];
+      const size_t at = static_cast<size_t>(row) * p.E + col;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (row >= (DGRAD ? p.N : k_hi) || col >= p.E) continue;
+      if (at + 8 <= dz_n) {
+        const Chunk q = *reinterpret_cast<const Chunk*>(dz + at);
+        v[j] = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+      } else {
+        uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = in && col + i < p.E ? dz[static_cast<size_t>(row) * p.E + col + i] : 0u;
-      v[j] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+        for (int i = 0; i < 8; ++i) w[i] = at + i < dz_n ? dz[at + i] : 0u;
+        v[j] = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+      }
+      if constexpr (DGRAD) {
+        const int n = p.E - col;   // elements of the row
+        auto keep = [&](uint32_t w, int i) { return n >= i + 2 ? w : (n > i ? w & 0xFFFFu : 0u); };
+        v[j] = make_uint4(keep(v[j].x, 0), keep(v[j].y, 2), keep(v[j].z, 4), keep(v[j].w, 6));
+      }
     }
   };
   auto put_a = [&](int sl, const uint4 (&v)[kAOps]) __attribute__((always_inline)) {
@@ -494,26 +512,87 @@ __global__ __launch_bounds__(kRbThreads) void router_wgrad_sum_kernel(const floa
   }
 }
 
-int rb_tile_rows(int rows) { return rows > 128 ? 256 : (rows > 64 ? 128 : 64); }
-// dgrad: 256 tokens halve the reads of W_r, but two workgroups fit a CU; up to 128 experts the reads and
-// writes of rest and dx count for more, and three workgroups of 128 tokens keep more of them in
-// flight (N 8192, H 7168, E 64: 57 us against 59; E 256: 85 against 81)
-int rb_dgrad_rows(int N, int E) { return E <= 128 && N > 64 ? 128 : rb_tile_rows(N); }
+// dgrad: 256 tokens halve the reads of W_r, but two workgroups fit a CU (128 tokens: three, 64: four).
+// Up to 128 experts the reads and writes of rest and dx count for more and smaller tiles keep more of them in
+// flight; with few tiles they also use more CUs and end sooner.  Measured with rest, us on 64 / 128 / 256
+// tokens (tiles of 64 tokens):
+//   N 300,  H 7168 (280):   E 8    4.3 /  5.3 /  8.2    E 256    7.8 /  8.2 / 12.2
+//   N 2048, H 2048 (512):   E 64   5.6 /  6.4 /  8.9    E 512   12.9 / 13.2 / 17.2
+//   N 1024, H 7168 (896):   E 64   8.8 /  9.5 / 11.0    E 256   15.0 / 14.1 / 14.8
+//   N 4096, H 4096 (2048):  E 8   13.5 / 14.9 / 14.1    E 256   23.2 / 23.1 / 22.1
+//   N 8192, H 4096 (4096):  E 64  39.3 / 37.1 / 36.0    E 256   57.6 / 51.9 / 48.9
+//   N 8192, H 7168 (7168):  E 64  63.0 / 58.4 / 60.2    E 256  103.9 / 86.6 / 82.7
+// dz rows through registers wait in each stage, and more workgroups share the waits:
+//   N 4096, H 4096 (2048):  E 60  16.5 / 19.3 / 17.5    E 250  30.1 / 34.1 / 32.1
+//   N 8192, H 7168 (7168):  E 60  64.1 / 61.0 / 66.0    E 250  108.7 / 100.7 / 121.8
+int rb_dgrad_rows(int N, int E, int H, bool dma) {
+  const long long t64 = static_cast<long long>((N + 63) / 64) * ((H + kRbTN - 1) / kRbTN);
+  if (!dma) return t64 <= 4096 ? 64 : 128;
+  if (E <= 128) return t64 <= 2048 ? 64 : 128;
+  return t64 <= 640 ? 64 : (t64 <= 1024 ? 128 : 256);
+}
 
-// token ranges of a wgrad: about two workgroups per CU, ranges of whole stages and at least two
-// (bf16, N 8192, E 256, H 7168, sum included: 4 / 8 / 9 / 16 ranges 53 / 51 / 50 / 68 us; fp32, N 2048, E 128,
-// H 8192, 256 / 512 / 1024 workgroups: 84 / 59 / 57 us, E 64, H 4096: 28 / 24 / 27)
+// Row tile and token ranges of a wgrad.
+// bf16: the pair with the least of
+//   stages of a range * t  +  (more than one range: 2 + (S + 3) * 8 E H bytes / 10 TB/s + S / 8 * 0.5)   us
+// where t is a stage's time by tile rows while a CU has one workgroup, and the second part the sum's
+// launch, the partial sums' way out and back, and the sum's batches of eight.  Workgroups beyond 256
+// take the CU's time from each other, so there are no more unless the tiles alone are.  dz rows that
+// come through registers wait for their loads in each stage: t is longer, and workgroups share the
+// waits.  Measured with the sum, us by S = 1 / 2 / 4 / 8 / 16 (64-row tiles to E 64, then 128, 256):
+//   N 300,  H 7168, E 8     5.7 /  6.7 /  6.4 /  6.8        E 256  13.3 / 20.3 / 23.5 / 24.0
+//   N 1024, H 1024, E 8    10.9 /  9.1 /  7.3 /  6.4 /  6.7   E 256  22.7 / 18.3 / 15.4 / 16.2 / 19.5
+//   N 1024, H 7168, E 64   11.4 / 11.3 / 11.6 / 15.9 / 18.4   E 256  24.2 / 25.8 / 23.6 / 28.1 / 44.2
+//   N 4096, H 7168, E 64   35.1 / 22.0 / 16.2 / 17.9 / 21.0   E 256  71.7 / 47.5 / 36.5 / 39.3 / 62.5
+//   N 2500, H 7168, E 60   51.7 / 31.0 / 20.3 / 16.6 / 18.2   E 250  94.0 / 56.8 / 39.2 / 36.6 / 54.0
+//   N 8192, H 7168, E 256: 4 ranges 55, 9 ranges 62;  E 5: 8 ranges 38, 16 ranges 29
+// and by tile rows 64 / 128 / 256 with the best S of each:
+//   N 300,  H 2048, E 256   5.8 /  8.1 / 12.5     N 1000, H 7168, E 256  12.4 / 15.5 / 23.8
+//   N 8192, H 2048, E 256  24.1 / 22.1 / 26.6     N 8192, H 7168, E 256  89.1 / 60.9 / 55.5
+// From 90 MB of x on, 64-row tiles are bound by its reading: where 256 workgroups are not a whole
+// number of tiles, 512 fill the CUs better (N 8192, E 8, H 7168: 31 -> 27 us; H 5632: 24 -> 21; with
+// H 8192, 64 tiles, 256 take 29 and 512 30).
+// fp32 (N 2048, E 128, H 8192, 256 / 512 / 1024 workgroups: 84 / 59 / 57 us; E 64, H 4096: 28 / 24 / 27):
+// 512, of at least two steps.
 struct RbSplit {
-  int S, span;
+  int S, span, rows;
 };
 RbSplit rb_split(int N, int H, int E, bool bf16) {
-  const int tm = bf16 ? rb_tile_rows(E) : kF32TM, tn = bf16 ? kRbTN : kF32TN, step = bf16 ? kRbKS : kF32KS;
-  const long long tiles = static_cast<long long>((E + tm - 1) / tm) * ((H + tn - 1) / tn);
-  long long S = tiles >= 512 ? 1 : 512 / tiles;
-  const long long most = (N + 2 * step - 1) / (2 * step);
-  S = S < most ? S : (most > 1 ? most : 1);
-  const int span = static_cast<int>(((N + S - 1) / S + step - 1) / step) * step;
-  return {(N + span - 1) / span, span};
+  const int step = bf16 ? kRbKS : kF32KS, steps = (N - 1) / step + 1;
+  const int n_tiles = bf16 ? (H + kRbTN - 1) / kRbTN : (H + kF32TN - 1) / kF32TN;
+  auto tiles = [&](int rows) { return static_cast<long long>((E + rows - 1) / rows) * n_tiles; };
+  auto at_most = [&](int groups, int rows) { return tiles(rows) >= groups ? 1 : static_cast<int>(groups / tiles(rows)); };
+  int S = 1, rows = kF32TM;
+  if (!bf16) {
+    const int most = (steps + 1) / 2;
+    S = at_most(512, rows) < most ? at_most(512, rows) : most;
+  } else if (E <= 64 && E % 8 == 0 && static_cast<long long>(N) * H >= 45000000 && tiles(64) * at_most(256, 64) <= 240) {
+    rows = 64;
+    S = at_most(512, rows);
+  } else {
+    const bool dma = E % 8 == 0;
+    const float move = static_cast<float>(E) * static_cast<float>(H) * 8e-7f;
+    const float stage[2][3] = {{0.5f, 0.7f, 1.1f}, {0.25f, 0.33f, 0.5f}};
+    const int groups[3] = {1024, 512, 512};
+    float best = 0.0f;
+    for (int i = 0; i < 3; ++i) {
+      const int r = 64 << i, most = at_most(dma ? 256 : groups[i], r);
+      for (int c = 1; c <= most && c <= steps; ++c) {
+        const float load = static_cast<float>(tiles(r)) * static_cast<float>(c) * (1.0f / 256);
+        const float t = stage[dma][i] * (load <= 1.0f ? 1.0f : (dma ? load : sqrtf(load)));
+        float us = static_cast<float>((steps + c - 1) / c) * t;
+        if (c > 1) us += 2.0f + static_cast<float>(c + 3) * move + 0.5f * static_cast<float>((c + 7) / 8);
+        if ((i == 0 && c == 1) || us < best) {
+          best = us;
+          S = c;
+          rows = r;
+        }
+      }
+      if (r >= E) break;
+    }
+  }
+  const int span = (steps + S - 1) / S * step;   // whole steps
+  return {(N + span - 1) / span, span, rows};
 }
 
 unsigned rb_grid(long long tiles) {
@@ -527,13 +606,20 @@ hipError_t rb_launch(const RbArgs& p, bool dma, long long tiles, hipStream_t s) 
   return hipGetLastError();
 }
 
+bool rb_dma(const RbArgs& p) { return p.E % 8 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0; }
+
 template <bool DGRAD>
-hipError_t rb_run(const RbArgs& p, hipStream_t s) {
+hipError_t rb_run(const RbArgs& p, int tm, hipStream_t s) {
   const int rows = DGRAD ? p.N : p.E;
-  const int tm = DGRAD ? rb_dgrad_rows(p.N, p.E) : rb_tile_rows(p.E);
+  const bool dma = rb_dma(p);
   const long long tiles = static_cast<long long>((rows + tm - 1) / tm) * ((p.H + kRbTN - 1) / kRbTN) * (DGRAD ? 1 : p.S);
-  const bool dma = p.E % 8 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0;
-  if (tm == 256) return rb_launch<DGRAD, 256>(p, dma, tiles, s);
+  if (tm == 256) {
+    if constexpr (DGRAD) {   // (256 tokens are taken with 16-byte dz rows only)
+      hipLaunchKernelGGL((router_grad_kernel<true, 256, true>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+      return hipGetLastError();
+    }
+    return rb_launch<DGRAD, 256>(p, dma, tiles, s);
+  }
   if (tm == 128) return rb_launch<DGRAD, 128>(p, dma, tiles, s);
   return rb_launch<DGRAD, 64>(p, dma, tiles, s);
 }
@@ -548,12 +634,12 @@ size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16) {
 
 hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, int N, int E, int H, void* dw,
                                      bool dw_f32, void* ws, hipStream_t s) {
-  const RbSplit r = N > 0 ? rb_split(N, H, E, bf16) : RbSplit{0, 0};
+  const RbSplit r = N > 0 ? rb_split(N, H, E, bf16) : RbSplit{0, 0, 0};
   RbArgs p = {dz, x, nullptr, r.S > 1 ? ws : dw, N, E, H, r.S, r.span, r.S > 1 || dw_f32 ? 1 : 0};
   if (r.S > 0) {
     hipError_t err = hipSuccess;
     if (bf16) {
-      err = rb_run<false>(p, s);
+      err = rb_run<false>(p, r.rows, s);
     } else {
       hipLaunchKernelGGL(router_grad_f32_kernel<false>,
                          dim3((E + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN, r.S), dim3(kRbThreads), 0, s, p);
@@ -571,7 +657,7 @@ hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, i
 hipError_t launch_router_dense_dgrad(const void* dz, const void* w_r, bool bf16, int N, int E, int H, const void* rest,
                                      void* dx, hipStream_t s) {
   const RbArgs p = {dz, w_r, rest, dx, N, E, H, 1, 0, bf16 ? 0 : 1};
-  if (bf16) return rb_run<true>(p, s);
+  if (bf16) return rb_run<true>(p, rb_dgrad_rows(N, E, H, rb_dma(p)), s);
   hipLaunchKernelGGL(router_grad_f32_kernel<true>, dim3((N + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN),
                      dim3(kRbThreads), 0, s, p);
   return hipGetLastError();

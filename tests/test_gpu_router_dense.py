@@ -63,6 +63,19 @@ def test_sizes(N, E, H, dt):
     _dgrad(dz, w, _t((N, H), 4, dt, 0.01))
 
 
+# the tiles and ranges of large batches: 16-byte dz rows and others, one and several row tiles, tails in every
+# direction
+@pytest.mark.parametrize("N,E,H", [(4200, 60, 8320), (4200, 64, 8200), (4100, 203, 8200), (4100, 136, 8200),
+                                   (8200, 256, 7176), (8200, 250, 7176), (8192, 24, 7168), (3000, 512, 1032)])
+def test_large_sizes(N, E, H):
+    say(f"dense router gradients N={N} E={E} H={H}")
+    dt = torch.bfloat16
+    dz, w = _t((N, E), 1, dt, 2.0 ** -9), _t((E, H), 3, dt, 0.02)
+    x = _t((N, H), 2, dt)
+    _wgrad(dz, x, torch.float32)
+    _dgrad(dz, w, x)
+
+
 def test_many_ranges_and_repeats():
     """A batch cut into many token ranges, and the same bits on every call."""
     say("dense router gradients: token ranges")
