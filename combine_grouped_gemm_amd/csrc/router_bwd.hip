@@ -23,8 +23,8 @@
 // fp32 operands run on v_mfma_f32_32x32x2_f32 (products and sums in fp32).
 //
 // Measured, bf16, N 8192, E 256, H 7168: wgrad 55 us with the sum of its 4 parts (117 MB of x, 29 MB of
-// partial sums out and back); dgrad with rest 75 us (60 us of it are rest and dx, as
-// with E = 8; the rest grows by 0.11 us an expert with the direct-to-LDS loads).
+// partial sums out and back); dgrad with rest 76 us (53 us of it are rest and dx, as
+// with E = 8; about 0.1 us an expert comes on top).
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <math.h>
