@@ -591,8 +591,8 @@ RbSplit rb_split(int N, int H, int E, bool bf16) {
       if (r >= E) break;
     }
   }
-  const int span = (steps + S - 1) / S * step;   // whole steps
-  return {(N + span - 1) / span, span, rows};
+  const long long span = static_cast<long long>((steps + S - 1) / S) * step;   // whole steps
+  return {static_cast<int>((N + span - 1) / span), static_cast<int>(span < INT_MAX ? span : INT_MAX), rows};
 }
 
 unsigned rb_grid(long long tiles) {

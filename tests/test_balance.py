@@ -135,3 +135,16 @@ def test_dense_router_binding_checks():
     for bad in (dict(dz=dz[:, :3]), dict(w_r=w.bfloat16()), dict(rest=x[:5]), dict(dx=x.bfloat16())):
         with pytest.raises(ValueError):
             moe.moe_router_dense_dgrad(**{**dict(dz=dz, w_r=w), **bad})
+
+
+def test_workspaces_at_the_ends_of_their_ranges():
+    """Every size of the workspace queries is answered: no tokens, one token, more sequences than
+    tokens, the largest counts."""
+    for N in (0, 1, 2, 63, 8192, 2 ** 24 - 1, 2 ** 31 - 1):
+        for E in (1, 7, 8, 160, 1024):
+            for S in (1, 2, 64, 2 ** 20):
+                assert 0 <= moe.moe_workspace_bytes(moe.MOE_OP_BALANCE_LOSS, N, 0, 0, E, S, 0) < 2 ** 45
+            for H in (8, 7168, 2 ** 20):
+                for dt in (MOE_F32, MOE_BF16):
+                    ws = moe.moe_workspace_bytes(moe.MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, dt)
+                    assert 0 <= ws <= 1024 * 4 * E * H + 255

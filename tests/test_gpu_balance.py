@@ -128,6 +128,17 @@ def test_sequences(N, E, S):
         _check(_case(N, E, 2, S=S, seed=S, mask=mask, bias=True), gates=mask)
 
 
+@pytest.mark.parametrize("N,E,ones", [(3000, 32, 64), (700, 4, 39), (5000, 100, 20)])
+def test_uneven_sequences(N, E, ones):
+    """Sequences of one token, then one of all the others: a chunk meets many sequences and a sequence
+    many chunks."""
+    say(f"balance uneven sequences N={N} E={E} ones={ones}")
+    c = _case(N, E, 2, seed=ones, mask=True)
+    for seq in ([*range(ones + 1), N], [0, *range(N - ones, N + 1)]):
+        c["seq_start"] = np.array(seq, np.int32)
+        _check(c, gates=True)
+
+
 def test_nothing_counts():
     """No tokens at all, a mask that leaves none, and no sequence with a token: loss 0, gradient 0."""
     say("balance: nothing counts")
