@@ -10,8 +10,8 @@
 // The gates' gradient needs no expert outputs: <dy, W_down h> = <W_down^T dy, h>.  With g folded
 // into h_out the weight gradient is dW_down = dy^T (g h) over the plain permuted dy.
 //
-// All three move each byte once and are bound by memory; a lane takes 8 adjacent columns (8 bytes of
-// codes, 16 of bf16), four lanes a block, so that a wave's accesses are contiguous, and every stream
+// All three move each byte once and are bound by memory; a lane takes 16 bytes of adjacent values (8
+// columns of bf16, 4 of fp32), four or eight lanes a block, so that a wave's accesses are contiguous, and every stream
 // is touched once (non-temporal).  Measured, bf16: 8191 x 7168 quantized in 31 us (5.8 TB/s) and
 // written to 8 expert-ordered rows each in 178 us (5.6 TB/s); SwiGLU backward of 65536 slots of I
 // 2048 with gates in 266 us (5.06 TB/s; a 1 GiB copy on the card: 5.15).
@@ -30,104 +30,113 @@ constexpr int kCkThreads = 256;
 typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
-// 8 adjacent values at 8-column group i
+// Columns of a lane: 16 bytes of values, so that a wave's access is contiguous (fp32 with 8 columns a
+// lane writes every second 16 bytes at a time: 3.4 TB/s in the SwiGLU backward)
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, size_t i, float (&v)[8]) {
-  if constexpr (F32) {
-    const u32x4v a = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p) + 2 * i);
-    const u32x4v b = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p) + 2 * i + 1);
+constexpr int kCols = F32 ? 4 : 8;
+
+// the adjacent values at column group i
+template <bool F32>
+__device__ __forceinline__ void load_cols(const void* p, size_t i, float (&v)[kCols<F32>]) {
+  const u32x4v a = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p) + i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (F32) {
       v[j] = __uint_as_float(a[j]);
-      v[4 + j] = __uint_as_float(b[j]);
-    }
-  } else {
-    const u32x4v a = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p) + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    } else {
       v[2 * j] = __uint_as_float(a[j] << 16);
       v[2 * j + 1] = __uint_as_float(a[j] & 0xFFFF0000u);
     }
   }
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void* p, size_t i, const float (&v)[8]) {
-  if constexpr (F32) {
-    u32x4v a, b;
+__device__ __forceinline__ void store_cols(void* p, size_t i, const float (&v)[kCols<F32>]) {
+  u32x4v a;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      a[j] = __float_as_uint(v[j]);
-      b[j] = __float_as_uint(v[4 + j]);
-    }
-    __builtin_nontemporal_store(a, reinterpret_cast<u32x4v*>(p) + 2 * i);
-    __builtin_nontemporal_store(b, reinterpret_cast<u32x4v*>(p) + 2 * i + 1);
-  } else {
-    const u32x4v a = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7])};
-    __builtin_nontemporal_store(a, reinterpret_cast<u32x4v*>(p) + i);
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (F32) a[j] = __float_as_uint(v[j]);
+    else a[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
   }
+  __builtin_nontemporal_store(a, reinterpret_cast<u32x4v*>(p) + i);
 }
+template <bool F32>
 __device__ __forceinline__ uint2 load_codes(const uint8_t* q, size_t i) {
+  if constexpr (F32) return make_uint2(__builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(q) + i), 0u);
   const u32x2v w = __builtin_nontemporal_load(reinterpret_cast<const u32x2v*>(q) + i);
   return make_uint2(w[0], w[1]);
 }
+template <bool F32>
+__device__ __forceinline__ void decode_cols(uint2 q, float s, float (&v)[kCols<F32>]) {
+  if constexpr (F32) mx_decode4(q.x, s, v[0], v[1], v[2], v[3]);
+  else mx_decode8(q, s, v);
+}
+template <bool F32>
+__device__ __forceinline__ size_t block_of(size_t i) { return i / (32 / kCols<F32>); }
 
 // Rows of cols % 32 == 0 columns lie one after the other, so blocks never straddle rows and the
-// tensor is a flat run of n8 groups of 8 columns (4 groups a block).
+// tensor is a flat run of n column groups (4 or 8 a block).
 template <bool F32>
-__global__ __launch_bounds__(kCkThreads) void quantize_mx_kernel(const void* __restrict__ x, long long n8,
+__global__ __launch_bounds__(kCkThreads) void quantize_mx_kernel(const void* __restrict__ x, long long n,
                                                                  uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  constexpr int V = kCols<F32>;
   const long long stride = static_cast<long long>(gridDim.x) * kCkThreads;
-  for (long long i = static_cast<long long>(blockIdx.x) * kCkThreads + threadIdx.x; i < n8; i += stride) {
-    float v[8];
-    load8<F32>(x, i, v);
+  for (long long i = static_cast<long long>(blockIdx.x) * kCkThreads + threadIdx.x; i < n; i += stride) {
+    float v[V];
+    load_cols<F32>(x, i, v);
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
       const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
       m = b > m ? b : m;
     }
-    // (n8 % 4 == 0: the four lanes of a block are all active)
+    // (n is a multiple of a block's groups: the lanes of a block are all active)
 #pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
+    for (int off = 1; off < 32 / V; off <<= 1) {
       const uint32_t o = __shfl_xor(m, off, kWave);
       m = o > m ? o : m;
     }
     const uint32_t byte = mx_scale_byte(m);
     const float inv = mx_inverse(byte);
-    const u32x2v w = {mx_encode4(v[0], v[1], v[2], v[3], inv), mx_encode4(v[4], v[5], v[6], v[7], inv)};
-    reinterpret_cast<u32x2v*>(q)[i] = w;
-    if ((i & 3) == 0) scale[i >> 2] = static_cast<uint8_t>(byte);
+    if constexpr (F32) {
+      reinterpret_cast<uint32_t*>(q)[i] = mx_encode4(v[0], v[1], v[2], v[3], inv);
+    } else {
+      const u32x2v w = {mx_encode4(v[0], v[1], v[2], v[3], inv), mx_encode4(v[4], v[5], v[6], v[7], inv)};
+      reinterpret_cast<u32x2v*>(q)[i] = w;
+    }
+    if (i % (32 / V) == 0) scale[block_of<F32>(i)] = static_cast<uint8_t>(byte);
   }
 }
 
 template <bool F32>
 __global__ __launch_bounds__(kCkThreads) void dequantize_mx_kernel(const uint8_t* __restrict__ q,
-                                                                   const uint8_t* __restrict__ scale, long long n8,
+                                                                   const uint8_t* __restrict__ scale, long long n,
                                                                    void* __restrict__ out) {
   const long long stride = static_cast<long long>(gridDim.x) * kCkThreads;
-  for (long long i = static_cast<long long>(blockIdx.x) * kCkThreads + threadIdx.x; i < n8; i += stride) {
-    float v[8];
-    mx_decode8(load_codes(q, i), mx_scale(scale[i >> 2]), v);
-    store8<F32>(out, i, v);
+  for (long long i = static_cast<long long>(blockIdx.x) * kCkThreads + threadIdx.x; i < n; i += stride) {
+    float v[kCols<F32>];
+    decode_cols<F32>(load_codes<F32>(q, i), mx_scale(scale[block_of<F32>(i)]), v);
+    store_cols<F32>(out, i, v);
   }
 }
 
-// one workgroup per token: its values to the k rows its slots name (negative positions: no row)
-template <bool F32>
+// TPT threads per token (a wave or the workgroup): its values to the k rows its slots name (negative
+// positions: no row); groups: column groups of a row
+template <bool F32, int TPT>
 __global__ __launch_bounds__(kCkThreads) void dequantize_rows_mx_kernel(const uint8_t* __restrict__ q,
-                                                                        const uint8_t* __restrict__ scale, int cols8,
-                                                                        int k, const int32_t* __restrict__ send_pos,
+                                                                        const uint8_t* __restrict__ scale,
+                                                                        long long rows, int groups, int k,
+                                                                        const int32_t* __restrict__ send_pos,
                                                                         long long out_rows, void* __restrict__ out) {
-  const size_t t = blockIdx.x;
-  for (int c = threadIdx.x; c < cols8; c += kCkThreads) {
-    const size_t i = t * cols8 + c;
-    float v[8];
-    mx_decode8(load_codes(q, i), mx_scale(scale[i >> 2]), v);
+  const long long t = static_cast<long long>(blockIdx.x) * (kCkThreads / TPT) + threadIdx.x / TPT;
+  if (t >= rows) return;
+  for (int c = threadIdx.x % TPT; c < groups; c += TPT) {
+    const size_t i = static_cast<size_t>(t) * groups + c;
+    float v[kCols<F32>];
+    decode_cols<F32>(load_codes<F32>(q, i), mx_scale(scale[block_of<F32>(i)]), v);
     for (int j = 0; j < k; ++j) {
       const int r = send_pos[t * k + j];
       if (r < 0 || r >= out_rows) continue;
-      store8<F32>(out, static_cast<size_t>(r) * cols8 + c, v);
+      store_cols<F32>(out, static_cast<size_t>(r) * groups + c, v);
     }
   }
 }
@@ -149,18 +158,19 @@ __global__ __launch_bounds__(kCkThreads) void swiglu_backward_mx_kernel(
     return;
   }
   const float g = gate != nullptr ? gate[s] : 1.0f;
-  const int c8 = I / 8;       // 8-column groups of a half row
-  const size_t a0 = static_cast<size_t>(r) * 2 * c8, h0 = static_cast<size_t>(r) * c8;
+  constexpr int V = kCols<F32>;
+  const int n = I / V;        // column groups of a half row
+  const size_t a0 = static_cast<size_t>(r) * 2 * n, h0 = static_cast<size_t>(r) * n;
   float dot = 0.0f;
-  for (int c = l; c < c8; c += TPR) {
-    float a[8], u[8], d[8], da[8], du[8], hv[8];
-    const uint2 qa = load_codes(au, a0 + c), qu = load_codes(au, a0 + c8 + c);
-    const uint32_t ba = au_scale[(a0 + c) >> 2], bu = au_scale[(a0 + c8 + c) >> 2];
-    load8<F32>(dh, h0 + c, d);
-    mx_decode8(qa, mx_scale(ba), a);
-    mx_decode8(qu, mx_scale(bu), u);
+  for (int c = l; c < n; c += TPR) {
+    float a[V], u[V], d[V], da[V], du[V], hv[V];
+    const uint2 qa = load_codes<F32>(au, a0 + c), qu = load_codes<F32>(au, a0 + n + c);
+    const uint32_t ba = au_scale[block_of<F32>(a0 + c)], bu = au_scale[block_of<F32>(a0 + n + c)];
+    load_cols<F32>(dh, h0 + c, d);
+    decode_cols<F32>(qa, mx_scale(ba), a);
+    decode_cols<F32>(qu, mx_scale(bu), u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < V; ++j) {
       const float sg = sigmoid_f32(a[j]);
       const float as = a[j] * sg, hj = as * u[j], gd = g * d[j];
       dot = fmaf(d[j], hj, dot);
@@ -168,9 +178,9 @@ __global__ __launch_bounds__(kCkThreads) void swiglu_backward_mx_kernel(
       du[j] = gd * as;
       hv[j] = g * hj;
     }
-    store8<F32>(d_au, a0 + c, da);
-    store8<F32>(d_au, a0 + c8 + c, du);
-    store8<F32>(h, h0 + c, hv);
+    store_cols<F32>(d_au, a0 + c, da);
+    store_cols<F32>(d_au, a0 + n + c, du);
+    store_cols<F32>(h, h0 + c, hv);
   }
   if (d_gate == nullptr) return;   // (uniform)
   constexpr int kSpan = TPR < kWave ? TPR : kWave;
@@ -186,8 +196,8 @@ __global__ __launch_bounds__(kCkThreads) void swiglu_backward_mx_kernel(
   if (l == 0) d_gate[s] = dot;
 }
 
-unsigned flat_grid(long long n8) {
-  const long long b = (n8 + kCkThreads - 1) / kCkThreads;
+unsigned flat_grid(long long n) {
+  const long long b = (n + kCkThreads - 1) / kCkThreads;
   return static_cast<unsigned>(b < 16384 ? b : 16384);
 }
 
@@ -195,31 +205,38 @@ unsigned flat_grid(long long n8) {
 
 hipError_t launch_quantize_mx(const void* x, bool f32, long long rows, int cols, uint8_t* q, uint8_t* scale,
                               hipStream_t s) {
-  const long long n8 = rows * (cols / 8);
+  const long long n = rows * (cols / (f32 ? kCols<true> : kCols<false>));
   if (f32)
-    hipLaunchKernelGGL(quantize_mx_kernel<true>, dim3(flat_grid(n8)), dim3(kCkThreads), 0, s, x, n8, q, scale);
+    hipLaunchKernelGGL(quantize_mx_kernel<true>, dim3(flat_grid(n)), dim3(kCkThreads), 0, s, x, n, q, scale);
   else
-    hipLaunchKernelGGL(quantize_mx_kernel<false>, dim3(flat_grid(n8)), dim3(kCkThreads), 0, s, x, n8, q, scale);
+    hipLaunchKernelGGL(quantize_mx_kernel<false>, dim3(flat_grid(n)), dim3(kCkThreads), 0, s, x, n, q, scale);
   return hipGetLastError();
 }
 
 hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, long long rows, int cols, int k,
                                 const int32_t* send_pos, long long out_rows, void* out, bool f32, hipStream_t s) {
   if (send_pos != nullptr) {
-    const dim3 grid(static_cast<unsigned>(rows));
-    if (f32)
-      hipLaunchKernelGGL(dequantize_rows_mx_kernel<true>, grid, dim3(kCkThreads), 0, s, q, scale, cols / 8, k,
-                         send_pos, out_rows, out);
-    else
-      hipLaunchKernelGGL(dequantize_rows_mx_kernel<false>, grid, dim3(kCkThreads), 0, s, q, scale, cols / 8, k,
-                         send_pos, out_rows, out);
+    const int groups = cols / (f32 ? kCols<true> : kCols<false>);
+#define MOE_DEQUANTIZE_ROWS(F32_, TPT_)                                                                            \
+  hipLaunchKernelGGL((dequantize_rows_mx_kernel<F32_, TPT_>),                                                      \
+                     dim3(static_cast<unsigned>((rows * TPT_ + kCkThreads - 1) / kCkThreads)), dim3(kCkThreads), 0, s, q, \
+                     scale, rows, groups, k, send_pos, out_rows, out)
+    // a wave per token while the row is one pass of it (us with 256 / 64 threads, bf16, 30000 rows: 256 columns
+    // to 1 row 10.6 / 7.4, to 8 rows 41 / 28; 512 columns 13.9 / 10.2, 54 / 46; 1024 columns 20 / 18, 97 / 99;
+    // 300 rows of 1024 columns to 8 rows 3.7 / 5.4)
+    const bool wave = groups <= kWave;
+    if (f32 && wave) MOE_DEQUANTIZE_ROWS(true, kWave);
+    else if (f32) MOE_DEQUANTIZE_ROWS(true, kCkThreads);
+    else if (wave) MOE_DEQUANTIZE_ROWS(false, kWave);
+    else MOE_DEQUANTIZE_ROWS(false, kCkThreads);
+#undef MOE_DEQUANTIZE_ROWS
     return hipGetLastError();
   }
-  const long long n8 = rows * (cols / 8);
+  const long long n = rows * (cols / (f32 ? kCols<true> : kCols<false>));
   if (f32)
-    hipLaunchKernelGGL(dequantize_mx_kernel<true>, dim3(flat_grid(n8)), dim3(kCkThreads), 0, s, q, scale, n8, out);
+    hipLaunchKernelGGL(dequantize_mx_kernel<true>, dim3(flat_grid(n)), dim3(kCkThreads), 0, s, q, scale, n, out);
   else
-    hipLaunchKernelGGL(dequantize_mx_kernel<false>, dim3(flat_grid(n8)), dim3(kCkThreads), 0, s, q, scale, n8, out);
+    hipLaunchKernelGGL(dequantize_mx_kernel<false>, dim3(flat_grid(n)), dim3(kCkThreads), 0, s, q, scale, n, out);
   return hipGetLastError();
 }
 

@@ -73,15 +73,17 @@ __device__ __forceinline__ uint4 block_codes(const f32x16_t& v, uint32_t& byte) 
   const u32x2_t y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
   return make_uint4(x[0], y[0], x[1], y[1]);
 }
+// the values of the 4 codes of a word
+__device__ __forceinline__ void mx_decode4(uint32_t q, float s, float& v0, float& v1, float& v2, float& v3) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), false);
+  const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q), true);
+  v0 = a.x * s; v1 = a.y * s; v2 = b.x * s; v3 = b.y * s;
+}
 // the values of the 8 codes of two words
 __device__ __forceinline__ void mx_decode8(uint2 q, float s, float (&v)[8]) {
-  typedef float f32x2_t __attribute__((ext_vector_type(2)));
-  const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), false);
-  const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), true);
-  const f32x2_t c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), false);
-  const f32x2_t d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), true);
-  v[0] = a.x * s; v[1] = a.y * s; v[2] = b.x * s; v[3] = b.y * s;
-  v[4] = c.x * s; v[5] = c.y * s; v[6] = d.x * s; v[7] = d.y * s;
+  mx_decode4(q.x, s, v[0], v[1], v[2], v[3]);
+  mx_decode4(q.y, s, v[4], v[5], v[6], v[7]);
 }
 
 }  // namespace moe
