@@ -273,8 +273,8 @@ __device__ __forceinline__ int block_sum_int(int v, int32_t* red) {
 
 // workgroup (`ex` experts of block x, sequence y): the chunks' partial sums, then the sequence's
 // share of the loss; the last workgroup to finish adds the shares in their order.  Every
-// workgroup takes one turn at the ticket, so they are kept to about 64 (610 for 61 sequences of 160
-// experts took 17 us).
+// workgroup takes one turn at the ticket, so up to 64 sequences they are kept to about 64, and
+// beyond one to each sequence (610 for 61 sequences of 160 experts took 17 us).
 __global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a, int ex) {
   __shared__ float rp[kBalThreads];
   __shared__ int32_t rc[kBalThreads];
@@ -403,13 +403,14 @@ __global__ __launch_bounds__(kBwdThreads) void balance_backward_kernel(BalBwdArg
       s_hi = a.N;
       if (a.seq_start != nullptr) s_hi = s < a.S ? a.seq_start[s + 1] : a.N;
       if (s < a.S) {
-        const float T = static_cast<float>(a.tokens[s]);
-        const float kT = static_cast<float>(a.k) * T, f = T > 0.0f ? scale / (T * T) : 0.0f;
+        // E c - k T in 64 bits, exact for every count: both products pass 2^24 with a few million tokens
+        const double E = a.E, kT = static_cast<double>(a.k) * a.tokens[s];
+        const float T = static_cast<float>(a.tokens[s]), f = T > 0.0f ? scale / (T * T) : 0.0f;
 #pragma unroll
         for (int i = 0; i < V * W; ++i) {
           const int e = ((i / W) * G + l) * W + i % W;
           const int c = e < a.E ? a.counts[static_cast<size_t>(s) * a.E + e] : 0;
-          co[i] = e < a.E ? f * fmaf(static_cast<float>(a.E), static_cast<float>(c), -kT) : 0.0f;
+          co[i] = e < a.E ? f * static_cast<float>(fma(E, static_cast<double>(c), -kT)) : 0.0f;
         }
       }
     }

@@ -1,12 +1,13 @@
-"""GPU parity of the balance loss where a group of lanes works on several tokens one after the other, and of
-batches without tokens or with an expert named twice by a token."""
+"""GPU parity of the balance loss where a group of lanes works on several tokens one after the other, of loads whose
+counts need more than 24 bits, and of batches without tokens or with an expert named twice by a token."""
 import numpy as np
 import pytest
 import torch
 
 import combine_grouped_gemm_amd as moe
-from tests.gpu_util import say, sync
-from tests.test_gpu_balance import DEV, _case, _check, _return_cached_blocks  # noqa: F401
+from oracle import moe_oracle as oracle
+from tests.gpu_util import f64, say, sync
+from tests.test_gpu_balance import DEV, U32, _case, _check, _dev, _prob_rel, _return_cached_blocks  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -33,6 +34,32 @@ def test_sequences_that_end_inside_a_workgroup():
     cuts = cuts[cuts < N - 30] + 3
     c["seq_start"] = np.sort(np.concatenate([cuts, cuts[::3]])).astype(np.int32)
     _check(c, gates=True)
+
+
+@pytest.mark.parametrize("E,k,T,odd", [(5, 5, 3500001, False), (7, 7, 5000001, True), (160, 6, 3000001, True), (160, 6, 8000001, True),
+                                       (3, 3, 100000007, True), (1024, 2, 1048575, True)])
+def test_loads_beyond_24_bits(E, k, T, odd):
+    """Counts of millions of tokens: the difference of an expert's load and the even one keeps every digit.  All
+    experts chosen by every token: no gradient at all; loads next to the even one: the gradient of that difference."""
+    say(f"balance, large counts: E={E} k={k} T={T}")
+    N, alpha = 9, 1e9
+    c = _case(N, E, k, seed=E)
+    counts = np.full((1, E), k * T // E, np.int64)
+    if odd:
+        counts[0] += np.arange(E) % 3 - 1
+    dz = moe.moe_balance_loss_backward(_dev(c["z"]), _dev(c["topk_idx"]), alpha, _dev(counts.astype(np.int32)),
+                                       torch.tensor([T], dtype=torch.int32, device=DEV))
+    sync()
+    diff = [E * int(n) - k * T for n in counts[0]]
+    if not odd:
+        assert not any(diff) and not dz.any()
+        return
+    a = alpha / k / float(T) ** 2 * np.array(diff, np.float64)
+    p = oracle._row_softmax(c["z"])
+    ref = p * (a[None, :] - (p @ a)[:, None])
+    # (as in the parity tests: a within 8 roundings, p within its bound, a sum of at most 22 steps)
+    bound = p * (np.abs(a)[None, :] + (p @ np.abs(a))[:, None]) * (2 * _prob_rel(c) + 2 * U32 * 32)
+    assert np.all(np.abs(f64(dz) - ref) <= bound + U32 * (np.abs(ref) + bound) + 1e-37)
 
 
 @pytest.mark.parametrize("S", [1, 2, 70])
