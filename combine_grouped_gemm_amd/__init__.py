@@ -202,6 +202,13 @@ def _optional_ws(op: int, N: int, H: int, E: int, k: int, dt: int, device):
     return (torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None), nbytes
 
 
+def _ws_bytes(ws: torch.Tensor, device) -> int:
+    """A caller's workspace in bytes; ValueError if it lies on another device than the data."""
+    if ws.device != device:
+        raise ValueError(f"ws is on {ws.device}, not on {device}")
+    return ws.numel() * ws.element_size()
+
+
 def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
@@ -625,6 +632,8 @@ def _balance_args(z, topk_idx, bias, seq_start, token_mask):
     N, E = z.shape
     k = topk_idx.shape[1]
     S = 1 if seq_start is None else seq_start.numel() - 1
+    if S < 1:
+        raise ValueError("seq_start must hold the S + 1 bounds of at least one sequence")
     _expect("z", z, (N, E), _F32, z.device)
     _expect("topk_idx", topk_idx, (N, k), _I32, z.device)
     _expect("bias", bias, (E,), _F32, z.device)
@@ -654,7 +663,7 @@ def moe_balance_loss(z: torch.Tensor, topk_idx: torch.Tensor, alpha: float, bias
     if ws is None:
         ws, ws_bytes = _optional_ws(MOE_OP_BALANCE_LOSS, N, 0, E, S, 0, dev)
     else:
-        ws_bytes = ws.numel()
+        ws_bytes = _ws_bytes(ws, dev)
     _run("moe_balance_loss", dev, _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S, _ptr(token_mask),
          alpha, _ptr(loss), _ptr(counts), _ptr(prob_mean), _ptr(tokens), _ptr(ws), ws_bytes, _stream(z))
     return loss, counts, prob_mean, tokens
@@ -700,7 +709,7 @@ def moe_router_dense_wgrad(dz: torch.Tensor, x: torch.Tensor, dw: Optional[torch
     if ws is None:
         ws, ws_bytes = _optional_ws(MOE_OP_ROUTER_WGRAD, N, H, E, 0, _dt(x), dev)
     else:
-        ws_bytes = ws.numel()
+        ws_bytes = _ws_bytes(ws, dev)
     _run("moe_router_dense_wgrad", dev, _ptr(dz), _ptr(x), _dt(x), N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws_bytes,
          _stream(x))
     return dw
@@ -789,8 +798,8 @@ def moe_expert_gate_up_mxfp8(x: torch.Tensor, src_slot: torch.Tensor, k: int, of
     _expect("w13", w13, (E, 2 * I, H), bf, dev)
     _expect("offsets", offsets, (E + 1,), _I32, dev)
     _expect("src_slot", src_slot, src_slot.shape, _I32, dev)
-    if src_slot.numel() < rows:
-        raise ValueError(f"src_slot must name {rows} rows")
+    if rows < 0 or src_slot.numel() < rows:
+        raise ValueError(f"src_slot names {src_slot.numel()} rows, not {rows}")
     if shared_w13 is not None:
         _expect("shared_w13", shared_w13.reshape(-1, H), (2 * I, H), bf, dev)
     scales = (total, 2 * I // MOE_MX_BLOCK)
@@ -806,8 +815,9 @@ def moe_expert_gate_up_mxfp8(x: torch.Tensor, src_slot: torch.Tensor, k: int, of
     if ws is None:
         n_seg = E + (1 if shared_w13 is not None else 0)
         ws = _workspace(moe_workspace_bytes(MOE_OP_EXPERT_GEMM, total, H, I, n_seg, 1, MOE_BF16), dev)
+    ws_bytes = _ws_bytes(ws, dev)
     _run("moe_expert_gate_up_mxfp8", dev, _ptr(x), _dt(x), N, _ptr(src_slot), k, _ptr(offsets), E, rows, H, I,
-         _ptr(w13), _ptr(shared_w13), _ptr(h), _ptr(au_q), _ptr(au_scale), _ptr(ws), ws.numel(), _stream(x))
+         _ptr(w13), _ptr(shared_w13), _ptr(h), _ptr(au_q), _ptr(au_scale), _ptr(ws), ws_bytes, _stream(x))
     return h, au_q, au_scale
 
 
