@@ -29,11 +29,11 @@ from . import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_BALANCE_LOS
                moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_backward, moe_dequantize_fp8,
                moe_dequantize_mxfp8, moe_dispatch_layout, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
                moe_expert_down_shared_e4m3, moe_expert_gate_up, moe_expert_gate_up_gathered,
-               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3, moe_expert_gate_up_mxfp8,
-               moe_expert_gate_up_preact, moe_expert_wgrad, moe_grouped_ffn, moe_permute, moe_quantize_fp8,
-               moe_quantize_mxfp8, moe_route, moe_router_backward, moe_router_dense_dgrad, moe_router_dense_wgrad,
-               moe_router_input_grad, moe_router_logits, moe_swiglu_backward, moe_swiglu_backward_mxfp8,
-               moe_workspace_bytes)
+               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3,
+               moe_expert_gate_up_mxfp8, moe_expert_gate_up_preact, moe_expert_wgrad, moe_grouped_ffn, moe_permute,
+               moe_quantize_fp8, moe_quantize_mxfp8, moe_route, moe_router_backward, moe_router_dense_dgrad,
+               moe_router_dense_wgrad, moe_router_input_grad, moe_router_logits, moe_swiglu_backward,
+               moe_swiglu_backward_mxfp8, moe_workspace_bytes, _balance_args, _expect)
 
 
 class MoELayer:
@@ -290,10 +290,12 @@ class MoELayer:
                 torch.empty(S, **i32),
                 torch.empty(max(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, self.N, 0, 0, self.E, S, 0), 256),
                             dtype=torch.uint8, device=self.device))
-        self.balance, ws = self.balance_bufs[S][:4], self.balance_bufs[S][4]
+        out, ws = self.balance_bufs[S][:4], self.balance_bufs[S][4]
+        moe_balance_loss(z, self.topk_idx, alpha, bias=self.bias, seq_start=seq_start, token_mask=token_mask, out=out,
+                         ws=ws)
+        self.balance = out
         self.balance_args = dict(z=z, alpha=alpha, seq_start=seq_start, token_mask=token_mask)
-        return moe_balance_loss(z, self.topk_idx, alpha, bias=self.bias, seq_start=seq_start, token_mask=token_mask,
-                                out=self.balance, ws=ws)
+        return out
 
     def forward(self, x: torch.Tensor, z: Optional[torch.Tensor] = None, save_for_backward=False,
                 balance_alpha: Optional[float] = None, seq_start: Optional[torch.Tensor] = None,
@@ -312,24 +314,32 @@ class MoELayer:
             raise ValueError('save_for_backward is False, True or "mxfp8"')
         if balance_alpha is None and (seq_start is not None or token_mask is not None):
             raise ValueError("seq_start and token_mask belong to a balance loss (balance_alpha)")
-        self.keep8 = isinstance(save_for_backward, str)
-        if self.keep8 and (self.dtype != "bf16" or not self.gather or (self.shared and not self.fuse)):
-            raise ValueError("8-bit keeping is built for bf16 layers that gather their rows from x and run a shared "
-                             "expert inside the routed launches")
-        self.save_au = bool(save_for_backward and not self.keep8 and self.fuse and not self.fp8)
+        keep8 = isinstance(save_for_backward, str)
+        # every refusal comes before the first change: what the last forward left stays for its backward
+        if keep8:
+            if self.dtype != "bf16" or not self.gather or (self.shared and not self.fuse):
+                raise ValueError("8-bit keeping is built for bf16 layers that gather their rows from x and run a shared "
+                                 "expert inside the routed launches")
+            if self.H % 128 or self.I % 128 or self.E >= 1024:
+                raise ValueError("8-bit keeping is built for H and I that are multiples of 128 and fewer than 1024 experts")
+            _expect("x", x, (self.N, self.H), (torch.bfloat16,), self.device)
+        if z is None and self.w_r is None:
+            raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
+        if balance_alpha is not None:
+            _balance_args(self.z if z is None else z, self.topk_idx, self.bias, seq_start, token_mask)
+        self.keep8 = keep8
+        self.save_au = bool(save_for_backward and not keep8 and self.fuse and not self.fp8)
         if self.save_au and self.au_all is None:
             self.au_all = torch.empty((self.N * self.k + self.N, 2 * self.I), dtype=torch.bfloat16,
                                       device=self.device)
         self.au_saved = self.save_au
-        if self.keep8:
+        if keep8:
             if self.kept_x is None:
                 self._keep8_buffers()
             moe_quantize_mxfp8(x, *self.kept_x)
         if self.side is not None:
             self.launch_shared_side(x)
         if z is None:
-            if self.w_r is None:
-                raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
             z = self.router(x)
         self.route(z)
         if balance_alpha is None:
