@@ -131,7 +131,8 @@ class MoELayer:
         self.keep8 = False       # the last forward kept the tokens and pre-activations in 8 bits
         self.kept_x = self.kept_au = None   # (codes, scales) of both
         # the balance loss of the last forward: (loss [1], counts [S, E], mean probabilities [S, E],
-        # counted tokens [S]), or None; what its gradient needs; and its buffers and workspace by S
+        # counted tokens [S]), or None; what its gradient needs; and its buffers and workspace by the
+        # power of two that holds S (never replaced: a captured step keeps its memory)
         self.balance = None
         self.balance_args = None
         self.balance_bufs = {}
@@ -283,16 +284,18 @@ class MoELayer:
                      token_mask: Optional[torch.Tensor] = None):
         """The balance loss of the routes of z into self.balance (see moe_balance_loss)."""
         S = 1 if seq_start is None else seq_start.numel() - 1
-        if S not in self.balance_bufs:
+        cap = 1 << max(S - 1, 0).bit_length()   # (every batch may bring another S: a set for each power of two)
+        if cap not in self.balance_bufs:
             i32, f32 = dict(dtype=torch.int32, device=self.device), dict(dtype=torch.float32, device=self.device)
-            self.balance_bufs[S] = (
-                torch.empty(1, **f32), torch.empty((S, self.E), **i32), torch.empty((S, self.E), **f32),
-                torch.empty(S, **i32),
-                torch.empty(max(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, self.N, 0, 0, self.E, S, 0), 256),
+            self.balance_bufs[cap] = (
+                torch.empty(1, **f32), torch.empty((cap, self.E), **i32), torch.empty((cap, self.E), **f32),
+                torch.empty(cap, **i32),
+                # (more sequences never need less)
+                torch.empty(max(moe_workspace_bytes(MOE_OP_BALANCE_LOSS, self.N, 0, 0, self.E, cap, 0), 256),
                             dtype=torch.uint8, device=self.device))
-        out, ws = self.balance_bufs[S][:4], self.balance_bufs[S][4]
-        moe_balance_loss(z, self.topk_idx, alpha, bias=self.bias, seq_start=seq_start, token_mask=token_mask, out=out,
-                         ws=ws)
+        loss, counts, prob_mean, tokens, ws = self.balance_bufs[cap]
+        out = moe_balance_loss(z, self.topk_idx, alpha, bias=self.bias, seq_start=seq_start, token_mask=token_mask,
+                               out=(loss, counts[:S], prob_mean[:S], tokens[:S]), ws=ws)
         self.balance = out
         self.balance_args = dict(z=z, alpha=alpha, seq_start=seq_start, token_mask=token_mask)
         return out

@@ -1,8 +1,10 @@
-"""What the layer holds and keeps between calls, on the CPU: refused calls change nothing
-(no GPU needed: nothing here is enqueued)."""
+"""What the layer holds and keeps between calls, on the CPU: refused calls change nothing, buffers of the balance loss
+are bounded (no GPU needed: nothing here is enqueued)."""
 import pytest
 import torch
 
+import combine_grouped_gemm_amd as moe
+import combine_grouped_gemm_amd.layer as layer_module
 from combine_grouped_gemm_amd.layer import MoELayer
 
 STATE = ("keep8", "kept_x", "kept_au", "save_au", "au_saved", "au_all", "balance", "balance_args")
@@ -46,3 +48,28 @@ def test_refused_forwards_leave_the_last_one_in_place():
             _refused(layer, x, balance_alpha=0.1, save_for_backward="mxfp8", **bad)
     layer = _layer(w_r=False)
     _refused(layer, torch.zeros(6, 128, dtype=torch.bfloat16), save_for_backward="mxfp8")
+
+
+def test_balance_buffers_are_bounded(monkeypatch):
+    """Batches of ever other sequence counts: the buffers are those of a few capacities, each call's views fit its
+    count and the workspace is large enough, and a count that came before finds its buffers again."""
+    calls = []
+
+    def record(z, idx, alpha, bias=None, seq_start=None, token_mask=None, out=None, ws=None):
+        S = 1 if seq_start is None else seq_start.numel() - 1
+        need = moe.moe_workspace_bytes(moe.MOE_OP_BALANCE_LOSS, z.shape[0], 0, 0, z.shape[1], S, 0)
+        assert [tuple(t.shape) for t in out] == [(1,), (S, 4), (S, 4), (S,)] and ws.numel() >= need
+        assert all(t.is_contiguous() for t in out)
+        calls.append((S, tuple(t.data_ptr() for t in out) + (ws.data_ptr(),)))
+        return out
+
+    monkeypatch.setattr(layer_module, "moe_balance_loss", record)
+    layer = _layer(N=700)
+    z = torch.zeros(700, 4)
+    for S in [None, *range(1, 1200), 65535, *range(1, 40)]:
+        seq = None if S is None else torch.zeros(S + 1, dtype=torch.int32)
+        layer.balance_step(z, 0.1, seq)
+    assert len(layer.balance_bufs) <= 17
+    first = {}
+    for S, at in calls:
+        assert first.setdefault(S, at) == at
