@@ -617,8 +617,9 @@ hipError_t rb_run(const RbArgs& p, int tm, hipStream_t s) {
     if constexpr (DGRAD) {   // (256 tokens are taken with 16-byte dz rows only)
       hipLaunchKernelGGL((router_grad_kernel<true, 256, true>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
       return hipGetLastError();
+    } else {
+      return rb_launch<DGRAD, 256>(p, dma, tiles, s);
     }
-    return rb_launch<DGRAD, 256>(p, dma, tiles, s);
   }
   if (tm == 128) return rb_launch<DGRAD, 128>(p, dma, tiles, s);
   return rb_launch<DGRAD, 64>(p, dma, tiles, s);
