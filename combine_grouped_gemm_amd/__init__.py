@@ -18,7 +18,7 @@ import torch
 
 __all__ = [
     "MoEError", "lib", "library_path", "declared_symbols",
-    "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3",
+    "MOE_F32", "MOE_BF16", "MOE_FP8_E4M3", "MOE_BF16X3",
     "MOE_OP_DISPATCH_LAYOUT", "MOE_OP_GROUPED_FFN", "MOE_OP_EXPERT_GEMM", "MOE_OP_ROUTER", "MOE_OP_EXPERT_DGRAD",
     "MOE_OP_BALANCE_LOSS", "MOE_OP_ROUTER_WGRAD",
     "MOE_LAYOUT_SCRATCH_BYTES", "moe_router_logits", "moe_route", "moe_dispatch_layout",
@@ -36,7 +36,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = range(3)
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_BF16X3 = range(4)
 (MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD,
  MOE_OP_BALANCE_LOSS, MOE_OP_ROUTER_WGRAD) = range(7)
 MOE_MX_BLOCK = 32                    # columns that share a scale of the kept 8-bit rows
@@ -622,7 +622,7 @@ def moe_stream_probe(src: torch.Tensor, ratio: int, dst: Optional[torch.Tensor] 
 # ------------------------------------------------------------------------------------------
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
-_ACT = (torch.float32, torch.bfloat16)
+_ACT, _BF16 = (torch.float32, torch.bfloat16), (torch.bfloat16,)
 
 
 def _balance_args(z, topk_idx, bias, seq_start, token_mask):
@@ -674,9 +674,11 @@ def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: fl
                               seq_start: Optional[torch.Tensor] = None, token_mask: Optional[torch.Tensor] = None,
                               d_loss: Optional[torch.Tensor] = None, topk_gate: Optional[torch.Tensor] = None,
                               d_gate: Optional[torch.Tensor] = None, dz: Optional[torch.Tensor] = None,
-                              dz_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+                              dz_dtype: torch.dtype = torch.float32, planes: bool = False) -> torch.Tensor:
     """dz [N, E]: the balance loss's gradient of the logits times d_loss [1] (None: 1), plus the
-    gates' (topk_gate and d_gate [N, k]) on the selected experts."""
+    gates' (topk_gate and d_gate [N, k]) on the selected experts.  planes (or a dz [3, N, E] bf16): three
+    bf16 planes whose sum is the fp32 gradient, the first the gradient rounded to bf16; the dense router
+    gradients take them beside bf16 operands."""
     N, E, k, S = _balance_args(z, topk_idx, bias, seq_start, token_mask)
     dev = z.device
     _expect("counts", counts, (S, E), _I32, dev)
@@ -684,51 +686,68 @@ def moe_balance_loss_backward(z: torch.Tensor, topk_idx: torch.Tensor, alpha: fl
     _expect("d_loss", d_loss, (1,), _F32, dev)
     _expect("topk_gate", topk_gate, (N, k), _F32, dev)
     _expect("d_gate", d_gate, (N, k), _F32, dev)
+    planes = planes or (dz is not None and dz.dim() == 3)
     if dz is None:
-        dz = torch.empty((N, E), dtype=dz_dtype, device=dev)
+        dz = torch.empty((3, N, E), dtype=torch.bfloat16, device=dev) if planes else torch.empty(
+            (N, E), dtype=dz_dtype, device=dev)
+    elif planes:
+        _expect("dz", dz, (3, N, E), _BF16, dev)
     else:
         _expect("dz", dz, (N, E), _ACT, dev)
     _run("moe_balance_loss_backward", dev, _ptr(z), _ptr(bias), _ptr(topk_idx), N, E, k, _ptr(seq_start), S,
          _ptr(token_mask), alpha, _ptr(counts), _ptr(tokens), _ptr(d_loss), _ptr(topk_gate), _ptr(d_gate), _ptr(dz),
-         _dt(dz), _stream(z))
+         MOE_BF16X3 if planes else _dt(dz), _stream(z))
     return dz
+
+
+def _dense_dz(dz, N, E, operand):
+    """The C dtype of a dense logit gradient [N, E] of operand's dtype, or [3, N, E] planes beside bf16."""
+    if dz.dim() == 3:
+        _expect("dz", dz, (3, N, E), _BF16, operand.device)
+        if operand.dtype != torch.bfloat16:
+            raise ValueError(f"dz in planes goes with bfloat16 operands, not {operand.dtype}")
+        return MOE_BF16X3
+    _expect("dz", dz, (N, E), (operand.dtype,), operand.device)
+    return _dt(operand)
 
 
 def moe_router_dense_wgrad(dz: torch.Tensor, x: torch.Tensor, dw: Optional[torch.Tensor] = None,
                            dw_dtype: torch.dtype = torch.float32, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """dW_r [E, H] = dz^T x for a dense logit gradient dz [N, E] (of x's dtype)."""
+    """dW_r [E, H] = dz^T x for a dense logit gradient dz [N, E] (of x's dtype; beside a bf16 x also
+    [3, N, E], an fp32 gradient in planes)."""
     N, H = x.shape
     E = dz.shape[-1]
     dev = x.device
     _expect("x", x, (N, H), _ACT, dev)
-    _expect("dz", dz, (N, E), (x.dtype,), dev)
+    dt = _dense_dz(dz, N, E, x)
     if dw is None:
         dw = torch.empty((E, H), dtype=dw_dtype, device=dev)
     else:
         _expect("dw", dw, (E, H), _ACT, dev)
     if ws is None:
-        ws, ws_bytes = _optional_ws(MOE_OP_ROUTER_WGRAD, N, H, E, 0, _dt(x), dev)
+        ws, ws_bytes = _optional_ws(MOE_OP_ROUTER_WGRAD, N, H, E, 0, dt, dev)
     else:
         ws_bytes = _ws_bytes(ws, dev)
-    _run("moe_router_dense_wgrad", dev, _ptr(dz), _ptr(x), _dt(x), N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws_bytes,
+    _run("moe_router_dense_wgrad", dev, _ptr(dz), _ptr(x), dt, N, E, H, _ptr(dw), _dt(dw), _ptr(ws), ws_bytes,
          _stream(x))
     return dw
 
 
 def moe_router_dense_dgrad(dz: torch.Tensor, w_r: torch.Tensor, rest: Optional[torch.Tensor] = None,
                            dx: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """dx [N, H] = dz W_r (+ rest) for a dense logit gradient dz [N, E] (of w_r's dtype)."""
+    """dx [N, H] = dz W_r (+ rest) for a dense logit gradient dz [N, E] (of w_r's dtype; beside a bf16 w_r
+    also [3, N, E], an fp32 gradient in planes)."""
     E, H = w_r.shape
-    N = dz.shape[0]
+    N = dz.shape[-2]
     dev = w_r.device
     _expect("w_r", w_r, (E, H), _ACT, dev)
-    _expect("dz", dz, (N, E), (w_r.dtype,), dev)
+    dt = _dense_dz(dz, N, E, w_r)
     _expect("rest", rest, (N, H), (w_r.dtype,), dev)
     if dx is None:
         dx = torch.empty((N, H), dtype=w_r.dtype, device=dev)
     else:
         _expect("dx", dx, (N, H), (w_r.dtype,), dev)
-    _run("moe_router_dense_dgrad", dev, _ptr(dz), _ptr(w_r), _dt(w_r), N, E, H, _ptr(rest), _ptr(dx), _stream(w_r))
+    _run("moe_router_dense_dgrad", dev, _ptr(dz), _ptr(w_r), dt, N, E, H, _ptr(rest), _ptr(dx), _stream(w_r))
     return dx
 
 

@@ -373,8 +373,33 @@ struct BalBwdArgs {
   float alpha;
 };
 
-// a workgroup takes `per` consecutive tokens, a group every kGroups-th of them
-template <int G, int V, int W, bool F32>
+// A run of n (1 or 4) values as three bf16 words each, every one the rounding of what the ones before it
+// leave: 8 bits of the significand each, so that their sum is the fp32 value (down to 2^-133; a value that is not
+// finite, or past bf16's largest, leaves a NaN)
+template <int W>
+__device__ __forceinline__ void store_planes(uint16_t* dz, size_t plane, const float* d) {
+  float r[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) r[i] = d[i];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    if constexpr (W == 4) {
+      const uint2 w = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+      *reinterpret_cast<uint2*>(dz + q * plane) = w;
+      r[0] -= __uint_as_float(w.x << 16);
+      r[1] -= __uint_as_float(w.x & 0xFFFF0000u);
+      r[2] -= __uint_as_float(w.y << 16);
+      r[3] -= __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+      const uint16_t w = f32_to_bf16(r[0]);
+      dz[q * plane] = w;
+      r[0] -= bf16_to_f32(w);
+    }
+  }
+}
+
+// a workgroup takes `per` consecutive tokens, a group every kGroups-th of them; dz of DT
+template <int G, int V, int W, int DT>
 __global__ __launch_bounds__(kBwdThreads) void balance_backward_kernel(BalBwdArgs a) {
   constexpr int kGroups = kBwdThreads / G;
   const int l = threadIdx.x % G, lane = threadIdx.x % kWave;
@@ -463,10 +488,12 @@ __global__ __launch_bounds__(kBwdThreads) void balance_backward_kernel(BalBwdArg
       const int e = (v * G + l) * W;
       if (e >= a.E) continue;
       const size_t o = static_cast<size_t>(t) * a.E + e;
-      if constexpr (F32 && W == 4)
+      if constexpr (DT == MOE_BF16X3)
+        store_planes<W>(reinterpret_cast<uint16_t*>(a.dz) + o, static_cast<size_t>(a.N) * a.E, d + v * W);
+      else if constexpr (DT == MOE_F32 && W == 4)
         *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.dz) + o) =
             make_float4(d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]);
-      else if constexpr (F32)
+      else if constexpr (DT == MOE_F32)
         reinterpret_cast<float*>(a.dz)[o] = d[v];
       else if constexpr (W == 4)
         *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.dz) + o) =
@@ -587,7 +614,7 @@ hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t*
 hipError_t launch_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
                                         const int32_t* seq_start, int S, const uint8_t* mask, float alpha,
                                         const int32_t* counts, const int32_t* tokens, const float* d_loss,
-                                        const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s) {
+                                        const float* gate, const float* d_gate, void* dz, int dz_dt, hipStream_t s) {
   BalBwdArgs a = {z, bias, topk_idx, seq_start, mask, counts, tokens, d_loss, gate, d_gate, dz,
                   N, E, k, S, 0, alpha};
   const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(z) % 16 == 0 && reinterpret_cast<uintptr_t>(dz) % 16 == 0;
@@ -597,10 +624,12 @@ hipError_t launch_balance_loss_backward(const float* z, const float* bias, const
     const int passes = ((N + pass - 1) / pass + 2047) / 2048;
     a.per = pass * passes;
     const int blocks = (N + a.per - 1) / a.per;
-    if (f32)
-      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), true>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
+    if (dz_dt == MOE_F32)
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), MOE_F32>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
+    else if (dz_dt == MOE_BF16)
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), MOE_BF16>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
     else
-      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), false>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
+      hipLaunchKernelGGL((balance_backward_kernel<g(), v(), wd(), MOE_BF16X3>), dim3(blocks), dim3(kBwdThreads), 0, s, a);
   });
   return hipGetLastError();
 }

@@ -58,10 +58,13 @@ moe_status check_balance(int N, int E, int k, const int32_t* seq_start, int S) {
   return MOE_OK;
 }
 
+// planes of a dense logit gradient
+int dz_planes(int dt) { return dt == MOE_BF16X3 ? 3 : 1; }
+
 // Checks shared by the router's dense gradients.
 moe_status check_router_dense(moe_dtype dt, int N, int E, int H) {
   if (N < 0 || E < 1 || H <= 0) return MOE_ERR_INVALID_ARG;
-  if (dt != MOE_F32 && dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_BF16X3) return MOE_ERR_UNSUPPORTED;
   if (E > MOE_MAX_EXPERTS || H % 8 != 0 || H > (1 << 20) || N >= kMaxRowsPerLaunch) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -106,7 +109,7 @@ size_t moe_workspace_bytes(int op, int N, int H, int I, int E, int k, int a_dt) 
       return moe::balance_ws_bytes(N, E, k);
     case MOE_OP_ROUTER_WGRAD:
       if (E < 1 || N == 0 || H <= 0) return 0;
-      return moe::router_wgrad_ws_bytes(N, H, E, a_dt == MOE_BF16);
+      return moe::router_wgrad_ws_bytes(N, H, E, a_dt == MOE_BF16 || a_dt == MOE_BF16X3, dz_planes(a_dt));
     default:
       return 0;
   }
@@ -532,14 +535,13 @@ moe_status moe_balance_loss_backward(const float* z, const float* bias, const in
                                      hipStream_t stream) {
   const moe_status st = check_balance(N, E, k, seq_start, S);
   if (st != MOE_OK) return st;
-  if (dz_dt != MOE_F32 && dz_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (dz_dt != MOE_F32 && dz_dt != MOE_BF16 && dz_dt != MOE_BF16X3) return MOE_ERR_UNSUPPORTED;
   if ((topk_gate == nullptr) != (d_gate == nullptr)) return MOE_ERR_INVALID_ARG;
   if (N == 0) return MOE_OK;
   if (z == nullptr || topk_idx == nullptr || counts == nullptr || tokens == nullptr || dz == nullptr)
     return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_balance_loss_backward(z, bias, topk_idx, N, E, k, seq_start, S, token_mask, alpha,
-                                                      counts, tokens, d_loss, topk_gate, d_gate, dz,
-                                                      dz_dt == MOE_F32, stream));
+                                                      counts, tokens, d_loss, topk_gate, d_gate, dz, dz_dt, stream));
 }
 
 moe_status moe_router_dense_wgrad(const void* dz, const void* x, moe_dtype dt, int N, int E, int H, void* dw,
@@ -549,10 +551,11 @@ moe_status moe_router_dense_wgrad(const void* dz, const void* x, moe_dtype dt, i
   if (dw_dt != MOE_F32 && dw_dt != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (dw == nullptr || !aligned16(dw) || (N > 0 && (dz == nullptr || x == nullptr || !aligned16(x))))
     return MOE_ERR_INVALID_ARG;
-  const size_t need = moe::router_wgrad_ws_bytes(N, H, E, dt == MOE_BF16);
+  const size_t need = moe::router_wgrad_ws_bytes(N, H, E, dt != MOE_F32, dz_planes(dt));
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   if (need > 0 && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_router_dense_wgrad(dz, x, dt == MOE_BF16, N, E, H, dw, dw_dt == MOE_F32, ws, stream));
+  return hip_status(moe::launch_router_dense_wgrad(dz, dz_planes(dt), x, dt != MOE_F32, N, E, H, dw, dw_dt == MOE_F32,
+                                                   ws, stream));
 }
 
 moe_status moe_router_dense_dgrad(const void* dz, const void* w_r, moe_dtype dt, int N, int E, int H, const void* rest,
@@ -562,7 +565,7 @@ moe_status moe_router_dense_dgrad(const void* dz, const void* w_r, moe_dtype dt,
   if (N == 0) return MOE_OK;
   if (dz == nullptr || w_r == nullptr || dx == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w_r) || !aligned16(dx) || (rest != nullptr && !aligned16(rest))) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_router_dense_dgrad(dz, w_r, dt == MOE_BF16, N, E, H, rest, dx, stream));
+  return hip_status(moe::launch_router_dense_dgrad(dz, dz_planes(dt), w_r, dt != MOE_F32, N, E, H, rest, dx, stream));
 }
 
 // ---- activations kept in 8 bits

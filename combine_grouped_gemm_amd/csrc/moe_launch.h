@@ -66,14 +66,14 @@ hipError_t launch_balance_loss(const float* z, const float* bias, const int32_t*
 hipError_t launch_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
                                         const int32_t* seq_start, int S, const uint8_t* mask, float alpha,
                                         const int32_t* counts, const int32_t* tokens, const float* d_loss,
-                                        const float* gate, const float* d_gate, void* dz, bool f32, hipStream_t s);
+                                        const float* gate, const float* d_gate, void* dz, int dz_dt, hipStream_t s);
 
-// the router's gradients from a dense dz (router_bwd.hip); rest may be null
-size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16);
-hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, int N, int E, int H, void* dw,
-                                     bool dw_f32, void* ws, hipStream_t s);
-hipError_t launch_router_dense_dgrad(const void* dz, const void* w_r, bool bf16, int N, int E, int H, const void* rest,
-                                     void* dx, hipStream_t s);
+// the router's gradients from a dense dz (router_bwd.hip); planes of dz: 1, or 3 (bf16); rest may be null
+size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16, int planes);
+hipError_t launch_router_dense_wgrad(const void* dz, int planes, const void* x, bool bf16, int N, int E, int H,
+                                     void* dw, bool dw_f32, void* ws, hipStream_t s);
+hipError_t launch_router_dense_dgrad(const void* dz, int planes, const void* w_r, bool bf16, int N, int E, int H,
+                                     const void* rest, void* dx, hipStream_t s);
 
 // activations kept in 8 bits (checkpoint.hip); send_pos, gate and d_gate may be null
 hipError_t launch_quantize_mx(const void* x, bool f32, long long rows, int cols, uint8_t* q, uint8_t* scale,

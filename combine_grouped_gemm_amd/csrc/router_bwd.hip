@@ -17,6 +17,10 @@
 // row is the next row's values: fragments past E are cleared, as 0 times their W_r row of zeros would
 // keep a NaN.  dz rows that are not multiples of 16 bytes (E % 8 != 0) come through registers.
 //
+// dz in three bf16 planes, whose sum is an fp32 value digit for digit (8 + 8 + 8 bits), gives products
+// of the fp32 dz: a stage of 32 becomes three, one for each plane of dz beside the same stage of the other
+// operand, which is loaded with the first and stays for the other two.
+//
 // wgrad has few tiles (E / TM x H / 128), so the tokens are cut into S ranges whose fp32 partial
 // sums a second launch adds in order: the result has the same bits on every run.
 //
@@ -24,7 +28,8 @@
 //
 // Measured, bf16, N 8192, E 256, H 7168: wgrad 55 us with the sum of its 4 parts (117 MB of x, 29 MB of
 // partial sums out and back); dgrad with rest 76 us (53 us of it are rest and dx, as
-// with E = 8; about 0.1 us an expert comes on top).
+// with E = 8; about 0.1 us an expert comes on top).  With three planes of dz 113 and 120 us, 60 and 75 with E
+// 128; N 4096, E 8, H 4096: 17 and 15 us against 11 and 14.
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <math.h>
@@ -44,7 +49,7 @@ constexpr int kRbKS = 32;    // K per stage
 constexpr int kRbSlots = 3;
 
 struct RbArgs {
-  const void* dz;     // [N, E]
+  const void* dz;     // [N, E], or three planes of it
   const void* b;      // wgrad: x [N, H]; dgrad: W_r [E, H]
   const void* rest;   // dgrad: [N, H] or null
   void* out;          // wgrad: partial sums [S, E, H] fp32, or dW_r when S = 1; dgrad: dx
@@ -96,12 +101,14 @@ __device__ __forceinline__ uint4 strided_frag(uint32_t addr, int s) {
   return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
 }
 
-// DGRAD: dx; otherwise wgrad.  DMA: dz rows are multiples of 16 bytes from a 16-byte base.
-template <bool DGRAD, int TM, bool DMA>
+// DGRAD: dx; otherwise wgrad.  DMA: dz rows are multiples of 16 bytes from a 16-byte base.  PLANES: of dz
+// (1 or 3)
+template <bool DGRAD, int TM, bool DMA, int PLANES>
 __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   using C = RbCfg<TM>;
   constexpr int kMB = C::kMB, kNB = C::kNB, kAOps = C::kAOps, kBOps = C::kBOps;
-  constexpr int kOps = (DMA ? kAOps : 0) + kBOps;
+  constexpr int kADma = DMA ? kAOps : 0, kOps = kADma + kBOps;
+  static_assert(PLANES == 1 || PLANES == kRbSlots, "plane p of a stage lies in slot p");
   constexpr int kPitch = kNB * 32 + 4;   // dgrad epilogue: floats of a staged row
   constexpr int kLds = DGRAD && 4 * 32 * kPitch * 4 > kRbSlots * C::kStage ? 4 * 32 * kPitch * 4 : kRbSlots * C::kStage;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
@@ -128,7 +135,9 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   const int nk = (k_hi - k_lo + kRbKS - 1) / kRbKS;
   const int mcount = rowsM - m0 < TM ? rowsM - m0 : TM;
   const int ncols = p.H - n0 < kRbTN ? p.H - n0 : kRbTN;
-  const uint16_t* dz = reinterpret_cast<const uint16_t*>(p.dz);
+  const uint16_t* dz0 = reinterpret_cast<const uint16_t*>(p.dz);
+  const size_t dz_n = static_cast<size_t>(p.N) * p.E;   // elements of a plane
+  auto plane_of = [&](int plane) { return PLANES == 1 ? dz0 : dz0 + plane * dz_n; };
   const uint16_t* bm = reinterpret_cast<const uint16_t*>(p.b);
 
   // ---- loads: op j of a wave fills 1 KB group wave + 4 j of its operand
@@ -145,7 +154,9 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
     const int r = (wave + 4 * j) * (64 / kBCh) + lane / kBCh;
     voff_b[j] = static_cast<uint32_t>(r) * p.H * 2 + (((lane % kBCh) ^ strided_key<kRbTN * 2>(r)) << 4);
   }
-  auto load_stage = [&](int ks, int sl) __attribute__((always_inline)) {
+  // stage ks of a plane into slot sl; the other operand's (with plane 0) into that of slot bsl
+  auto load_stage = [&](int ks, int plane, int sl, int bsl) __attribute__((always_inline)) {
+    const uint16_t* dz = plane_of(plane);
     const int k0 = k_lo + ks * kRbKS;
     const int left = k_hi - k0 < kRbKS ? k_hi - k0 : kRbKS;
     const uint32_t base = __builtin_amdgcn_readfirstlane(lds0 + sl * C::kStage);
@@ -158,16 +169,18 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
 #pragma unroll
       for (int j = 0; j < kAOps; ++j) dma16_window(wa, voff_a[j], base + (wave + 4 * j) * 1024);
     }
+    if (PLANES > 1 && plane != 0) return;
+    const uint32_t base_b = PLANES == 1 ? base : __builtin_amdgcn_readfirstlane(lds0 + bsl * C::kStage);
     const u32x4_t wb = buffer_window(bm + static_cast<size_t>(k0) * p.H + n0,
                                      (static_cast<uint32_t>(left - 1) * p.H + ncols) * 2);
 #pragma unroll
-    for (int j = 0; j < kBOps; ++j) dma16_window(wb, voff_b[j], base + C::kABytes + (wave + 4 * j) * 1024);
+    for (int j = 0; j < kBOps; ++j) dma16_window(wb, voff_b[j], base_b + C::kABytes + (wave + 4 * j) * 1024);
   };
   // (rows that are not multiples of 16 bytes) one 16-byte chunk of 8 elements per op: a load of 2-byte
   // alignment while all 8 lie in dz, element by element at its end.  Zeros past the rows and, in
   // dgrad, past the columns of dz.
-  const size_t dz_n = static_cast<size_t>(p.N) * p.E;
-  auto read_a = [&](int ks, uint4 (&v)[kAOps]) __attribute__((always_inline)) {
+  auto read_a = [&](int ks, int plane, uint4 (&v)[kAOps]) __attribute__((always_inline)) {
+    const uint16_t* dz = plane_of(plane);
     struct __attribute__((packed, aligned(2))) Chunk {
       uint32_t w[4];
     };
@@ -221,14 +234,16 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
 #pragma unroll
     for (int j = 0; j < kNB; ++j) acc[i][j] = f32x16_t{};
 
-  // ---- K loop.  Stage ks, two K steps of 16, fragments one step ahead of their MFMAs:
-  //   read step 1; multiply step 0; wait for stage ks + 1 and synchronise (every wave has now read
-  //   all of stage ks); load stage ks + 3 into its slot; read step 0 of stage ks + 1; multiply step 1
+  // ---- K loop.  Stage st (stage ks of a plane), two K steps of 16, fragments one step ahead of their MFMAs:
+  //   read step 1; multiply step 0; wait for stage st + 1 and synchronise (every wave has now read
+  //   all of stage st); load stage st + 3 into its slot; read step 0 of stage st + 1; multiply step 1
+  // With three planes slot sl is that of plane sl, and the other operand's stages go round the three slots
+  // by themselves: stage ks + 1 is loaded while plane 0 of stage ks is multiplied, into the place of ks - 2.
   struct Frags {
     uint4 a[kMB], b[kNB];
   };
-  auto read_frags = [&](int sl, int s, Frags& f) __attribute__((always_inline)) {
-    const uint32_t sb = lds0 + sl * C::kStage;
+  auto read_frags = [&](int sl, int bsl, int s, Frags& f) __attribute__((always_inline)) {
+    const uint32_t sb = lds0 + sl * C::kStage, bb = PLANES == 1 ? sb : lds0 + bsl * C::kStage;
 #pragma unroll
     for (int i = 0; i < kMB; ++i) {
       if constexpr (DGRAD)
@@ -237,7 +252,7 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
         f.a[i] = strided_frag<TM * 2>(sb + fo_a[i], s);
     }
 #pragma unroll
-    for (int j = 0; j < kNB; ++j) f.b[j] = strided_frag<kRbTN * 2>(sb + fo_b[j], s);
+    for (int j = 0; j < kNB; ++j) f.b[j] = strided_frag<kRbTN * 2>(bb + fo_b[j], s);
   };
   auto multiply = [&](int ks, int s, Frags& f) __attribute__((always_inline)) {
     if constexpr (DGRAD) {
@@ -278,46 +293,56 @@ __global__ __launch_bounds__(kRbThreads, 2) void router_grad_kernel(RbArgs p) {
   }
   uint4 va[kAOps];
   auto first_stage = [&](int st) __attribute__((always_inline)) {
-    load_stage(st, st);
+    const int ks = PLANES == 1 ? st : 0, plane = PLANES == 1 ? 0 : st;
+    load_stage(ks, plane, st, 0);
     if constexpr (!DMA) {
-      read_a(st, va);
+      read_a(ks, plane, va);
       put_a(st, va);
     }
   };
+  const int nst = nk * PLANES;
   first_stage(0);
-  if (nk > 1) first_stage(1);
-  if (nk > 2) first_stage(2);
-  if (nk > 2) wait_vmcnt<2 * kOps>();
+  if (nst > 1) first_stage(1);
+  if (nst > 2) first_stage(2);
+  if constexpr (PLANES > 1) wait_vmcnt<2 * kADma>();   // (stages 1 and 2 are planes of the same stage)
+  else if (nk > 2) wait_vmcnt<2 * kOps>();
   else if (nk > 1) wait_vmcnt<kOps>();
   else wait_vmcnt<0>();
   wait_lgkmcnt_all();
   block_barrier();
   Frags f0, f1;
-  read_frags(0, 0, f0);
-  int sl = 0;   // ring slot of stage ks
-  for (int ks = 0; ks < nk; ++ks) {
-    const bool next = ks + 1 < nk, load = ks + kRbSlots < nk;
+  read_frags(0, 0, 0, f0);
+  int sl = 0, ks = 0, bsl = 0;   // ring slot of stage st; its K stage; slot of the other operand's stage
+  for (int st = 0; st < nst; ++st) {
+    const bool next = st + 1 < nst, load = st + kRbSlots < nst;
+    const int ks3 = PLANES == 1 ? ks + kRbSlots : ks + 1;   // (stage st + 3: with planes, the same plane)
+    const int plane3 = PLANES == 1 ? 0 : sl;
     if constexpr (!DMA) {
-      if (load) read_a(ks + kRbSlots, va);
+      if (load) read_a(ks3, plane3, va);
     }
-    read_frags(sl, 1, f1);
+    read_frags(sl, bsl, 1, f1);
     __builtin_amdgcn_sched_barrier(0);
     multiply(ks, 0, f0);
-    const int sl1 = sl + 1 == kRbSlots ? 0 : sl + 1;
+    const int sl1 = sl + 1 == kRbSlots ? 0 : sl + 1, bsl3 = bsl + 1 == kRbSlots ? 0 : bsl + 1;
+    const bool turn = PLANES == 1 || sl1 == 0;   // stage st + 1 is another K stage
+    const int bsl1 = turn ? bsl3 : bsl;
     if (next) {
       wait_lgkmcnt_all();
-      if (ks + 2 < nk) wait_vmcnt<kOps>();
-      else wait_vmcnt<0>();
+      if (st + 2 >= nst) wait_vmcnt<0>();
+      else if (PLANES == 1 || sl == 1) wait_vmcnt<kOps>();   // stage st + 2 has loads of both operands
+      else wait_vmcnt<kADma>();
       block_barrier();
       if (load) {
-        load_stage(ks + kRbSlots, sl);
+        load_stage(ks3, plane3, sl, bsl3);
         if constexpr (!DMA) put_a(sl, va);
       }
-      read_frags(sl1, 0, f0);
+      read_frags(sl1, bsl1, 0, f0);
       __builtin_amdgcn_sched_barrier(0);
     }
     multiply(ks, 1, f1);
     sl = sl1;
+    bsl = bsl1;
+    if (turn) ++ks;
   }
 
   if constexpr (!DGRAD) {
@@ -525,6 +550,10 @@ __global__ __launch_bounds__(kRbThreads) void router_wgrad_sum_kernel(const floa
 // dz rows through registers wait in each stage, and more workgroups share the waits:
 //   N 4096, H 4096 (2048):  E 60  16.5 / 19.3 / 17.5    E 250  30.1 / 34.1 / 32.1
 //   N 8192, H 7168 (7168):  E 60  64.1 / 61.0 / 66.0    E 250  108.7 / 100.7 / 121.8
+// Three planes of dz follow the same rule:
+//   N 1024, H 7168 (896):   E 64  10.9 / 11.4 / 12.5    E 256  24.6 / 23.3 / 24.1
+//   N 4096, H 4096 (2048):  E 64  19.5 / 20.3 / 19.1    E 512  79 / 69 / 59
+//   N 8192, H 7168 (7168):  E 64  51 / 54 / 59          E 256  134 / 126 / 118
 int rb_dgrad_rows(int N, int E, int H, bool dma) {
   const long long t64 = static_cast<long long>((N + 63) / 64) * ((H + kRbTN - 1) / kRbTN);
   if (!dma) return t64 <= 4096 ? 64 : 128;
@@ -539,7 +568,8 @@ int rb_dgrad_rows(int N, int E, int H, bool dma) {
 // launch, the partial sums' way out and back, and the sum's batches of eight.  Workgroups beyond 256
 // take the CU's time from each other, so there are no more unless the tiles alone are.  dz rows that
 // come through registers wait for their loads in each stage: t is longer, and workgroups share the
-// waits.  Measured with the sum, us by S = 1 / 2 / 4 / 8 / 16 (64-row tiles to E 64, then 128, 256):
+// waits; so do three planes of dz, whose stages bring only dz rows two times of three.  Measured with
+// the sum, us by S = 1 / 2 / 4 / 8 / 16 (64-row tiles to E 64, then 128, 256):
 //   N 300,  H 7168, E 8     5.7 /  6.7 /  6.4 /  6.8        E 256  13.3 / 20.3 / 23.5 / 24.0
 //   N 1024, H 1024, E 8    10.9 /  9.1 /  7.3 /  6.4 /  6.7   E 256  22.7 / 18.3 / 15.4 / 16.2 / 19.5
 //   N 1024, H 7168, E 64   11.4 / 11.3 / 11.6 / 15.9 / 18.4   E 256  24.2 / 25.8 / 23.6 / 28.1 / 44.2
@@ -549,6 +579,9 @@ int rb_dgrad_rows(int N, int E, int H, bool dma) {
 // and by tile rows 64 / 128 / 256 with the best S of each:
 //   N 300,  H 2048, E 256   5.8 /  8.1 / 12.5     N 1000, H 7168, E 256  12.4 / 15.5 / 23.8
 //   N 8192, H 2048, E 256  24.1 / 22.1 / 26.6     N 8192, H 7168, E 256  89.1 / 60.9 / 55.5
+// Three planes, S = 4 / 8 / 16: N 8192, H 8192, E 32  77 / 46 / 42 (with 256 workgroups at most 60);
+//   N 8192, H 7168, 256-row tiles, E 256: 4 ranges 134, 8 ranges 103, 9 ranges 114;  E 128 (128 rows): 4 ranges 80, 9
+//   ranges 59;  N 1024, H 7168, E 64: 16.4 / 18.3;  N 300, H 2048, E 256: 1 range 11.9, 5 ranges 14.2.
 // From 90 MB of x on, 64-row tiles are bound by its reading: where 256 workgroups are not a whole
 // number of tiles, 512 fill the CUs better (N 8192, E 8, H 7168: 31 -> 27 us; H 5632: 24 -> 21; with
 // H 8192, 64 tiles, 256 take 29 and 512 30).
@@ -557,7 +590,7 @@ int rb_dgrad_rows(int N, int E, int H, bool dma) {
 struct RbSplit {
   int S, span, rows;
 };
-RbSplit rb_split(int N, int H, int E, bool bf16) {
+RbSplit rb_split(int N, int H, int E, bool bf16, int planes) {
   const int step = bf16 ? kRbKS : kF32KS, steps = (N - 1) / step + 1;
   const int n_tiles = bf16 ? (H + kRbTN - 1) / kRbTN : (H + kF32TN - 1) / kF32TN;
   auto tiles = [&](int rows) { return static_cast<long long>((E + rows - 1) / rows) * n_tiles; };
@@ -566,21 +599,21 @@ RbSplit rb_split(int N, int H, int E, bool bf16) {
   if (!bf16) {
     const int most = (steps + 1) / 2;
     S = at_most(512, rows) < most ? at_most(512, rows) : most;
-  } else if (E <= 64 && E % 8 == 0 && static_cast<long long>(N) * H >= 45000000 && tiles(64) * at_most(256, 64) <= 240) {
+  } else if (planes == 1 && E <= 64 && E % 8 == 0 && static_cast<long long>(N) * H >= 45000000 && tiles(64) * at_most(256, 64) <= 240) {
     rows = 64;
     S = at_most(512, rows);
   } else {
-    const bool dma = E % 8 == 0;
+    const bool waits = E % 8 != 0 || planes > 1;
     const float move = static_cast<float>(E) * static_cast<float>(H) * 8e-7f;
-    const float stage[2][3] = {{0.5f, 0.7f, 1.1f}, {0.25f, 0.33f, 0.5f}};
+    const float stage[2][3] = {{0.25f, 0.33f, 0.5f}, {0.5f, 0.7f, 1.1f}};
     const int groups[3] = {1024, 512, 512};
     float best = 0.0f;
     for (int i = 0; i < 3; ++i) {
-      const int r = 64 << i, most = at_most(dma ? 256 : groups[i], r);
+      const int r = 64 << i, most = at_most(waits ? groups[i] : 256, r);
       for (int c = 1; c <= most && c <= steps; ++c) {
         const float load = static_cast<float>(tiles(r)) * static_cast<float>(c) * (1.0f / 256);
-        const float t = stage[dma][i] * (load <= 1.0f ? 1.0f : (dma ? load : sqrtf(load)));
-        float us = static_cast<float>((steps + c - 1) / c) * t;
+        const float t = stage[waits][i] * (load <= 1.0f ? 1.0f : (waits ? sqrtf(load) : load));
+        float us = static_cast<float>((steps + c - 1) / c * planes) * t;
         if (c > 1) us += 2.0f + static_cast<float>(c + 3) * move + 0.5f * static_cast<float>((c + 7) / 8);
         if ((i == 0 && c == 1) || us < best) {
           best = us;
@@ -599,48 +632,45 @@ unsigned rb_grid(long long tiles) {
   return static_cast<unsigned>((tiles + kNumXcd - 1) / kNumXcd * kNumXcd);
 }
 
-template <bool DGRAD, int TM>
+template <bool DGRAD, int TM, int PLANES>
 hipError_t rb_launch(const RbArgs& p, bool dma, long long tiles, hipStream_t s) {
-  if (dma) hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, true>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
-  else hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, false>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+  if (dma)
+    hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, true, PLANES>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+  else if constexpr (!DGRAD || TM < 256)   // (a dgrad takes 256 tokens with 16-byte dz rows only)
+    hipLaunchKernelGGL((router_grad_kernel<DGRAD, TM, false, PLANES>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
+  else
+    return hipErrorNotSupported;
   return hipGetLastError();
 }
 
 bool rb_dma(const RbArgs& p) { return p.E % 8 == 0 && reinterpret_cast<uintptr_t>(p.dz) % 16 == 0; }
 
-template <bool DGRAD>
+template <bool DGRAD, int PLANES>
 hipError_t rb_run(const RbArgs& p, int tm, hipStream_t s) {
   const int rows = DGRAD ? p.N : p.E;
   const bool dma = rb_dma(p);
   const long long tiles = static_cast<long long>((rows + tm - 1) / tm) * ((p.H + kRbTN - 1) / kRbTN) * (DGRAD ? 1 : p.S);
-  if (tm == 256) {
-    if constexpr (DGRAD) {   // (256 tokens are taken with 16-byte dz rows only)
-      hipLaunchKernelGGL((router_grad_kernel<true, 256, true>), dim3(rb_grid(tiles)), dim3(kRbThreads), 0, s, p);
-      return hipGetLastError();
-    } else {
-      return rb_launch<DGRAD, 256>(p, dma, tiles, s);
-    }
-  }
-  if (tm == 128) return rb_launch<DGRAD, 128>(p, dma, tiles, s);
-  return rb_launch<DGRAD, 64>(p, dma, tiles, s);
+  if (tm == 256) return rb_launch<DGRAD, 256, PLANES>(p, dma, tiles, s);
+  if (tm == 128) return rb_launch<DGRAD, 128, PLANES>(p, dma, tiles, s);
+  return rb_launch<DGRAD, 64, PLANES>(p, dma, tiles, s);
 }
 
 }  // namespace
 
-size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16) {
+size_t router_wgrad_ws_bytes(int N, int H, int E, bool bf16, int planes) {
   if (N <= 0) return 0;
-  const RbSplit r = rb_split(N, H, E, bf16);
+  const RbSplit r = rb_split(N, H, E, bf16, planes);
   return r.S <= 1 ? 0 : (static_cast<size_t>(r.S) * E * H * sizeof(float) + 255) & ~static_cast<size_t>(255);
 }
 
-hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, int N, int E, int H, void* dw,
-                                     bool dw_f32, void* ws, hipStream_t s) {
-  const RbSplit r = N > 0 ? rb_split(N, H, E, bf16) : RbSplit{0, 0, 0};
+hipError_t launch_router_dense_wgrad(const void* dz, int planes, const void* x, bool bf16, int N, int E, int H,
+                                     void* dw, bool dw_f32, void* ws, hipStream_t s) {
+  const RbSplit r = N > 0 ? rb_split(N, H, E, bf16, planes) : RbSplit{0, 0, 0};
   RbArgs p = {dz, x, nullptr, r.S > 1 ? ws : dw, N, E, H, r.S, r.span, r.S > 1 || dw_f32 ? 1 : 0};
   if (r.S > 0) {
     hipError_t err = hipSuccess;
     if (bf16) {
-      err = rb_run<false>(p, r.rows, s);
+      err = planes == 3 ? rb_run<false, 3>(p, r.rows, s) : rb_run<false, 1>(p, r.rows, s);
     } else {
       hipLaunchKernelGGL(router_grad_f32_kernel<false>,
                          dim3((E + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN, r.S), dim3(kRbThreads), 0, s, p);
@@ -655,10 +685,11 @@ hipError_t launch_router_dense_wgrad(const void* dz, const void* x, bool bf16, i
   return hipGetLastError();
 }
 
-hipError_t launch_router_dense_dgrad(const void* dz, const void* w_r, bool bf16, int N, int E, int H, const void* rest,
-                                     void* dx, hipStream_t s) {
+hipError_t launch_router_dense_dgrad(const void* dz, int planes, const void* w_r, bool bf16, int N, int E, int H,
+                                     const void* rest, void* dx, hipStream_t s) {
   const RbArgs p = {dz, w_r, rest, dx, N, E, H, 1, 0, bf16 ? 0 : 1};
-  if (bf16) return rb_run<true>(p, rb_dgrad_rows(N, E, H, rb_dma(p)), s);
+  if (bf16 && planes == 3) return rb_run<true, 3>(p, rb_dgrad_rows(N, E, H, rb_dma(p)), s);
+  if (bf16) return rb_run<true, 1>(p, rb_dgrad_rows(N, E, H, rb_dma(p)), s);
   hipLaunchKernelGGL(router_grad_f32_kernel<true>, dim3((N + kF32TM - 1) / kF32TM, (H + kF32TN - 1) / kF32TN),
                      dim3(kRbThreads), 0, s, p);
   return hipGetLastError();

@@ -24,7 +24,7 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_BALANCE_LOSS, MOE_OP_DISPATCH_LAYOUT,
+from . import (MOE_BF16, MOE_BF16X3, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_BALANCE_LOSS, MOE_OP_DISPATCH_LAYOUT,
                MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM, MOE_OP_GROUPED_FFN, MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD,
                moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_backward, moe_dequantize_fp8,
                moe_dequantize_mxfp8, moe_dispatch_layout, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
@@ -409,9 +409,14 @@ class MoELayer:
             need("dx_s", (N, H), bf)
             need("dsw13", (1, 2 * I, H), dw_dtype)
             need("dsw2", (1, H, I), dw_dtype)
-        if self.balance_args is not None:   # the whole logit gradient (fp32 where the caller has the router)
-            need("dz_all", (N, E), bf if self.w_r is not None else torch.float32)
-            need_ws("wgrad_ws", moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, MOE_BF16))
+        if self.balance_args is not None and self.w_r is not None:
+            # the whole logit gradient, fp32 in three bf16 planes (the loss's part is often below half a bf16
+            # step of the gates', so one rounding to bf16 would lose it); the first rounded to bf16
+            need("dz_planes", (3, N, E), bf)
+            b["dz_all"] = b["dz_planes"][0]
+            need_ws("wgrad_ws", moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, MOE_BF16X3))
+        elif self.balance_args is not None:   # (the caller has the router)
+            need("dz_all", (N, E), torch.float32)
         if self.w_r is not None:
             if self.balance_args is None:
                 need("dz", (N, k), torch.float32)
@@ -422,8 +427,8 @@ class MoELayer:
 
     def _gradients(self) -> dict:
         """self.grads without the logit gradient of the other kind of forward (an earlier one's)."""
-        stale = "dz_all" if self.balance_args is None else "dz"
-        return {n: t for n, t in self.grads.items() if n != stale} if stale in self.grads else self.grads
+        stale = ("dz_all", "dz_planes") if self.balance_args is None else ("dz",)
+        return {n: t for n, t in self.grads.items() if n not in stale} if stale[0] in self.grads else self.grads
 
     def backward_steps(self, x: Optional[torch.Tensor], dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16,
                        d_loss: Optional[torch.Tensor] = None) -> list:
@@ -492,13 +497,14 @@ class MoELayer:
             ba, (_, counts, _, tokens) = self.balance_args, self.balance
             st.append(("logit_grad", lambda: moe_balance_loss_backward(
                 ba["z"], self.topk_idx, ba["alpha"], counts, tokens, bias=self.bias, seq_start=ba["seq_start"],
-                token_mask=ba["token_mask"], d_loss=d_loss, topk_gate=self.topk_gate, d_gate=b["dg"], dz=b["dz_all"])))
+                token_mask=ba["token_mask"], d_loss=d_loss, topk_gate=self.topk_gate, d_gate=b["dg"],
+                dz=b["dz_all"] if self.w_r is None else b["dz_planes"])))
         if self.w_r is not None:
             # sum_j dz_tj W_r[e_tj] (+ the shared expert's input gradient); dense: over all experts
             rest_r = rest
             st += [
-                ("router_bwd", lambda: moe_router_dense_wgrad(b["dz_all"], x, dw=b["dw_r"], ws=b["wgrad_ws"])),
-                ("router_dx", lambda: moe_router_dense_dgrad(b["dz_all"], self.w_r, rest=rest_r, dx=b["dx_r"])),
+                ("router_bwd", lambda: moe_router_dense_wgrad(b["dz_planes"], x, dw=b["dw_r"], ws=b["wgrad_ws"])),
+                ("router_dx", lambda: moe_router_dense_dgrad(b["dz_planes"], self.w_r, rest=rest_r, dx=b["dx_r"])),
             ] if dense else [
                 ("router_bwd", lambda: moe_router_backward(self.topk_gate, b["dg"], offsets, src_slot, x, b["dz"],
                                                            b["dw_r"])),
@@ -550,7 +556,9 @@ class MoELayer:
         pre-activations are the kept codes' values, h and the gates' gradient come from them
         (d_gate = <dy W_down, h>), and the expert outputs are not read.  After a forward with a
         balance loss its gradient times d_loss ([1] fp32, None: 1) joins the gates' in the logits'
-        gradient 'dz_all' [N, E], which then gives dW_r and the router's share of dx.
+        gradient, which then gives dW_r and the router's share of dx: 'dz_planes' [3, N, E], three bf16
+        planes whose sum is the fp32 gradient, the first of them 'dz_all' [N, E] (without w_r only 'dz_all',
+        in fp32).
         """
         steps = self.backward_steps(x, dy, dw_dtype, d_loss)
         if not (overlap_shared and self.shared):

@@ -60,7 +60,8 @@ typedef enum {
 typedef enum {
   MOE_F32 = 0,
   MOE_BF16 = 1,
-  MOE_FP8_E4M3 = 2 /* OCP e4m3fn: 1 sign, 4 exponent (bias 7), 3 mantissa bits, max 448 */
+  MOE_FP8_E4M3 = 2, /* OCP e4m3fn: 1 sign, 4 exponent (bias 7), 3 mantissa bits, max 448 */
+  MOE_BF16X3 = 3 /* three bf16 planes whose sum is an fp32 value (a dense logit gradient only) */
 } moe_dtype;
 
 /* Workspace query ids for moe_workspace_bytes(). */
@@ -546,7 +547,10 @@ moe_status moe_balance_loss(const float* z, const float* bias, const int32_t* to
  *   d_loss             [1] fp32: the gradient of what is minimised by the loss, or NULL (1).
  *   topk_gate, d_gate  [N, k] fp32 (moe_route's gates, moe_combine_backward's gradient), or
  *                      both NULL.
- *   dz                 [N, E] of dz_dt (MOE_F32 or MOE_BF16) out, every row written.
+ *   dz                 [N, E] of dz_dt (MOE_F32 or MOE_BF16) out, every row written.  MOE_BF16X3:
+ *                      [3, N, E] bf16, whose sum over the planes is the fp32 gradient digit for digit
+ *                      (to 2^-133; what is not finite stays so) and whose first plane is the gradient
+ *                      rounded to bf16: the loss's part is often below half a bf16 step of the gates'.
  */
 moe_status moe_balance_loss_backward(const float* z, const float* bias, const int32_t* topk_idx, int N, int E, int k,
                                      const int32_t* seq_start, int S, const uint8_t* token_mask, float alpha,
@@ -563,7 +567,8 @@ moe_status moe_balance_loss_backward(const float* z, const float* bias, const in
  *     dw[e, h] = sum_t dz[t, e] x[t, h],     dx[t, h] = sum_e dz[t, e] W_r[e, h] (+ rest[t, h])
  *
  *   dz [N, E], x [N, H], w_r [E, H], rest [N, H] or NULL and dx [N, H] of dt (MOE_F32 or
- *   MOE_BF16); dw [E, H] of dw_dt (MOE_F32 or MOE_BF16).
+ *   MOE_BF16); dw [E, H] of dw_dt (MOE_F32 or MOE_BF16).  dt MOE_BF16X3: dz [3, N, E] as
+ *   moe_balance_loss_backward writes it, an fp32 gradient beside x, w_r, rest and dx of bf16.
  *   ws  (wgrad) workspace of moe_workspace_bytes(MOE_OP_ROUTER_WGRAD, N, H, 0, E, 0, dt) bytes
  *       (may be 0: then ws may be NULL).
  * Sums are fp32 in a fixed order, one rounding at the end.  N == 0 writes dw's zeros.  Requires
