@@ -582,9 +582,16 @@ int rb_dgrad_rows(int N, int E, int H, bool dma) {
 // Three planes, S = 4 / 8 / 16: N 8192, H 8192, E 32  77 / 46 / 42 (with 256 workgroups at most 60);
 //   N 8192, H 7168, 256-row tiles, E 256: 4 ranges 134, 8 ranges 103, 9 ranges 114;  E 128 (128 rows): 4 ranges 80, 9
 //   ranges 59;  N 1024, H 7168, E 64: 16.4 / 18.3;  N 300, H 2048, E 256: 1 range 11.9, 5 ranges 14.2.
-// From 90 MB of x on, 64-row tiles are bound by its reading: where 256 workgroups are not a whole
-// number of tiles, 512 fill the CUs better (N 8192, E 8, H 7168: 31 -> 27 us; H 5632: 24 -> 21; with
-// H 8192, 64 tiles, 256 take 29 and 512 30).
+// From 90 MB of x on, 64-row tiles are bound by its reading (inputs that no cache holds): where 256 workgroups
+// are not a whole number of tiles, 512 fill the CUs better.  us with 256 / 512 / 1024 workgroups at most:
+//   N 8192,  H 5632 (44 tiles):  E 8  25.6 / 22.6 / 24.7    E 32  26.0 / 24.6 / 28.0    E 64  27.0 / 27.6 / 32.7
+//   N 8192,  H 6656 (52):        E 8  29.6 / 24.8 / 27.8    E 32  30.1 / 27.0 / 31.2    E 64  31.3 / 30.1 / 35.8
+//   N 6400,  H 7168 (56):        E 8  24.7 / 21.9 / 24.3    E 32  25.1 / 23.7 / 27.7    E 64  26.7 / 27.2 / 32.5
+//   N 16384, H 7168 (56):        E 8  52.8 / 45.9 / 49.8    E 32  53.2 / 48.5 / 53.6    E 64  54.6 / 53.3 / 58.9
+//   N 16384, H 5120 (40):        E 8  37.8 / 35.5 / 38.2    E 32  38.9 / 38.0 / 41.5    E 64  41.7 / 41.1 / 46.1
+// and where they are:
+//   N 16384, H 4096 (32):        E 8  30.5 / 30.8 / 34.5    E 32  31.3 / 32.7 / 37.4    E 64  33.2 / 35.2 / 40.6
+//   N 8192,  H 8192 (64):        E 8  28.7 / 30.0 / 33.0    E 32  29.6 / 32.7 / 37.3    E 64  31.4 / 37.3 / 44.1
 // fp32 (N 2048, E 128, H 8192, 256 / 512 / 1024 workgroups: 84 / 59 / 57 us; E 64, H 4096: 28 / 24 / 27):
 // 512, of at least two steps.
 struct RbSplit {
