@@ -22,7 +22,8 @@
 // Measured: N 8192, E 256, k 8: 5.0 us (8.4 MB of logits) + 6.4 us and, with the gates, 8.6 us
 // backward: latencies (loads, the ticket).  N 32768, E 160, 61 sequences: 13.4 + 5.9 and 15.6 us: still
 // latencies (groups of 16 lanes with three runs each, a third of the instructions a token, take 15.1
-// and 14.6 us in a row of calls against 15.7 and 13.9).
+// and 14.6 us in a row of calls against 15.7 and 13.9).  With dz in three planes the backward of N 8192,
+// E 256 takes 11.8 us (10 as a step of the layer).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -132,6 +133,8 @@ __device__ __forceinline__ void softmax_row(float (&p)[V * W], const float (&b)[
     sum += p[i];
   }
   sum = group_sum<G>(sum);
+  // (hardware reciprocal: within one ulp; a probability is two to three times as far off as with
+  // correctly rounded exponentials and quotients, near 1e-7, and errors of a mean average out)
   const float inv = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
   for (int i = 0; i < V * W; ++i) p[i] *= inv;

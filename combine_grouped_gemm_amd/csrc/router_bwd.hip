@@ -26,10 +26,11 @@
 //
 // fp32 operands run on v_mfma_f32_32x32x2_f32 (products and sums in fp32).
 //
-// Measured, bf16, N 8192, E 256, H 7168: wgrad 55 us with the sum of its 4 parts (117 MB of x, 29 MB of
-// partial sums out and back); dgrad with rest 76 us (53 us of it are rest and dx, as
-// with E = 8; about 0.1 us an expert comes on top).  With three planes of dz 113 and 120 us, 60 and 75 with E
-// 128; N 4096, E 8, H 4096: 17 and 15 us against 11 and 14.
+// Measured, bf16, N 8192, E 256, H 7168, over changing inputs: wgrad 55 us with the sum of its 4 parts (117 MB of
+// x, 29 MB of partial sums out and back; a bf16 library product 84); dgrad with rest 77 us (53 us of it are rest
+// and dx, as with E = 8; about 0.1 us an expert comes on top; the library's sum and product 100).  With three
+// planes of dz 128 and 149 us (113 and 120 on the same inputs again and again, 97 and 111 as steps of the layer);
+// N 4096, E 8, H 4096: 23 and 21 us against 12 and 11.
 #include <hip/hip_runtime.h>
 #include <limits.h>
 #include <math.h>

@@ -145,8 +145,9 @@ class MoELayer:
 
         weights: the routed, shared and router weights, fp8 scales included; workspace: the
         library's scratch buffers; activations: the forward's other buffers (logits, routes,
-        layout, permuted rows, h, expert outputs, y; the kept pre-activations, or the 8-bit codes
-        of both, once a training forward ran; the balance loss's).  After a backward also weight_grads and backward (its intermediates and
+        layout, permuted rows, h, expert outputs, y, all from construction on; the kept
+        pre-activations, and the 8-bit codes of both, each once a training forward of that kind ran;
+        the balance loss's).  After a backward also weight_grads and backward (its intermediates and
         workspaces).  The caller's input x is not the layer's and is not counted.
         """
         seen, out = set(), {"weights": 0, "activations": 0, "workspace": 0}
