@@ -330,7 +330,9 @@ class MoELayer:
         if z is None and self.w_r is None:
             raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
         if balance_alpha is not None:
-            _balance_args(self.z if z is None else z, self.topk_idx, self.bias, seq_start, token_mask)
+            S = _balance_args(self.z if z is None else z, self.topk_idx, self.bias, seq_start, token_mask)[3]
+            if S > 65535:
+                raise ValueError(f"a balance loss takes at most 65535 sequences, not {S}")
         self.keep8 = keep8
         self.save_au = bool(save_for_backward and not keep8 and self.fuse and not self.fp8)
         if self.save_au and self.au_all is None:

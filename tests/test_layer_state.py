@@ -43,7 +43,8 @@ def test_refused_forwards_leave_the_last_one_in_place():
         _refused(layer, torch.zeros(5, 128, dtype=torch.bfloat16), save_for_backward="mxfp8")
         _refused(layer, x.float(), save_for_backward="mxfp8")
         for bad in (dict(seq_start=torch.zeros(3, dtype=torch.int64)), dict(seq_start=torch.zeros(0, dtype=torch.int32)),
-                    dict(seq_start=torch.zeros(1, dtype=torch.int32)), dict(seq_start=torch.zeros(2, 2, dtype=torch.int32)),
+                    dict(seq_start=torch.zeros(1, dtype=torch.int32)), dict(seq_start=torch.zeros(65537, dtype=torch.int32)),
+                    dict(seq_start=torch.zeros(2, 2, dtype=torch.int32)),
                     dict(token_mask=torch.ones(5, dtype=torch.uint8)), dict(token_mask=torch.ones(6))):
             _refused(layer, x, balance_alpha=0.1, save_for_backward="mxfp8", **bad)
     layer = _layer(w_r=False)
