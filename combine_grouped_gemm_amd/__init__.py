@@ -30,6 +30,9 @@ __all__ = [
     "moe_expert_wgrad", "moe_router_backward", "moe_router_input_grad", "moe_stream_probe",
     "moe_balance_loss", "moe_balance_loss_backward", "moe_quantize_mxfp8", "moe_dequantize_mxfp8",
     "moe_expert_gate_up_mxfp8", "moe_swiglu_backward_mxfp8", "MOE_MX_BLOCK", "moe_router_dense_wgrad", "moe_router_dense_dgrad",
+    "MOE_OP_EXPERT_LINEAR", "MOE_OP_ACT_BACKWARD", "MOE_ACT_NONE", "MOE_ACT_RELU", "MOE_ACT_RELU2", "MOE_ACT_GELU",
+    "MOE_ACT_GELU_TANH", "MOE_ACT_SILU", "moe_expert_linear", "moe_expert_act_backward", "moe_combine_dropout",
+    "moe_combine_dropout_backward", "moe_dropout",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +41,8 @@ _HEADER = os.path.join(os.path.dirname(_HERE), "include", "moe.h")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_BF16X3 = range(4)
 (MOE_OP_DISPATCH_LAYOUT, MOE_OP_GROUPED_FFN, MOE_OP_EXPERT_GEMM, MOE_OP_ROUTER, MOE_OP_EXPERT_DGRAD,
- MOE_OP_BALANCE_LOSS, MOE_OP_ROUTER_WGRAD) = range(7)
+ MOE_OP_BALANCE_LOSS, MOE_OP_ROUTER_WGRAD, MOE_OP_EXPERT_LINEAR, MOE_OP_ACT_BACKWARD) = range(9)
+(MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_RELU2, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_SILU) = range(6)
 MOE_MX_BLOCK = 32                    # columns that share a scale of the kept 8-bit rows
 MOE_LAYOUT_SCRATCH_BYTES = 4 << 20   # the fixed count table of moe_dispatch_layout_noalloc
 
@@ -94,6 +98,11 @@ _SIGS = {
     "moe_dequantize_mxfp8": [_P, _P, ctypes.c_int64, _I, _I, _P, ctypes.c_int64, _P, _I, _P],
     "moe_expert_gate_up_mxfp8": [_P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P],
     "moe_swiglu_backward_mxfp8": [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P],
+    "moe_expert_linear": [_P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P],
+    "moe_expert_act_backward": [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _SZ, _P],
+    "moe_combine_dropout": [_P, _I, _I, _I, _I, _P, _P, _P, _P, ctypes.c_double, _P, _P, _I, _P],
+    "moe_combine_dropout_backward": [_P, _I, _I, _I, _I, _I, _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P],
+    "moe_dropout": [_P, _I, ctypes.c_int64, ctypes.c_double, _P, _P, _P, _I, _P],
     "moe_status_str": [_I],
     "moe_version": [],
 }
@@ -871,3 +880,213 @@ def moe_swiglu_backward_mxfp8(au_q: torch.Tensor, au_scale: torch.Tensor, dh: to
     _run("moe_swiglu_backward_mxfp8", dev, _ptr(au_q), _ptr(au_scale), _ptr(dh), _dt(dh), rows, I, slots,
          _ptr(send_pos), _ptr(topk_gate), _ptr(d_au), _ptr(h), _ptr(d_gate), _stream(dh))
     return d_au, h, d_gate
+
+
+# ------------------------------------------------------------------------------------------
+# experts with biases and other activations, dropout
+# ------------------------------------------------------------------------------------------
+
+_RNG = (torch.int64,) + ((torch.uint64,) if hasattr(torch, "uint64") else ())
+
+
+def _act_dtype(name, t):
+    if t.dtype not in _ACT:
+        raise ValueError(f"{name} must be float32 or bfloat16, not {t.dtype}")
+
+
+def _segments(offsets, E, device):
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"{E} experts need offsets [E + 1]")
+        return
+    _expect("offsets", offsets, (E + 1,), _I32, device)
+
+
+def moe_expert_linear(a: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                      offsets: Optional[torch.Tensor] = None, act: int = MOE_ACT_NONE, gated: bool = False,
+                      src_slot: Optional[torch.Tensor] = None, k: int = 1, residual: Optional[torch.Tensor] = None,
+                      rows: Optional[int] = None, out: Optional[torch.Tensor] = None,
+                      z: Optional[torch.Tensor] = None, want_z: bool = False, ws: Optional[torch.Tensor] = None):
+    """(out [rows, N], z [rows, Nw] or None): z = a W_e^T + b_e over each expert's rows, out = act(z) (gated:
+    act of z's first half times the second) plus the residual.  w [E, Nw, K] (Nw = N, gated 2N), bias [E, Nw]
+    fp32 or of a's type; src_slot: row r reads token src_slot[r] // k of a; offsets None: one expert, all rows."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K] and w [E, Nw, K]")
+    a_nrows, K = a.shape
+    E, Nw, _ = w.shape
+    dev = a.device
+    _act_dtype("a", a)
+    gated = bool(gated)
+    if gated and Nw % 2:
+        raise ValueError("a gated product needs an even number of weight rows")
+    N = Nw // 2 if gated else Nw
+    if rows is None:
+        rows = a_nrows if src_slot is None else src_slot.numel()
+    if rows < 0 or (src_slot is None and rows > a_nrows):
+        raise ValueError(f"rows must lie in 0 .. {a_nrows}, not {rows}")
+    _expect("w", w, (E, Nw, K), (a.dtype,), dev)
+    _expect("bias", bias, (E, Nw), (torch.float32, a.dtype), dev)
+    _segments(offsets, E, dev)
+    if src_slot is not None:
+        if src_slot.numel() < rows:
+            raise ValueError(f"src_slot must hold {rows} rows, not {src_slot.numel()}")
+        _expect("src_slot", src_slot, (src_slot.numel(),), _I32, dev)
+    _expect("residual", residual, (rows, N), (a.dtype,), dev)
+    if out is None:
+        out = torch.empty((rows, N), dtype=a.dtype, device=dev)
+    else:
+        _expect("out", out, (rows, N), (a.dtype,), dev)
+    if z is None:
+        z = torch.empty((rows, Nw), dtype=a.dtype, device=dev) if want_z else None
+    else:
+        _expect("z", z, (rows, Nw), (a.dtype,), dev)
+    dt = _dt(a)
+    if ws is None:
+        nbytes = lib().moe_workspace_bytes(MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    else:
+        nbytes = _ws_bytes(ws, dev)
+    _run("moe_expert_linear", dev, _ptr(a), dt, a_nrows, _ptr(src_slot), k, _ptr(offsets), E, rows, K, N, _ptr(w),
+         _ptr(bias), dt if bias is None else _dt(bias), act, gated, _ptr(residual), _ptr(out), _ptr(z), _ptr(ws),
+         nbytes, _stream(a))
+    return out, z
+
+
+def moe_expert_act_backward(d_out: torch.Tensor, z: Optional[torch.Tensor] = None,
+                            offsets: Optional[torch.Tensor] = None, act: int = MOE_ACT_NONE, gated: bool = False,
+                            E: Optional[int] = None, dz: Optional[torch.Tensor] = None,
+                            db: Optional[torch.Tensor] = None, db_dtype: torch.dtype = torch.float32,
+                            h: Optional[torch.Tensor] = None, want_dz: bool = True, want_db: bool = True,
+                            want_h: bool = False, ws: Optional[torch.Tensor] = None):
+    """(dz [rows, Nw], db [E, Nw], h [rows, N]; None where not wanted) of moe_expert_linear's z and the gradient
+    d_out [rows, N] of its out.  z None: act MOE_ACT_NONE, not gated (the bias gradient of a plain product)."""
+    if d_out.dim() != 2:
+        raise ValueError("d_out must be [rows, N]")
+    rows, N = d_out.shape
+    dev = d_out.device
+    _act_dtype("d_out", d_out)
+    gated = bool(gated)
+    Nw = 2 * N if gated else N
+    if E is None:
+        E = 1 if offsets is None else offsets.numel() - 1
+    _segments(offsets, E, dev)
+    _expect("z", z, (rows, Nw), (d_out.dtype,), dev)
+    if dz is None:
+        dz = torch.empty((rows, Nw), dtype=d_out.dtype, device=dev) if want_dz else None
+    else:
+        _expect("dz", dz, (rows, Nw), (d_out.dtype,), dev)
+    if db is None:
+        db = torch.empty((E, Nw), dtype=db_dtype, device=dev) if want_db else None
+    else:
+        _expect("db", db, (E, Nw), _ACT, dev)
+    if h is None:
+        h = torch.empty((rows, N), dtype=d_out.dtype, device=dev) if want_h else None
+    else:
+        _expect("h", h, (rows, N), (d_out.dtype,), dev)
+    if ws is not None:
+        nbytes = _ws_bytes(ws, dev)
+    else:
+        nbytes = lib().moe_workspace_bytes(MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0) if db is not None else 0
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _run("moe_expert_act_backward", dev, _ptr(z), _ptr(d_out), _dt(d_out), _ptr(offsets), E, rows, N, act, gated,
+         _ptr(dz), _ptr(db), MOE_F32 if db is None else _dt(db), _ptr(h), _ptr(ws), nbytes, _stream(d_out))
+    return dz, db, h
+
+
+def _slots(send_pos, topk_gate, N, k, device):
+    """k of the N tokens' slots after their checks."""
+    if topk_gate is not None:
+        if topk_gate.dim() != 2:
+            raise ValueError("topk_gate must be [N, k]")
+        k = topk_gate.shape[1]
+        _expect("topk_gate", topk_gate, (N, k), _F32, device)
+    elif k is None:
+        raise ValueError("k is needed without topk_gate")
+    if send_pos.numel() != N * k:
+        raise ValueError(f"send_pos must hold N * k = {N * k} rows, not {send_pos.numel()}")
+    _expect("send_pos", send_pos, send_pos.shape, _I32, device)
+    return k
+
+
+def moe_combine_dropout(expert_out: torch.Tensor, send_pos: torch.Tensor, topk_gate: Optional[torch.Tensor],
+                        p: float, rng: torch.Tensor, shared_out: Optional[torch.Tensor] = None,
+                        residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                        y_dtype: Optional[torch.dtype] = None, k: Optional[int] = None) -> torch.Tensor:
+    """y [N, H] = residual + D(moe_combine's sum); D drops with probability p (to 2^-16) from the counter-based
+    numbers of rng (device int64 [2]: seed, offset).  topk_gate None: weight 1 (pass k)."""
+    if expert_out.dim() != 2:
+        raise ValueError("expert_out must be [rows, H]")
+    H, dev = expert_out.shape[1], expert_out.device
+    _act_dtype("expert_out", expert_out)
+    if topk_gate is None and (k is None or k < 1):
+        raise ValueError("k is needed without topk_gate")
+    N = topk_gate.shape[0] if topk_gate is not None else send_pos.numel() // k
+    k = _slots(send_pos, topk_gate, N, k, dev)
+    _expect("rng", rng, (2,), _RNG, dev)
+    _expect("shared_out", shared_out, (N, H), (expert_out.dtype,), dev)
+    if y is None:
+        y = torch.empty((N, H), dtype=y_dtype or (expert_out.dtype if residual is None else residual.dtype), device=dev)
+    else:
+        _expect("y", y, (N, H), _ACT, dev)
+    _expect("residual", residual, (N, H), (y.dtype,), dev)
+    _run("moe_combine_dropout", dev, _ptr(expert_out), _dt(expert_out), N, H, k, _ptr(send_pos), _ptr(topk_gate),
+         _ptr(shared_out), _ptr(residual), p, _ptr(rng), _ptr(y), _dt(y), _stream(expert_out))
+    return y
+
+
+def moe_combine_dropout_backward(dy: torch.Tensor, send_pos: torch.Tensor, topk_gate: Optional[torch.Tensor],
+                                 expert_out: Optional[torch.Tensor], p: float, rng: torch.Tensor,
+                                 d_expert_out: Optional[torch.Tensor] = None, d_gate: Optional[torch.Tensor] = None,
+                                 d_shared: Optional[torch.Tensor] = None, want_shared: bool = False,
+                                 k: Optional[int] = None):
+    """(d_expert_out [rows, H], d_gate [N, k] fp32, d_shared [N, H]; None where not wanted) of
+    moe_combine_dropout with the same p and rng; the residual's gradient is dy.  Without expert_out there is no
+    d_gate (pass d_expert_out)."""
+    if dy.dim() != 2:
+        raise ValueError("dy must be [N, H]")
+    N, H = dy.shape
+    dev = dy.device
+    k = _slots(send_pos, topk_gate, N, k, dev)
+    like = expert_out if expert_out is not None else d_expert_out
+    if like is None:
+        raise ValueError("d_expert_out is needed without expert_out")
+    _act_dtype("expert_out", like)
+    if like.dim() != 2:
+        raise ValueError("expert_out must be [rows, H]")
+    rows, dt = like.shape[0], like.dtype
+    _expect("expert_out", expert_out, (rows, H), (dt,), dev)
+    _expect("dy", dy, (N, H), (torch.float32, dt), dev)
+    _expect("rng", rng, (2,), _RNG, dev)
+    if d_expert_out is None:
+        d_expert_out = torch.empty((rows, H), dtype=dt, device=dev)
+    else:
+        _expect("d_expert_out", d_expert_out, (rows, H), (dt,), dev)
+    if d_gate is not None:
+        if expert_out is None:
+            raise ValueError("d_gate needs expert_out")
+        _expect("d_gate", d_gate, (N, k), _F32, dev)
+    elif expert_out is not None:
+        d_gate = torch.empty((N, k), dtype=torch.float32, device=dev)
+    if d_shared is None:
+        d_shared = torch.empty((N, H), dtype=dt, device=dev) if want_shared else None
+    else:
+        _expect("d_shared", d_shared, (N, H), (dt,), dev)
+    _run("moe_combine_dropout_backward", dev, _ptr(dy), _dt(dy), _dt(like), N, H, k, _ptr(send_pos), _ptr(topk_gate),
+         _ptr(expert_out), p, _ptr(rng), _ptr(d_expert_out), _ptr(d_gate), _ptr(d_shared), _stream(dy))
+    return d_expert_out, d_gate, d_shared
+
+
+def moe_dropout(x: torch.Tensor, p: float, rng: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, y_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """y = residual + D(x), D as in moe_combine_dropout over x's elements; the gradient is moe_dropout(dy, p,
+    rng)."""
+    dev = x.device
+    _act_dtype("x", x)
+    _expect("rng", rng, (2,), _RNG, dev)
+    if y is None:
+        y = torch.empty(x.shape, dtype=y_dtype or (x.dtype if residual is None else residual.dtype), device=dev)
+    else:
+        _expect("y", y, x.shape, _ACT, dev)
+    _expect("residual", residual, x.shape, (y.dtype,), dev)
+    _run("moe_dropout", dev, _ptr(x), _dt(x), x.numel(), p, _ptr(rng), _ptr(residual), _ptr(y), _dt(y), _stream(x))
+    return y

@@ -20,7 +20,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["router.hip", "route.hip", "layout.hip", "permute.hip", "combine.hip", "grouped_gemm.hip", "grouped_gemm_stream.hip",
            "grouped_gemm_wide.hip", "grouped_gemm_bwd.hip", "backward.hip", "balance.hip", "checkpoint.hip",
-           "router_bwd.hip",
+           "router_bwd.hip", "linear.hip", "act_bwd.hip", "dropout.hip",
            "moe_api.cpp"]
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 

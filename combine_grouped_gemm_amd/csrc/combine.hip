@@ -17,28 +17,11 @@
 
 #include "moe_common.h"
 #include "moe_launch.h"
+#include "row_load.h"
 
 namespace moe {
 
 constexpr int kCombMaxThreads = 256;
-
-template <bool kEoF32>
-__device__ __forceinline__ void load8(const void* base, size_t row, int H, int c, float (&v)[8]) {
-  if (kEoF32) {
-    const float4* p = reinterpret_cast<const float4*>(base) + (row * H) / 4 + 2 * c;
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(base)[(row * H) / 8 + c];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(static_cast<uint16_t>(w[i] & 0xFFFFu));
-      v[2 * i + 1] = bf16_to_f32(static_cast<uint16_t>(w[i] >> 16));
-    }
-  }
-}
 
 template <int U, bool kEoF32, bool kGated>
 __device__ __forceinline__ void gather_sum(const void* eo, const int32_t* sp, const float* g, int H, int c,
@@ -106,57 +89,6 @@ __global__ __launch_bounds__(kCombMaxThreads) void combine_kernel(
       o.z = pack_bf16x2(acc[4], acc[5]);
       o.w = pack_bf16x2(acc[6], acc[7]);
       reinterpret_cast<uint4*>(y)[(static_cast<size_t>(t) * H) / 8 + c] = o;
-    }
-  }
-}
-
-// 8 columns of one row as loaded: one 16-byte word (bf16) or two (fp32)
-template <bool kEoF32>
-struct Raw8 {
-  uint4 w[kEoF32 ? 2 : 1];
-};
-
-// streaming 16-byte load: every expert row and shared row is read exactly once, so the
-// loads carry the non-temporal hint (measured: a 9-rows-read-per-row-written stream moves
-// ~10% more bytes per second with it)
-typedef uint32_t stream_word_t __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 load_stream(const uint4* p) {
-  const stream_word_t v = __builtin_nontemporal_load(reinterpret_cast<const stream_word_t*>(p));
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-
-// NT: the non-temporal hint (rows read once); otherwise plain loads (rows read by many
-// tokens, such as the router weight's rows in the router's input gradient)
-template <bool NT>
-__device__ __forceinline__ uint4 load_row16(const uint4* p) {
-  if (NT) return load_stream(p);
-  return *p;
-}
-
-template <bool kEoF32, bool NT>
-__device__ __forceinline__ void raw_load(const void* base, size_t row, int H, int c, Raw8<kEoF32>& r) {
-  if (kEoF32) {
-    const uint4* p = reinterpret_cast<const uint4*>(base) + (row * H) / 4 + 2 * c;
-    r.w[0] = load_row16<NT>(p);
-    r.w[kEoF32 ? 1 : 0] = load_row16<NT>(p + 1);
-  } else {
-    r.w[0] = load_row16<NT>(reinterpret_cast<const uint4*>(base) + (row * H) / 8 + c);
-  }
-}
-
-template <bool kEoF32>
-__device__ __forceinline__ void raw_values(const Raw8<kEoF32>& r, float (&v)[8]) {
-  if (kEoF32) {
-    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w,
-                           r.w[kEoF32 ? 1 : 0].x, r.w[kEoF32 ? 1 : 0].y, r.w[kEoF32 ? 1 : 0].z, r.w[kEoF32 ? 1 : 0].w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-  } else {
-    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_to_f32(static_cast<uint16_t>(w[i] & 0xFFFFu));
-      v[2 * i + 1] = bf16_to_f32(static_cast<uint16_t>(w[i] >> 16));
     }
   }
 }

@@ -1,0 +1,280 @@
+// Dropout at the layer's end, and its gradient:
+//   combine      y_t = residual_t + D(sum_{j<k} g_{t,j} expert_out[send_pos[t*k+j]] (+ shared_out_t))
+//   its gradient d = D(dy_t): d_expert_out[send_pos[s]] = g_s d, d_gate[s] = <d, expert_out[send_pos[s]]>, d_shared_t = d
+//   rows         y = residual + D(x)
+// D drops and scales element by element, from numbers that are computed where they are used (philox.h):
+// the element's place in y is its counter, so forward and backward agree without a stored mask.
+#include <type_traits>
+
+#include "moe_common.h"
+#include "moe_launch.h"
+#include "philox.h"
+#include "row_load.h"
+
+namespace moe {
+namespace {
+
+constexpr int kDropThreads = 256;
+
+// 8 values of group i (8 adjacent elements) of a matrix of fp32 or bf16
+template <bool F32>
+__device__ __forceinline__ void store_group(void* p, size_t i, const float (&v)[8]) {
+  if (F32) {
+    float4* q = reinterpret_cast<float4*>(p) + 2 * i;
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    reinterpret_cast<uint4*>(p)[i] =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_group(const void* p, size_t i) {
+  Raw8<F32> r;
+  if (F32) {
+    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i);
+    r.w[F32 ? 1 : 0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i + 1);
+  } else {
+    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + i);
+  }
+  return r;
+}
+
+// One workgroup takes a token and a span of its columns, a lane 8 columns; the rows are summed in slot
+// order in batches of KMAX whose loads go out together, then the shared row, in fp32.
+template <int KMAX, bool EO32, bool Y32>
+__global__ __launch_bounds__(kDropThreads) void combine_dropout_kernel(
+    const void* __restrict__ eo, int H, int k, const int32_t* __restrict__ send_pos, const float* __restrict__ gate,
+    const void* __restrict__ shared, const void* residual, DropArgs drop, void* y, int spans) {
+  const int t = blockIdx.x / spans, span = blockIdx.x % spans;
+  const DropState ds = drop_state(drop);
+  const int groups8 = H / 8;
+  const int c = span * static_cast<int>(blockDim.x) + threadIdx.x;
+  const int step = spans * static_cast<int>(blockDim.x);
+  const int32_t* sp = send_pos + static_cast<size_t>(t) * k;
+  const float* gp = gate + static_cast<size_t>(t) * k;
+  for (int g8 = c; g8 < groups8; g8 += step) {
+    const size_t at = static_cast<size_t>(t) * groups8 + g8;
+    Raw8<EO32> sh;
+    Raw8<Y32> re;
+    if (shared != nullptr) sh = load_group<EO32>(shared, at);
+    if (residual != nullptr) re = load_group<Y32>(residual, at);
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int j0 = 0; j0 < k; j0 += KMAX) {
+      Raw8<EO32> b[KMAX];
+      int r[KMAX];
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) r[j] = j0 + j < k ? sp[j0 + j] : -1;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j)
+        if (r[j] >= 0) b[j] = load_group<EO32>(eo, static_cast<size_t>(r[j]) * groups8 + g8);
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        if (r[j] < 0) continue;
+        const float g = gate != nullptr ? gp[j0 + j] : 1.0f;
+        float v[8];
+        raw_values<EO32>(b[j], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+      }
+    }
+    if (shared != nullptr) {
+      float v[8];
+      raw_values<EO32>(sh, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    }
+    drop8(ds, philox(ds, at), acc);
+    if (residual != nullptr) {
+      float v[8];
+      raw_values<Y32>(re, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+    }
+    store_group<Y32>(y, at, acc);
+  }
+}
+
+// One workgroup takes a token: a lane forms d for its 8 columns once and goes through the token's rows
+// in batches of KMAX (k > KMAX: d again for each batch); the rows' dot products are kept per lane and
+// summed over the workgroup at the end of a batch, in a fixed order.
+template <int KMAX, bool DT32, bool DY32>
+__global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int H, int k,
+                                                const int32_t* __restrict__ send_pos, const float* __restrict__ gate,
+                                                const void* __restrict__ eo, DropArgs drop, void* __restrict__ d_eo,
+                                                float* __restrict__ d_gate, void* __restrict__ d_shared) {
+  __shared__ float red[16][KMAX];
+  const int t = blockIdx.x;
+  const DropState ds = drop_state(drop);
+  const int groups8 = H / 8;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  const int32_t* sp = send_pos + static_cast<size_t>(t) * k;
+  for (int j0 = 0; j0 < k; j0 += KMAX) {
+    int r[KMAX];
+    float g[KMAX], dot[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      r[j] = j0 + j < k ? sp[j0 + j] : -1;
+      g[j] = gate != nullptr && j0 + j < k ? gate[static_cast<size_t>(t) * k + j0 + j] : 1.0f;
+      dot[j] = 0.0f;
+    }
+    for (int g8 = threadIdx.x; g8 < groups8; g8 += blockDim.x) {
+      const size_t at = static_cast<size_t>(t) * groups8 + g8;
+      const Raw8<DY32> rd = load_group<DY32>(dy, at);
+      Raw8<DT32> b[KMAX];
+      if (d_gate != nullptr) {
+#pragma unroll
+        for (int j = 0; j < KMAX; ++j)
+          if (r[j] >= 0) b[j] = load_group<DT32>(eo, static_cast<size_t>(r[j]) * groups8 + g8);
+      }
+      const uint4 w = philox(ds, at);
+      float d[8];
+      raw_values<DY32>(rd, d);
+      drop8(ds, w, d);
+      if (d_shared != nullptr && j0 == 0) store_group<DT32>(d_shared, at, d);
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        if (r[j] < 0) continue;
+        float v[8];
+        if (d_gate != nullptr) {
+          raw_values<DT32>(b[j], v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], v[i], dot[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = g[j] * d[i];
+        store_group<DT32>(d_eo, static_cast<size_t>(r[j]) * groups8 + g8, v);
+      }
+    }
+    if (d_gate == nullptr) continue;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) dot[j] += __shfl_xor(dot[j], off, 64);
+      if (lane == 0) red[wave][j] = dot[j];
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < KMAX && j0 + static_cast<int>(threadIdx.x) < k) {
+      float s = 0.0f;   // (a slot without a row: 0)
+      for (int w = 0; w < waves; ++w) s += red[w][threadIdx.x];
+      d_gate[static_cast<size_t>(t) * k + j0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+  }
+}
+
+// 8 elements a lane; the last n % 8 elements one by one
+template <bool X32, bool Y32>
+__global__ __launch_bounds__(kDropThreads) void dropout_kernel(const void* x, long long n, DropArgs drop,
+                                                               const void* residual,
+                                                               void* y) {
+  const DropState ds = drop_state(drop);
+  const long long i = static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x;
+  if (i < n / 8) {
+    const Raw8<X32> a = load_group<X32>(x, i);
+    Raw8<Y32> re;
+    if (residual != nullptr) re = load_group<Y32>(residual, i);
+    const uint4 w = philox(ds, i);
+    float v[8];
+    raw_values<X32>(a, v);
+    drop8(ds, w, v);
+    if (residual != nullptr) {
+      float q[8];
+      raw_values<Y32>(re, q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += q[j];
+    }
+    store_group<Y32>(y, i, v);
+  } else if (i == n / 8 && n % 8 != 0) {
+    const uint4 w = philox(ds, i);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int tail = static_cast<int>(n % 8);
+    auto get = [](const void* p, bool f32, long long at) {
+      return f32 ? reinterpret_cast<const float*>(p)[at] : bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[at]);
+    };
+    for (int j = 0; j < 8; ++j)
+      if (j < tail) v[j] = get(x, X32, 8 * i + j);
+    drop8(ds, w, v);
+    for (int j = 0; j < 8; ++j) {
+      if (j >= tail) break;
+      if (residual != nullptr) v[j] += get(residual, Y32, 8 * i + j);
+      if (Y32) reinterpret_cast<float*>(y)[8 * i + j] = v[j];
+      else reinterpret_cast<uint16_t*>(y)[8 * i + j] = f32_to_bf16(v[j]);
+    }
+  }
+}
+
+template <typename F>
+void two(bool a, bool b, F&& f) {
+  if (a && b) f(std::true_type{}, std::true_type{});
+  else if (a) f(std::true_type{}, std::false_type{});
+  else if (b) f(std::false_type{}, std::true_type{});
+  else f(std::false_type{}, std::false_type{});
+}
+
+}  // namespace
+
+hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int N, int H, int k, const int32_t* send_pos,
+                                  const float* gate, const void* shared, const void* residual, double p,
+                                  const uint64_t* rng, void* y, bool y_f32, hipStream_t s) {
+  const int groups8 = H / 8;
+  // few tokens: workgroups of one wave, as many as the row has passes
+  const int threads = N < 1024 ? 64 : groups8 % 256 == 0 || groups8 % 128 != 0 ? 256 : 128;
+  const int passes = (groups8 + threads - 1) / threads;
+  const int want = (8192 + N - 1) / N;
+  const int spans = want < passes ? want : passes;
+  const dim3 grid(static_cast<unsigned>(static_cast<long long>(N) * spans)), block(threads);
+  const DropArgs d = drop_args(p, rng);
+  two(eo_f32, y_f32, [&](auto a, auto b) {
+    constexpr bool A = decltype(a)::value, B = decltype(b)::value;
+    if (k <= 2)
+      hipLaunchKernelGGL((combine_dropout_kernel<2, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+                         residual, d, y, spans);
+    else if (k <= 4)
+      hipLaunchKernelGGL((combine_dropout_kernel<4, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+                         residual, d, y, spans);
+    else
+      hipLaunchKernelGGL((combine_dropout_kernel<8, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+                         residual, d, y, spans);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int N, int H, int k,
+                                           const int32_t* send_pos, const float* gate, const void* eo, double p,
+                                           const uint64_t* rng, void* d_eo, float* d_gate, void* d_shared,
+                                           hipStream_t s) {
+  const int groups8 = H / 8;
+  // few tokens: larger workgroups, up to the row's groups
+  int threads = 256;
+  while (threads < 1024 && threads < groups8 && N * (threads / 256) < 512) threads *= 2;
+  const dim3 grid(static_cast<unsigned>(N)), block(threads);
+  const DropArgs d = drop_args(p, rng);
+  two(f32, dy_f32, [&](auto a, auto b) {
+    constexpr bool A = decltype(a)::value, B = decltype(b)::value;
+    if (k <= 2)
+      hipLaunchKernelGGL((combine_dropout_backward_kernel<2, A, B>), grid, block, 0, s, dy, H, k, send_pos, gate, eo, d,
+                         d_eo, d_gate, d_shared);
+    else if (k <= 4)
+      hipLaunchKernelGGL((combine_dropout_backward_kernel<4, A, B>), grid, block, 0, s, dy, H, k, send_pos, gate, eo, d,
+                         d_eo, d_gate, d_shared);
+    else
+      hipLaunchKernelGGL((combine_dropout_backward_kernel<8, A, B>), grid, block, 0, s, dy, H, k, send_pos, gate, eo, d,
+                         d_eo, d_gate, d_shared);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_dropout(const void* x, bool x_f32, long long n, double p, const uint64_t* rng, const void* residual,
+                          void* y, bool y_f32, hipStream_t s) {
+  const long long lanes = (n + 7) / 8;
+  const dim3 grid(static_cast<unsigned>((lanes + kDropThreads - 1) / kDropThreads)), block(kDropThreads);
+  const DropArgs d = drop_args(p, rng);
+  two(x_f32, y_f32, [&](auto a, auto b) {
+    constexpr bool A = decltype(a)::value, B = decltype(b)::value;
+    hipLaunchKernelGGL((dropout_kernel<A, B>), grid, block, 0, s, x, n, d, residual, y);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -69,6 +69,25 @@ moe_status check_router_dense(moe_dtype dt, int N, int E, int H) {
   return MOE_OK;
 }
 
+bool act_type(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
+
+// null, or at a 16-byte boundary
+bool fits16(const void* p) { return p == nullptr || aligned16(p); }
+
+// Checks shared by the dropout entry points.
+bool drop_ok(double p, const uint64_t* rng) {
+  return p >= 0.0 && p <= 1.0 && rng != nullptr && (reinterpret_cast<uintptr_t>(rng) & 7u) == 0;   // (a NaN p fails)
+}
+
+// Checks shared by the experts' product and its activation's gradient.
+moe_status check_linear(const int32_t* offsets, int E, int rows, int N, int act, int gated) {
+  if (E < 1 || rows < 0 || N <= 0 || (offsets == nullptr && E != 1)) return MOE_ERR_INVALID_ARG;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU || (gated != 0 && gated != 1)) return MOE_ERR_INVALID_ARG;
+  if (E > MOE_MAX_EXPERTS || N % 8 != 0 || N >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0x7FFFFFFF - (1 << 16)) return MOE_ERR_UNSUPPORTED;   // (a row number plus a tile stays below 2^31)
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -110,6 +129,12 @@ size_t moe_workspace_bytes(int op, int N, int H, int I, int E, int k, int a_dt) 
     case MOE_OP_ROUTER_WGRAD:
       if (E < 1 || N == 0 || H <= 0) return 0;
       return moe::router_wgrad_ws_bytes(N, H, E, a_dt == MOE_BF16 || a_dt == MOE_BF16X3, dz_planes(a_dt));
+    case MOE_OP_EXPERT_LINEAR:   // (I: the weight rows)
+      if (E < 1 || N == 0 || H <= 0 || I <= 0) return 0;
+      return moe::expert_linear_ws_bytes(N, H, I, E, a_dt == MOE_F32);
+    case MOE_OP_ACT_BACKWARD:   // (I: the columns of z)
+      if (E < 1 || N == 0 || I <= 0) return 0;
+      return moe::act_backward_ws_bytes(N, I, E);
     default:
       return 0;
   }
@@ -633,6 +658,93 @@ moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scal
   if (!aligned16(au_q) || !aligned16(dh) || !aligned16(d_au) || !aligned16(h)) return MOE_ERR_INVALID_ARG;
   return hip_status(moe::launch_swiglu_backward_mx(au_q, au_scale, dh, dt == MOE_F32, rows, I, slots, send_pos,
                                                    topk_gate, d_au, h, d_gate, stream));
+}
+
+// ---- experts with biases, dropout
+
+moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int32_t* src_slot, int k,
+                             const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,
+                             moe_dtype bias_dt, moe_act act, int gated, const void* residual, void* out, void* z,
+                             void* ws, size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_linear(offsets, E, rows, N, act, gated);
+  if (st != MOE_OK) return st;
+  if (K <= 0 || (src_slot != nullptr && (k < 1 || a_nrows < 0))) return MOE_ERR_INVALID_ARG;
+  if (!act_type(dt) || (bias != nullptr && bias_dt != MOE_F32 && bias_dt != dt)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 != 0 || K >= (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (src_slot != nullptr && static_cast<long long>(a_nrows) * K * dtype_bytes(dt) >= (1ll << 32) - 4096)
+    return MOE_ERR_UNSUPPORTED;   // (32-bit offsets into the gathered operand)
+  const int Nw = gated ? 2 * N : N;
+  if (rows == 0) return MOE_OK;
+  if (!moe::expert_linear_grid_fits(rows, N, E)) return MOE_ERR_UNSUPPORTED;
+  if (a == nullptr || w == nullptr || out == nullptr || (src_slot != nullptr && a_nrows == 0)) return MOE_ERR_INVALID_ARG;
+  const size_t need = moe::expert_linear_ws_bytes(rows, K, Nw, E, dt == MOE_F32);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!aligned16(a) || !aligned16(w) || !aligned16(out) || !fits16(bias) || !fits16(residual) || !fits16(z) ||
+      (need > 0 && !aligned16(ws)))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_expert_linear(a, dt == MOE_F32, a_nrows, src_slot, k, offsets, E, rows, K, N, w, bias,
+                                              bias_dt == MOE_F32, act, gated != 0, residual, out, z, ws, stream));
+}
+
+moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype dt, const int32_t* offsets, int E,
+                                   int rows, int N, moe_act act, int gated, void* dz, void* db, moe_dtype db_dt,
+                                   void* h, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_linear(offsets, E, rows, N, act, gated);
+  if (st != MOE_OK) return st;
+  if (!act_type(dt) || (db != nullptr && !act_type(db_dt))) return MOE_ERR_UNSUPPORTED;
+  if (dz == nullptr && db == nullptr && h == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!fits16(db)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0 && db == nullptr) return MOE_OK;
+  if (rows > 0) {
+    const bool plain = act == MOE_ACT_NONE && gated == 0;
+    if (d_out == nullptr || (z == nullptr && (!plain || h != nullptr))) return MOE_ERR_INVALID_ARG;
+    const size_t need = db != nullptr ? moe::act_backward_ws_bytes(rows, gated ? 2 * N : N, E) : 0;
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+    if (!aligned16(d_out) || !fits16(z) || !fits16(dz) || !fits16(h) || (need > 0 && !aligned16(ws)))
+      return MOE_ERR_INVALID_ARG;
+  }
+  return hip_status(moe::launch_act_backward(z, d_out, dt == MOE_F32, offsets, E, rows, N, act, gated != 0, dz, db,
+                                             db_dt == MOE_F32, h, ws, stream));
+}
+
+moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, int H, int k, const int32_t* send_pos,
+                               const float* topk_gate, const void* shared_out, const void* residual, double p,
+                               const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream) {
+  if (N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
+  if (!act_type(eo_dt) || !act_type(y_dt)) return MOE_ERR_UNSUPPORTED;
+  if (k > MOE_MAX_TOPK || N >= kMaxRowsPerLaunch || H % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  if (N == 0) return MOE_OK;
+  if (expert_out == nullptr || send_pos == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(expert_out) || !aligned16(y) || !fits16(shared_out) || !fits16(residual)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine_dropout(expert_out, eo_dt == MOE_F32, N, H, k, send_pos, topk_gate, shared_out,
+                                                residual, p, rng, y, y_dt == MOE_F32, stream));
+}
+
+moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int N, int H, int k,
+                                        const int32_t* send_pos, const float* topk_gate, const void* expert_out,
+                                        double p, const uint64_t* rng, void* d_expert_out, float* d_gate,
+                                        void* d_shared, hipStream_t stream) {
+  if (N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
+  if (!act_type(dt) || (dy_dt != MOE_F32 && dy_dt != dt)) return MOE_ERR_UNSUPPORTED;
+  if (k > MOE_MAX_TOPK || N >= kMaxRowsPerLaunch || H % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  if (N == 0) return MOE_OK;
+  if (dy == nullptr || send_pos == nullptr || d_expert_out == nullptr || (expert_out == nullptr && d_gate != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(d_expert_out) || !fits16(expert_out) || !fits16(d_shared)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine_dropout_backward(dy, dy_dt == MOE_F32, dt == MOE_F32, N, H, k, send_pos,
+                                                         topk_gate, expert_out, p, rng, d_expert_out, d_gate, d_shared,
+                                                         stream));
+}
+
+moe_status moe_dropout(const void* x, moe_dtype x_dt, int64_t n, double p, const uint64_t* rng, const void* residual,
+                       void* y, moe_dtype y_dt, hipStream_t stream) {
+  if (n < 0 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
+  if (!act_type(x_dt) || !act_type(y_dt) || n >= (1ll << 41)) return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (x == nullptr || y == nullptr || !aligned16(x) || !aligned16(y) || !fits16(residual)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_dropout(x, x_dt == MOE_F32, n, p, rng, residual, y, y_dt == MOE_F32, stream));
 }
 
 }  // extern "C"

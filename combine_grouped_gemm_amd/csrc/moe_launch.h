@@ -84,6 +84,29 @@ hipError_t launch_swiglu_backward_mx(const uint8_t* au, const uint8_t* au_scale,
                                      int I, int slots, const int32_t* send_pos, const float* gate, void* d_au, void* h,
                                      float* d_gate, hipStream_t s);
 
+// experts with biases (linear.hip, act_bwd.hip); src_slot, offsets, bias, residual, z, dz, db, h may be null
+bool expert_linear_grid_fits(int rows, int N, int E);
+size_t expert_linear_ws_bytes(int rows, int K, int Nw, int E, bool f32);
+hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int32_t* src_slot, int k,
+                                const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,
+                                bool bias_f32, int act, bool gated, const void* residual, void* out, void* z, void* ws,
+                                hipStream_t s);
+size_t act_backward_ws_bytes(int rows, int Nw, int E);
+hipError_t launch_act_backward(const void* z, const void* d_out, bool f32, const int32_t* offsets, int E, int rows,
+                               int N, int act, bool gated, void* dz, void* db, bool db_f32, void* h, void* ws,
+                               hipStream_t s);
+
+// dropout (dropout.hip); gate, shared, residual, d_gate (and then eo) and d_shared may be null
+hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int N, int H, int k, const int32_t* send_pos,
+                                  const float* gate, const void* shared, const void* residual, double p,
+                                  const uint64_t* rng, void* y, bool y_f32, hipStream_t s);
+hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int N, int H, int k,
+                                           const int32_t* send_pos, const float* gate, const void* eo, double p,
+                                           const uint64_t* rng, void* d_eo, float* d_gate, void* d_shared,
+                                           hipStream_t s);
+hipError_t launch_dropout(const void* x, bool x_f32, long long n, double p, const uint64_t* rng, const void* residual,
+                          void* y, bool y_f32, hipStream_t s);
+
 size_t gemm_tile_cap(int rows, int E);
 size_t gemm_schedule_bytes(int rows, int E);
 // the fp8 gate/up's bf16 copy of its activations, kept after the schedule (rows x K)

@@ -72,8 +72,21 @@ typedef enum {
   MOE_OP_ROUTER = 3,      /* moe_router_logits: fp32 partial sums (N, H, E, a_dt = x_dt) */
   MOE_OP_EXPERT_DGRAD = 4, /* moe_expert_dgrad: tile schedule (N = rows, E)              */
   MOE_OP_BALANCE_LOSS = 5, /* moe_balance_loss: partial sums (N, E, k = S sequences)     */
-  MOE_OP_ROUTER_WGRAD = 6 /* moe_router_dense_wgrad: fp32 partial sums (N, H, E, a_dt)   */
+  MOE_OP_ROUTER_WGRAD = 6, /* moe_router_dense_wgrad: fp32 partial sums (N, H, E, a_dt)  */
+  MOE_OP_EXPERT_LINEAR = 7, /* moe_expert_linear: fp32 partial sums (N = rows, H = K, I = weight rows, E, a_dt) */
+  MOE_OP_ACT_BACKWARD = 8 /* moe_expert_act_backward: partial bias sums (N = rows, I = columns of z, E) */
 } moe_op;
+
+/* Activations of moe_expert_linear: act(x) = x; max(x, 0); max(x, 0)^2; x Phi(x), Phi the normal
+ * distribution function; x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2; x / (1 + exp(-x)). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_RELU2 = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4,
+  MOE_ACT_SILU = 5
+} moe_act;
 
 /* Limits of this implementation. */
 #define MOE_MAX_EXPERTS 1024
@@ -660,6 +673,130 @@ moe_status moe_expert_gate_up_mxfp8(const void* x, moe_dtype x_dt, int N, const 
 moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scale, const void* dh, moe_dtype dt,
                                      int rows, int I, int slots, const int32_t* send_pos, const float* topk_gate,
                                      void* d_au, void* h, float* d_gate, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Experts with biases and other activations, and a dropped-out sum with the residual stream.
+ *
+ *   forward:   moe_expert_linear (src_slot, act, z kept)   h, z
+ *              moe_expert_linear (offsets)                 expert outputs
+ *              moe_combine_dropout (residual)              y
+ *   backward:  moe_combine_dropout_backward                d_expert_out, d_gate
+ *              moe_expert_act_backward (MOE_ACT_NONE)      the second product's bias gradient
+ *              moe_expert_dgrad                            d_h
+ *              moe_expert_act_backward                     dz, the first product's bias gradient, h
+ *              moe_expert_wgrad (twice), moe_expert_dgrad  weight gradients, the slots' input gradients
+ *              moe_combine (gates = NULL)                  the tokens' input gradient
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * moe_expert_linear -- the experts' matrix product with bias, activation and residual.
+ *
+ * Definition: "MoE part 4" page, section 2 (one launch for many expert GEMMs with differing row
+ * counts) and section 4.1 (an expert is FC1 -> activation -> FC2), for experts whose products
+ * have biases.  For each expert e and its rows r in [offsets[e], offsets[e+1]):
+ *
+ *     z[r]   = a[r'] W_e^T + b_e
+ *     out[r] = act(z[r]) (+ residual[r])                                  (gated == 0)
+ *     out[r] = act(z[r, 0 .. N-1]) * z[r, N .. 2N-1] (+ residual[r])      (gated == 1)
+ *
+ *   a         [rows, K] of dt (MOE_F32 or MOE_BF16): r' = r, a_nrows is ignored.  With src_slot
+ *             (device [rows] int32, from moe_dispatch_layout): [a_nrows, K] tokens and
+ *             r' = src_slot[r] / k, clamped into [0, a_nrows).
+ *   offsets   [E + 1] int32, non-decreasing; rows outside [offsets[0], offsets[E]) are not
+ *             computed and stay as they are.  NULL: E must be 1, and all rows are its.
+ *   w         [E, Nw, K] of dt, Nw = N (gated: 2N, the activated half first).
+ *   bias      [E, Nw] of bias_dt (MOE_F32, or dt), or NULL.
+ *   residual  [rows, N] of dt, or NULL; added after the activation.
+ *   out       [rows, N] of dt; may be residual.
+ *   z         [rows, Nw] of dt: the pre-activations for moe_expert_act_backward, or NULL.
+ *   ws        workspace of moe_workspace_bytes(MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt) bytes
+ *             (may be 0: then ws may be NULL).
+ * Sums are fp32 in a fixed order; out comes from the unrounded z, with one rounding.  Requires
+ * K % 8 == 0 and N % 8 == 0, K < 2^20, N < 2^24 and rows < 2^31 - 2^16, with src_slot a_nrows * K * sizeof(dt) <
+ * 2^32 - 4096 (MOE_ERR_UNSUPPORTED otherwise); 16-byte aligned a, w, bias, residual, out, z, ws.
+ */
+moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int32_t* src_slot, int k,
+                             const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,
+                             moe_dtype bias_dt, moe_act act, int gated, const void* residual, void* out, void* z,
+                             void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_expert_act_backward -- the gradients of moe_expert_linear's activation and biases.
+ *
+ * Definition: the chain rule on moe_expert_linear, d_out the gradient of out:
+ *
+ *     dz[r] = d_out[r] act'(z[r])                                           (gated == 0)
+ *     dz[r, 0 .. N-1] = d_out[r] u act'(g),  dz[r, N .. 2N-1] = d_out[r] act(g)    (gated == 1;
+ *                       g, u the halves of z[r])
+ *     db[e] = sum of dz[r] over expert e's rows,   h[r] = moe_expert_linear's out of z[r] without residual
+ *
+ *   z         [rows, Nw] of dt as moe_expert_linear kept it; NULL when act is MOE_ACT_NONE and
+ *             gated is 0 (then h must be NULL).
+ *   d_out     [rows, N] of dt.
+ *   offsets, E   as given to moe_expert_linear.
+ *   dz [rows, Nw], h [rows, N] of dt out, or NULL: rows of no expert are left as they are.
+ *   db        [E, Nw] of db_dt (MOE_F32 or MOE_BF16) out, or NULL; zeros for an expert without rows.
+ *   ws        moe_workspace_bytes(MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0) bytes (not read when db is NULL).
+ * max(x, 0) has slope 0 at 0.  db sums the unrounded dz in fp32 in a fixed order.  Requires N % 8 ==
+ * 0, N < 2^24, rows < 2^31 - 2^16; 16-byte aligned arrays.  dz, db and h not all NULL.
+ */
+moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype dt, const int32_t* offsets, int E,
+                                   int rows, int N, moe_act act, int gated, void* dz, void* db, moe_dtype db_dt,
+                                   void* h, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * moe_combine_dropout -- combine, with dropout and the residual stream.
+ *
+ * Definition: "EP / DeepEP explanation" page, section 2 (y_t), dropped out:
+ *
+ *     y_t = residual_t + D(sum_{j<k} g_{t,j} expert_out[send_pos[t*k+j]] (+ shared_out_t))
+ *
+ * D keeps element i = t H + h where its number is at least c = floor(65536 p + 1/2) and multiplies it
+ * by 65536 / (65536 - c); the others become 0, whatever they held.  The numbers are 16 bits: element i takes half
+ * i % 8 (low halves first) of the four words of Philox 4x32-10 with counter (i / 8, offset) and key
+ * seed, each as two 32-bit words, low first.  So the mask depends on rng and the place alone.
+ *   expert_out ... shared_out  as for moe_combine (topk_gate NULL: weight 1).
+ *   residual   [N, H] of y_dt, or NULL.
+ *   p          dropout probability in [0, 1]; 1 drops everything.
+ *   rng        device [2] uint64: seed, offset, read when the work runs.  The caller gives every
+ *              call that shall draw anew another offset.
+ *   y          [N, H] of y_dt out; may be residual.
+ * The sum is fp32 in slot order, then the shared row, dropout, the residual; one rounding.  Requires what
+ * moe_combine does, residual included; rng 8-byte aligned.
+ */
+moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, int H, int k, const int32_t* send_pos,
+                               const float* topk_gate, const void* shared_out, const void* residual, double p,
+                               const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream);
+
+/*
+ * moe_combine_dropout_backward -- the gradients of moe_combine_dropout (residual's is dy).
+ *
+ * Definition: the chain rule, with d_t = D(dy_t) of the same p and rng:
+ *
+ *     d_expert_out[send_pos[s]] = g_s d_t,   d_gate[s] = <d_t, expert_out[send_pos[s]]>,   d_shared_t = d_t
+ *
+ *   dy         [N, H] of dy_dt (MOE_F32, or dt).
+ *   expert_out, d_expert_out  [rows, H] of dt (MOE_F32 or MOE_BF16); rows that no slot names are left
+ *              as they are.  expert_out may be NULL when d_gate is.
+ *   topk_gate  [N, k] fp32, or NULL (1).
+ *   d_gate     [N, k] fp32 out (0 for a slot without a row), or NULL.
+ *   d_shared   [N, H] of dt out, or NULL.
+ * Dot products are fp32 in a fixed order.  Requires H % 8 == 0; 16-byte aligned arrays.
+ */
+moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int N, int H, int k,
+                                        const int32_t* send_pos, const float* topk_gate, const void* expert_out,
+                                        double p, const uint64_t* rng, void* d_expert_out, float* d_gate,
+                                        void* d_shared, hipStream_t stream);
+
+/*
+ * moe_dropout -- y = residual + D(x), D as in moe_combine_dropout over n elements; its gradient is
+ * the same call on dy without a residual.
+ *
+ *   x [n] of x_dt, residual [n] of y_dt or NULL, y [n] of y_dt out (MOE_F32 or MOE_BF16); y may be x (of
+ *   one type) or residual.  p, rng as for moe_combine_dropout.  Requires n < 2^41; 16-byte aligned arrays.
+ */
+moe_status moe_dropout(const void* x, moe_dtype x_dt, int64_t n, double p, const uint64_t* rng, const void* residual,
+                       void* y, moe_dtype y_dt, hipStream_t stream);
 
 /*
  * moe_workspace_bytes -- bytes of workspace `op` needs for these sizes (0 if none).

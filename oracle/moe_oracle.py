@@ -634,3 +634,126 @@ def kept_swiglu_backward(au: np.ndarray, dh: np.ndarray, send_pos=None, gates=No
         hg[r] = g[s] * h
         dg[s] = float(dh[r] @ h)
     return d_au, hg, dg
+
+
+# --------------------------------------------------------------------------------------
+# experts with biases and other activations
+# --------------------------------------------------------------------------------------
+
+def _normal_cdf(x):
+    from scipy.special import erfc
+    return 0.5 * erfc(-x / np.sqrt(2.0))   # (1 + erf loses its digits far below 0)
+
+
+def _gelu_tanh_inner(x):
+    return np.sqrt(2.0 / np.pi) * (x + 0.044715 * x ** 3)
+
+
+ACTIVATIONS = {
+    "none": lambda x: x,
+    "relu": lambda x: np.maximum(x, 0.0),
+    "relu2": lambda x: np.maximum(x, 0.0) ** 2,
+    "gelu": lambda x: x * _normal_cdf(x),
+    "gelu_tanh": lambda x: x / (1.0 + np.exp(-2.0 * _gelu_tanh_inner(x))),   # ((1 + tanh v) / 2)
+    "silu": lambda x: x / (1.0 + np.exp(-x)),
+}
+
+ACTIVATION_SLOPES = {
+    "none": np.ones_like,
+    "relu": lambda x: (x > 0).astype(np.float64),
+    "relu2": lambda x: 2.0 * np.maximum(x, 0.0),
+    "gelu": lambda x: _normal_cdf(x) + x * np.exp(-0.5 * x * x) / np.sqrt(2.0 * np.pi),
+    "gelu_tanh": lambda x: (lambda e: 1.0 / (1.0 + e) + x * e / (1.0 + e) ** 2 * 2.0 * np.sqrt(2.0 / np.pi)
+                            * (1.0 + 3 * 0.044715 * x * x))(np.exp(-2.0 * _gelu_tanh_inner(x))),
+    "silu": lambda x: (1.0 + np.exp(-x) * (1.0 + x)) / (1.0 + np.exp(-x)) ** 2,
+}
+
+
+def expert_linear(a, offsets, w, bias=None, act="none", gated=False, residual=None, tokens=None):
+    """(out, z) of z[r] = a[r'] W_e^T + b_e over every expert's rows (r' = tokens[r] if given); rows of no
+    expert are NaN."""
+    rows = len(a) if tokens is None else len(tokens)
+    E, Nw, _ = w.shape
+    N = Nw // 2 if gated else Nw
+    z = np.full((rows, Nw), np.nan)
+    for e in range(E):
+        for r in range(offsets[e], offsets[e + 1]):
+            z[r] = w[e] @ a[r if tokens is None else tokens[r]] + (0 if bias is None else bias[e])
+    h = ACTIVATIONS[act](z[:, :N]) * (z[:, N:] if gated else 1.0)
+    return (h if residual is None else h + residual), z
+
+
+def expert_act_backward(z, d_out, offsets, act="none", gated=False):
+    """(dz, db, h) of expert_linear's z for the gradient d_out of its out."""
+    N = d_out.shape[1]
+    f, slope = ACTIVATIONS[act], ACTIVATION_SLOPES[act]
+    if gated:
+        g, u = z[:, :N], z[:, N:]
+        dz, h = np.concatenate([d_out * u * slope(g), d_out * f(g)], axis=1), f(g) * u
+    else:
+        dz, h = d_out * slope(z), f(z)
+    db = np.stack([dz[offsets[e]:offsets[e + 1]].sum(axis=0) for e in range(len(offsets) - 1)])
+    return dz, db, h
+
+
+# --------------------------------------------------------------------------------------
+# dropout from a counter-based generator (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3")
+# --------------------------------------------------------------------------------------
+
+def philox(counter, key, rounds=10):
+    """The four 32-bit words of Philox 4x32 for counter (4 words) and key (2 words), in Python integers."""
+    c, k = list(counter), list(key)
+    for _ in range(rounds):
+        p, q = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [(q >> 32) ^ c[1] ^ k[0], q & 0xFFFFFFFF, (p >> 32) ^ c[3] ^ k[1], p & 0xFFFFFFFF]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return c
+
+
+def dropout_numbers(seed, offset, n):
+    """The 16-bit number of each of n elements."""
+    out = []
+    halves = lambda v: (v & 0xFFFFFFFF, v >> 32)  # noqa: E731
+    for i in range((n + 7) // 8):
+        for w in philox(halves(i) + halves(offset % 2 ** 64), halves(seed % 2 ** 64)):
+            out += [w & 0xFFFF, w >> 16]
+    return np.array(out[:n], np.int64)
+
+
+def dropout_mask(p, seed, offset, n):
+    """What each of n elements is multiplied by: 0 or 65536 / (65536 - c), c = floor(65536 p + 1/2)."""
+    c = int(np.floor(65536.0 * p + 0.5))
+    keep = dropout_numbers(seed, offset, n) >= c
+    return np.where(keep, 65536.0 / (65536 - c) if c < 65536 else 0.0, 0.0)
+
+
+def combine_dropout(expert_out, send_pos, gates, p, seed, offset, shared=None, residual=None):
+    """y_t = residual_t + D(sum_j g_tj expert_out[send_pos] + shared_t)."""
+    N, k = gates.shape
+    H = expert_out.shape[1]
+    s = np.zeros((N, H))
+    for t in range(N):
+        for j in range(k):
+            r = send_pos[t * k + j]
+            if r >= 0:
+                s[t] += gates[t, j] * expert_out[r]
+    if shared is not None:
+        s += shared
+    m = dropout_mask(p, seed, offset, N * H).reshape(N, H)
+    y = np.where(m > 0, s, 0.0) * m   # (a dropped element is 0 whatever it held)
+    return y if residual is None else y + residual
+
+
+def combine_dropout_backward(dy, send_pos, gates, expert_out, p, seed, offset):
+    """(d_expert_out (NaN in rows that no slot names), d_gate, d_shared)."""
+    N, k = gates.shape
+    m = dropout_mask(p, seed, offset, dy.size).reshape(dy.shape)
+    d = np.where(m > 0, dy, 0.0) * m
+    d_eo, d_gate = np.full(expert_out.shape, np.nan), np.zeros((N, k))
+    for t in range(N):
+        for j in range(k):
+            r = send_pos[t * k + j]
+            if r >= 0:
+                d_eo[r] = gates[t, j] * d[t]
+                d_gate[t, j] = d[t] @ expert_out[r]
+    return d_eo, d_gate, d

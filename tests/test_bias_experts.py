@@ -1,0 +1,305 @@
+"""Experts with biases, other activations and dropout, on the CPU: the oracle's functions against known answers and
+differences, and the refusals of the C entry points and of their bindings (no GPU needed)."""
+import numpy as np
+import pytest
+import torch
+
+import combine_grouped_gemm_amd as moe
+from combine_grouped_gemm_amd import (MOE_BF16, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_F32,
+                                      MOE_FP8_E4M3, MOE_OK)
+from oracle import moe_oracle as oracle
+
+FAKE = 4096   # a non-null, 16-byte aligned host integer: never dereferenced on these paths
+
+
+# ------------------------------------------------------------------------------- the oracle
+
+def test_philox_known_answers():
+    """The generator's published test vectors (ten rounds)."""
+    assert oracle.philox((0,) * 4, (0,) * 2) == [0x6627E8D5, 0xE169C58D, 0xBC57AC4C, 0x9B00DBD8]
+    f = 0xFFFFFFFF
+    assert oracle.philox((f,) * 4, (f,) * 2) == [0x408F276D, 0x41C83B0E, 0xA20BC7C6, 0x6D5451FD]
+    assert oracle.philox((0x243F6A88, 0x85A308D3, 0x13198A2E, 0x03707344), (0xA4093822, 0x299F31D0)) == [
+        0xD16CFE09, 0x94FDCCEB, 0x5001E420, 0x24126EA1]
+
+
+def test_dropout_mask():
+    m = oracle.dropout_mask(0.25, 7, 3, 40000)
+    assert set(np.unique(m)) == {0.0, 4 / 3}
+    # 40000 draws: the share dropped within 5 standard deviations of 1/4
+    assert abs((m == 0).mean() - 0.25) < 5 * np.sqrt(0.25 * 0.75 / 40000)
+    assert np.array_equal(m[:1000], oracle.dropout_mask(0.25, 7, 3, 1000))   # a place's number is its own
+    assert not np.array_equal(m, oracle.dropout_mask(0.25, 7, 4, 40000))
+    assert not np.array_equal(m, oracle.dropout_mask(0.25, 8, 3, 40000))
+    assert np.all(oracle.dropout_mask(0.0, 1, 2, 100) == 1) and np.all(oracle.dropout_mask(1.0, 1, 2, 100) == 0)
+    # the high words of seed and offset count
+    assert not np.array_equal(m, oracle.dropout_mask(0.25, 7 + 2 ** 32, 3, 40000))
+    assert not np.array_equal(m, oracle.dropout_mask(0.25, 7, 3 + 2 ** 32, 40000))
+
+
+@pytest.mark.parametrize("act", sorted(oracle.ACTIVATIONS))
+def test_activation_slopes_by_differences(act):
+    x = np.linspace(-6, 6, 241) + 0.01   # (not at the kinks)
+    f = oracle.ACTIVATIONS[act]
+    h = 1e-5
+    assert np.allclose((f(x + h) - f(x - h)) / (2 * h), oracle.ACTIVATION_SLOPES[act](x), atol=1e-8)
+
+
+def test_activations_against_torch():
+    x = torch.linspace(-8, 8, 400, dtype=torch.float64)
+    F = torch.nn.functional
+    for act, ref in (("relu", F.relu(x)), ("gelu", F.gelu(x)), ("gelu_tanh", F.gelu(x, approximate="tanh")),
+                     ("silu", F.silu(x)), ("relu2", F.relu(x) ** 2)):
+        assert np.allclose(oracle.ACTIVATIONS[act](x.numpy()), ref.numpy(), atol=1e-14)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", sorted(oracle.ACTIVATIONS))
+def test_act_backward_by_differences(act, gated):
+    """<d_out, out> moves with the biases and with z as db and dz say."""
+    rng = np.random.default_rng(5)
+    off, N, K = [0, 3, 3, 8], 4, 5
+    Nw = 8 if gated else 4
+    a, w, b = rng.normal(size=(8, K)), rng.normal(size=(3, Nw, K)), rng.normal(size=(3, Nw))
+    d = rng.normal(size=(8, N))
+    _, z = oracle.expert_linear(a, off, w, b, act, gated)
+    dz, db, h = oracle.expert_act_backward(z, d, off, act, gated)
+    f = lambda bias: (oracle.expert_linear(a, off, w, bias, act, gated)[0] * d).sum()  # noqa: E731
+    eps = 1e-6
+    for e, c in ((0, 0), (2, Nw - 1), (1, 1), (2, N - 1)):
+        up, dn = b.copy(), b.copy()
+        up[e, c] += eps
+        dn[e, c] -= eps
+        assert abs((f(up) - f(dn)) / (2 * eps) - db[e, c]) < 1e-7
+    assert np.allclose(h, oracle.expert_linear(a, off, w, b, act, gated)[0]) and not db[1].any()
+
+
+def test_combine_dropout_backward_by_differences():
+    rng = np.random.default_rng(6)
+    N, k, H = 5, 2, 16
+    pos = np.array([3, 0, -1, 5, 1, 2, 4, 6, 7, 8])
+    eo, g, sh, dy = rng.normal(size=(10, H)), rng.random((N, k)), rng.normal(size=(N, H)), rng.normal(size=(N, H))
+    d_eo, dg, dsh = oracle.combine_dropout_backward(dy, pos, g, eo, 0.3, 11, 12)
+    f = lambda eo_, g_, sh_: (oracle.combine_dropout(eo_, pos, g_, 0.3, 11, 12, sh_) * dy).sum()  # noqa: E731
+    eps = 1e-6
+    for t, j in ((0, 0), (1, 0), (4, 1)):
+        u, v = g.copy(), g.copy()
+        u[t, j] += eps
+        v[t, j] -= eps
+        assert abs((f(eo, u, sh) - f(eo, v, sh)) / (2 * eps) - dg[t, j]) < 1e-7
+    for r, c in ((3, 0), (8, 15), (5, 7)):
+        u, v = eo.copy(), eo.copy()
+        u[r, c] += eps
+        v[r, c] -= eps
+        assert abs((f(u, g, sh) - f(v, g, sh)) / (2 * eps) - d_eo[r, c]) < 1e-7
+    u, v = sh.copy(), sh.copy()
+    u[2, 3] += eps
+    v[2, 3] -= eps
+    assert abs((f(eo, g, u) - f(eo, g, v)) / (2 * eps) - dsh[2, 3]) < 1e-7
+    assert np.isnan(d_eo[9]).all() and dg[1, 0] == 0
+
+
+def test_planted_mistakes_are_found(monkeypatch):
+    """A swapped half, a mask of the wrong place and a slope without its chain factor change what the pins see."""
+    rng = np.random.default_rng(7)
+    a, w, d = rng.normal(size=(4, 3)), rng.normal(size=(1, 8, 3)), rng.normal(size=(4, 4))
+    _, z = oracle.expert_linear(a, [0, 4], w, None, "silu", True)
+    good = oracle.expert_act_backward(z, d, [0, 4], "silu", True)[0]
+    swapped = oracle.expert_act_backward(np.concatenate([z[:, 4:], z[:, :4]], axis=1), d, [0, 4], "silu", True)[0]
+    assert not np.allclose(good, swapped)
+    monkeypatch.setitem(oracle.ACTIVATION_SLOPES, "silu", lambda x: 1 / (1 + np.exp(-x)))
+    assert not np.allclose(good, oracle.expert_act_backward(z, d, [0, 4], "silu", True)[0])
+    assert not np.array_equal(oracle.dropout_mask(0.5, 1, 1, 64)[8:], oracle.dropout_mask(0.5, 1, 1, 56))
+
+
+# ------------------------------------------------------------------------------- the C entry points
+
+def _linear(**kw):
+    v = dict(a=FAKE, dt=MOE_BF16, a_nrows=64, src=FAKE, k=2, off=FAKE, E=4, rows=128, K=64, N=64, w=FAKE, bias=FAKE,
+             bias_dt=MOE_F32, act=moe.MOE_ACT_SILU, gated=1, res=FAKE, out=FAKE, z=FAKE, ws=FAKE, ws_bytes=1 << 40)
+    v.update(kw)
+    return moe.lib().moe_expert_linear(*v.values(), None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(E=0), MOE_ERR_INVALID_ARG), (dict(rows=-1), MOE_ERR_INVALID_ARG), (dict(K=0), MOE_ERR_INVALID_ARG),
+    (dict(N=0), MOE_ERR_INVALID_ARG), (dict(k=0), MOE_ERR_INVALID_ARG), (dict(a_nrows=-1), MOE_ERR_INVALID_ARG),
+    (dict(a_nrows=0), MOE_ERR_INVALID_ARG), (dict(off=None), MOE_ERR_INVALID_ARG), (dict(act=6), MOE_ERR_INVALID_ARG),
+    (dict(act=-1), MOE_ERR_INVALID_ARG), (dict(gated=2), MOE_ERR_INVALID_ARG), (dict(a=None), MOE_ERR_INVALID_ARG),
+    (dict(w=None), MOE_ERR_INVALID_ARG), (dict(out=None), MOE_ERR_INVALID_ARG), (dict(a=FAKE + 8), MOE_ERR_INVALID_ARG),
+    (dict(bias=FAKE + 4), MOE_ERR_INVALID_ARG), (dict(res=FAKE + 2), MOE_ERR_INVALID_ARG),
+    (dict(z=FAKE + 8), MOE_ERR_INVALID_ARG), (dict(w=FAKE + 8), MOE_ERR_INVALID_ARG),
+    (dict(out=FAKE + 8), MOE_ERR_INVALID_ARG), (dict(dt=MOE_FP8_E4M3), MOE_ERR_UNSUPPORTED),
+    (dict(bias_dt=MOE_FP8_E4M3), MOE_ERR_UNSUPPORTED), (dict(dt=MOE_F32, bias_dt=MOE_BF16), MOE_ERR_UNSUPPORTED),
+    (dict(K=60), MOE_ERR_UNSUPPORTED), (dict(N=60), MOE_ERR_UNSUPPORTED), (dict(E=1025), MOE_ERR_UNSUPPORTED),
+    (dict(K=1 << 20), MOE_ERR_UNSUPPORTED), (dict(N=1 << 24), MOE_ERR_UNSUPPORTED),
+    (dict(a_nrows=1 << 20, K=2048), MOE_ERR_UNSUPPORTED), (dict(rows=2 ** 31 - 2 ** 16, N=8), MOE_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31 - 2 ** 16 - 1, N=1 << 20), MOE_ERR_UNSUPPORTED)])
+def test_linear_refusals(bad, status):
+    assert _linear(**bad) == status
+
+
+def test_linear_without_rows():
+    assert _linear(rows=0) == MOE_OK and _linear(rows=0, a=None, w=None, out=None) == MOE_OK
+    assert moe.moe_workspace_bytes(moe.MOE_OP_EXPERT_LINEAR, 0, 64, 64, 4, 0, MOE_BF16) == 0
+
+
+def test_linear_workspace():
+    """Every size has an answer, and a smaller workspace than that is refused."""
+    for dt in (MOE_BF16, MOE_F32):
+        for rows in (1, 2, 17, 100, 4096, 2 ** 31 - 2 ** 16 - 1):
+            for K, Nw in ((8, 8), (14336, 4096), (4096, 14336), (2 ** 20 - 8, 8)):
+                for E in (1, 8, 1024):
+                    need = moe.moe_workspace_bytes(moe.MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt)
+                    assert 0 <= need < 2 ** 40
+                    if need and rows < 10000:
+                        kw = dict(dt=dt, rows=rows, K=K, N=Nw, E=E, gated=0, src=None)
+                        assert _linear(ws_bytes=need - 1, **kw) == MOE_ERR_WORKSPACE
+                        assert _linear(ws=None, **kw) == MOE_ERR_WORKSPACE
+                        assert _linear(ws=FAKE + 8, **kw) == MOE_ERR_INVALID_ARG
+
+
+def _act(**kw):
+    v = dict(z=FAKE, d=FAKE, dt=MOE_BF16, off=FAKE, E=4, rows=128, N=64, act=moe.MOE_ACT_SILU, gated=0, dz=FAKE, db=FAKE,
+             db_dt=MOE_F32, h=FAKE, ws=FAKE, ws_bytes=1 << 40)
+    v.update(kw)
+    return moe.lib().moe_expert_act_backward(*v.values(), None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(E=0), MOE_ERR_INVALID_ARG), (dict(rows=-1), MOE_ERR_INVALID_ARG), (dict(N=0), MOE_ERR_INVALID_ARG),
+    (dict(off=None), MOE_ERR_INVALID_ARG), (dict(act=9), MOE_ERR_INVALID_ARG), (dict(gated=-1), MOE_ERR_INVALID_ARG),
+    (dict(z=None), MOE_ERR_INVALID_ARG), (dict(z=None, act=0), MOE_ERR_INVALID_ARG),
+    (dict(z=None, act=0, gated=1, h=None), MOE_ERR_INVALID_ARG), (dict(d=None), MOE_ERR_INVALID_ARG),
+    (dict(dz=None, db=None, h=None), MOE_ERR_INVALID_ARG), (dict(db=FAKE + 4), MOE_ERR_INVALID_ARG),
+    (dict(z=FAKE + 4), MOE_ERR_INVALID_ARG), (dict(d=FAKE + 8), MOE_ERR_INVALID_ARG),
+    (dict(dz=FAKE + 8), MOE_ERR_INVALID_ARG), (dict(h=FAKE + 8), MOE_ERR_INVALID_ARG),
+    (dict(ws=FAKE + 8), MOE_ERR_INVALID_ARG), (dict(dt=MOE_FP8_E4M3), MOE_ERR_UNSUPPORTED),
+    (dict(db_dt=MOE_FP8_E4M3), MOE_ERR_UNSUPPORTED), (dict(N=60), MOE_ERR_UNSUPPORTED),
+    (dict(E=1025), MOE_ERR_UNSUPPORTED), (dict(N=1 << 24), MOE_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31 - 2 ** 16), MOE_ERR_UNSUPPORTED), (dict(ws=None), MOE_ERR_WORKSPACE),
+    (dict(ws_bytes=0), MOE_ERR_WORKSPACE)])
+def test_act_backward_refusals(bad, status):
+    assert _act(**bad) == status
+
+
+def test_act_backward_workspace():
+    assert _act(rows=0, db=None) == MOE_OK
+    for rows in (1, 31, 300, 65536, 2 ** 31 - 2 ** 16 - 1):
+        for Nw in (8, 520, 4096, 1 << 24):
+            need = moe.moe_workspace_bytes(moe.MOE_OP_ACT_BACKWARD, rows, 0, Nw, 16, 0, 0)
+            # a partial row is written for every expert and every range of at least 8 rows
+            assert 17 * Nw * 4 <= need <= (rows // 8 + 17) * Nw * 4
+            if Nw < 1 << 24 and Nw % 8 == 0:
+                assert _act(rows=rows, N=Nw, E=16, ws_bytes=need - 1) == MOE_ERR_WORKSPACE
+
+
+def _cd(**kw):
+    v = dict(eo=FAKE, eo_dt=MOE_BF16, N=16, H=64, k=2, pos=FAKE, gate=FAKE, sh=FAKE, res=FAKE, p=0.1, rng=FAKE, y=FAKE,
+             y_dt=MOE_F32)
+    v.update(kw)
+    return moe.lib().moe_combine_dropout(*v.values(), None)
+
+
+def _cdb(**kw):
+    v = dict(dy=FAKE, dy_dt=MOE_F32, dt=MOE_BF16, N=16, H=64, k=2, pos=FAKE, gate=FAKE, eo=FAKE, p=0.1, rng=FAKE,
+             d_eo=FAKE, dg=FAKE, dsh=FAKE)
+    v.update(kw)
+    return moe.lib().moe_combine_dropout_backward(*v.values(), None)
+
+
+@pytest.mark.parametrize("f", [_cd, _cdb])
+def test_combine_dropout_refusals(f):
+    inv, un = MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
+    for bad in (dict(N=-1), dict(H=0), dict(k=0), dict(p=-0.1), dict(p=1.001), dict(p=float("nan")), dict(rng=None),
+                dict(rng=FAKE + 4), dict(pos=None)):
+        assert f(**bad) == inv, bad
+    for bad in (dict(k=33), dict(H=60), dict(N=1 << 24)):
+        assert f(**bad) == un, bad
+    assert f(N=0) == MOE_OK
+
+
+def test_combine_dropout_pointers_and_types():
+    inv, un = MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
+    for bad in (dict(eo=None), dict(y=None), dict(eo=FAKE + 8), dict(y=FAKE + 8), dict(sh=FAKE + 8), dict(res=FAKE + 8)):
+        assert _cd(**bad) == inv, bad
+    assert _cd(eo_dt=MOE_FP8_E4M3) == un and _cd(y_dt=MOE_FP8_E4M3) == un
+    for bad in (dict(dy=None), dict(d_eo=None), dict(eo=None), dict(dy=FAKE + 8), dict(d_eo=FAKE + 8), dict(eo=FAKE + 8),
+                dict(dsh=FAKE + 8)):
+        assert _cdb(**bad) == inv, bad
+    assert _cdb(dt=MOE_FP8_E4M3) == un and _cdb(dt=MOE_F32, dy_dt=MOE_BF16) == un
+
+
+def test_dropout_refusals():
+    f = moe.lib().moe_dropout
+    inv, un = MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
+    assert f(FAKE, MOE_BF16, -1, 0.1, FAKE, None, FAKE, MOE_BF16, None) == inv
+    assert f(FAKE, MOE_BF16, 8, 1.5, FAKE, None, FAKE, MOE_BF16, None) == inv
+    assert f(FAKE, MOE_BF16, 8, 0.5, None, None, FAKE, MOE_BF16, None) == inv
+    assert f(None, MOE_BF16, 8, 0.5, FAKE, None, FAKE, MOE_BF16, None) == inv
+    assert f(FAKE, MOE_BF16, 8, 0.5, FAKE, None, None, MOE_BF16, None) == inv
+    assert f(FAKE + 2, MOE_BF16, 8, 0.5, FAKE, None, FAKE, MOE_BF16, None) == inv
+    assert f(FAKE, MOE_BF16, 8, 0.5, FAKE, FAKE + 2, FAKE, MOE_BF16, None) == inv
+    assert f(FAKE, MOE_FP8_E4M3, 8, 0.5, FAKE, None, FAKE, MOE_BF16, None) == un
+    assert f(FAKE, MOE_BF16, 8, 0.5, FAKE, None, FAKE, MOE_FP8_E4M3, None) == un
+    assert f(FAKE, MOE_BF16, 1 << 41, 0.5, FAKE, None, FAKE, MOE_BF16, None) == un
+    assert f(None, MOE_BF16, 0, 0.5, FAKE, None, None, MOE_BF16, None) == MOE_OK
+
+
+# ------------------------------------------------------------------------------- the bindings
+
+def test_linear_binding_refusals():
+    bf = torch.bfloat16
+    a, w = torch.zeros(6, 16, dtype=bf), torch.zeros(2, 8, 16, dtype=bf)
+    off, slot = torch.zeros(3, dtype=torch.int32), torch.zeros(12, dtype=torch.int32)
+    good = dict(a=a, w=w, offsets=off, src_slot=slot, k=2)
+    for bad in (dict(a=a.half()), dict(a=a[0]), dict(w=w[0]), dict(w=w[:, :, :8]), dict(w=w.float()),
+                dict(w=torch.zeros(2, 7, 16, dtype=bf), gated=True), dict(bias=torch.zeros(2, 7)),
+                dict(bias=torch.zeros(2, 8).half()), dict(offsets=None), dict(offsets=off[:2]), dict(offsets=off.long()),
+                dict(src_slot=slot.long()), dict(rows=13), dict(rows=-1), dict(rows=7, src_slot=None),
+                dict(residual=torch.zeros(12, 8)), dict(residual=torch.zeros(11, 8, dtype=bf)),
+                dict(out=torch.zeros(12, 8)), dict(z=torch.zeros(12, 16, dtype=bf)),
+                dict(out=torch.zeros(12, 8, dtype=bf, device="meta")),
+                dict(ws=torch.zeros(8, dtype=torch.uint8, device="meta"))):
+        with pytest.raises(ValueError):
+            moe.moe_expert_linear(**{**good, **bad})
+
+
+def test_act_backward_binding_refusals():
+    bf = torch.bfloat16
+    d, z, off = torch.zeros(6, 8, dtype=bf), torch.zeros(6, 16, dtype=bf), torch.zeros(3, dtype=torch.int32)
+    good = dict(d_out=d, z=z, offsets=off, act=moe.MOE_ACT_SILU, gated=True)
+    for bad in (dict(d_out=d.half()), dict(d_out=d[0]), dict(z=z.float()), dict(z=z[:, :8]), dict(offsets=off.long()),
+                dict(E=3), dict(offsets=None, E=2), dict(dz=z.float()), dict(db=torch.zeros(2, 8)),
+                dict(db=torch.zeros(2, 16).half()), dict(h=z), dict(ws=torch.zeros(8, dtype=torch.uint8, device="meta"))):
+        with pytest.raises(ValueError):
+            moe.moe_expert_act_backward(**{**good, **bad})
+
+
+def test_dropout_binding_refusals():
+    eo, pos, g = torch.zeros(12, 16), torch.zeros(12, dtype=torch.int32), torch.zeros(6, 2)
+    rng, dy = torch.zeros(2, dtype=torch.int64), torch.zeros(6, 16)
+    good = dict(expert_out=eo, send_pos=pos, topk_gate=g, p=0.1, rng=rng)
+    for bad in (dict(expert_out=eo.half()), dict(expert_out=eo[0]), dict(send_pos=pos[:11]), dict(send_pos=pos.long()),
+                dict(topk_gate=g.double()), dict(topk_gate=g[0]), dict(topk_gate=None), dict(topk_gate=None, k=0),
+                dict(topk_gate=None, k=5), dict(rng=rng[:1]), dict(rng=rng.int()), dict(rng=rng.to("meta")),
+                dict(shared_out=dy[:5]), dict(shared_out=dy.bfloat16()), dict(residual=dy.bfloat16(), y=dy),
+                dict(residual=dy[:, :8]), dict(y=dy.half())):
+        with pytest.raises(ValueError):
+            moe.moe_combine_dropout(**{**good, **bad})
+    good = dict(dy=dy, send_pos=pos, topk_gate=g, expert_out=eo, p=0.1, rng=rng)
+    for bad in (dict(dy=dy[0]), dict(dy=dy.half()), dict(dy=dy.bfloat16()), dict(expert_out=eo[:, :8]),
+                dict(expert_out=None), dict(expert_out=None, d_expert_out=eo, d_gate=g), dict(send_pos=pos[:3]),
+                dict(rng=rng.float()), dict(d_expert_out=eo[:11]), dict(d_gate=g[:5]), dict(d_shared=dy.bfloat16())):
+        with pytest.raises(ValueError):
+            moe.moe_combine_dropout_backward(**{**good, **bad})
+    for bad in (dict(x=dy.half()), dict(rng=rng[:1]), dict(residual=dy.bfloat16()), dict(residual=dy[:3]),
+                dict(y=dy[:3]), dict(y=dy.half())):
+        with pytest.raises(ValueError):
+            moe.moe_dropout(**{**dict(x=dy, p=0.1, rng=rng, y=dy), **bad})
+
+
+def test_host_tensors_are_refused():
+    dy, rng = torch.zeros(6, 16), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="device tensors"):
+        moe.moe_dropout(dy, 0.1, rng)
