@@ -8,7 +8,8 @@
 // products are bf16 with fp32 sums, or fp32.
 //
 // A workgroup computes TM rows x TN weight rows (gated: TN / 2 rows of either half, so that a lane holds
-// both factors).  K advances in stages of 128 bytes a row (64 bf16, 32 fp32), loaded straight to LDS
+// both factors); an expert's rows are split evenly into as few tiles as hold them, and a wave skips the
+// products of 32-row blocks without rows.  K advances in stages of 128 bytes a row (64 bf16, 32 fp32), loaded straight to LDS
 // through buffer windows: rows past the segment, weight rows past the matrix and columns past K read as
 // zeros, so no size needs a kernel of its own.  Chunk c of 16 bytes of row r lies in slot c ^ key(r), so
 // that a load (8 rows) and a fragment read (32 rows, two chunks) touch every bank once.  A fragment is one
@@ -16,7 +17,17 @@
 // operands take their k in the same order).  The weights are the first operand: a lane's accumulators are
 // 4 adjacent columns of one row, and one exchange between lanes l and l + 32 makes them 8, which is what
 // bias, residual, u and out are read and written in (16 bytes a bf16 row).
+//
+// A ring of S stages is kept ahead.  Every k-step's products run between the LDS reads of the next
+// k-step's fragments; before a stage's last k-step, whose fragments are read by then, the workgroup
+// meets, so the next stage's first reads and the loads into the slot just left hide under that k-step's
+// products too, and the matrix pipes never wait at the barrier.  Shapes: 320 x 256 (8 waves of 160 x 64,
+// two stages, one workgroup a CU) reads 0.7 fragments a product and loads least: 256 x 256 took 1.13
+// times as long on 4096 x 14336 x 4096, 128 x 128 with two workgroups a CU 1.2 times; 128 x 256 (three
+// stages) for fewer rows; 64 x 64 (three stages, three workgroups a CU) where there are few tiles,
+// with K in parts when even those leave CUs idle.  Stages of 64 bytes took as long or longer.
 #include <type_traits>
+#include <utility>
 
 #include "activation.h"
 #include "gemm_device.h"
@@ -38,10 +49,14 @@ struct LinearArgs {
   const int32_t* a_rows;     // [rows] or null: row r is row a_rows[r] / a_div of a
   int a_div, a_nrows;
   int E, rows, K, N, act, bias_f32;
+  float* part;               // split K: [split, rows, Nw] sums instead of the epilogue, or null
+  int split;
 };
 
+constexpr int kLinRow = 128;   // bytes of a row and stage
 constexpr uint32_t kOutside = 0xFFFFFFF0u;   // past every window (windows are below 2^32 - 2^12 bytes)
 
+// slot of chunk c of row r: c ^ key
 __device__ __forceinline__ int lin_key(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 __device__ __forceinline__ void lin_segment(const LinearArgs& p, int e, int& lo, int& hi) {
@@ -112,27 +127,60 @@ __device__ __forceinline__ void lin_store8(uint8_t* p, size_t i, const float (&v
   }
 }
 
-// v: 8 columns from column col of the weights of expert e, without the bias; adds it and keeps u
+// 8 biases from column col of expert e's weights (0 without biases)
 template <bool F32>
-__device__ __forceinline__ void lin_bias(const LinearArgs& p, int Nw, int e, size_t row, int col, float (&v)[8]) {
-  if (p.bias != nullptr) {
-    float b[8];
-    const size_t at = static_cast<size_t>(e) * Nw + col;
-    if (F32 || p.bias_f32) lin_load8<true>(p.bias, at, b);
-    else lin_load8<false>(p.bias, at, b);
+__device__ __forceinline__ void lin_bias(const LinearArgs& p, int Nw, int e, int col, float (&b)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (p.z != nullptr) lin_store8<F32>(p.z, row * Nw + col, v);
+  for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+  if (p.bias == nullptr) return;
+  const size_t at = static_cast<size_t>(e) * Nw + col;
+  if (F32 || p.bias_f32) lin_load8<true>(p.bias, at, b);
+  else lin_load8<false>(p.bias, at, b);
 }
 
-// the epilogue of 8 columns of a row: v (gated: and w, the same columns of the second half)
+// 8 columns of a row as they lie
+template <bool F32>
+struct Raw {
+  uint4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ Raw<F32> lin_raw(const uint8_t* p, size_t i) {   // elements i .. i + 7
+  Raw<F32> r;
+  const uint4* q = reinterpret_cast<const uint4*>(p + i * (F32 ? 4 : 2));
+  r.w[0] = q[0];
+  if constexpr (F32) r.w[1] = q[1];
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void lin_values(const Raw<F32>& r, float (&v)[8]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (F32) {
+      v[2 * j] = __uint_as_float(w[2 * j]);
+      v[2 * j + 1] = __uint_as_float(w[2 * j + 1]);
+    } else {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+}
+
+// the epilogue of 8 columns of a row: sums v (gated: and w, the same columns of the second half), their
+// biases bv (and bw), the residual's values res (read when there is one)
 template <bool F32, bool GATED>
-__device__ __forceinline__ void lin_finish(const LinearArgs& p, int e, size_t row, int col, float (&v)[8],
-                                           float (&w)[8]) {
-  const int Nw = GATED ? 2 * p.N : p.N;
-  lin_bias<F32>(p, Nw, e, row, col, v);
-  if constexpr (GATED) lin_bias<F32>(p, Nw, e, row, p.N + col, w);
+__device__ __forceinline__ void lin_finish(const LinearArgs& p, size_t row, int col, float (&v)[8], float (&w)[8],
+                                           const float (&bv)[8], const float (&bw)[8], const Raw<F32>& res) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] += bv[i];
+    if constexpr (GATED) w[i] += bw[i];
+  }
+  if (p.z != nullptr) {
+    const size_t at = row * (GATED ? 2 * p.N : p.N) + col;
+    lin_store8<F32>(p.z, at, v);
+    if constexpr (GATED) lin_store8<F32>(p.z, at + p.N, w);
+  }
   act8<F32>(p.act, v);
   if constexpr (GATED) {
 #pragma unroll
@@ -140,11 +188,23 @@ __device__ __forceinline__ void lin_finish(const LinearArgs& p, int e, size_t ro
   }
   if (p.residual != nullptr) {
     float q[8];
-    lin_load8<F32>(p.residual, row * p.N + col, q);
+    lin_values<F32>(res, q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += q[i];
   }
   lin_store8<F32>(p.out, row * p.N + col, v);
+}
+// the same, its biases and residual read here
+template <bool F32, bool GATED>
+__device__ __forceinline__ void lin_finish_one(const LinearArgs& p, int e, size_t row, int col, float (&v)[8],
+                                               float (&w)[8]) {
+  const int Nw = GATED ? 2 * p.N : p.N;
+  float bv[8], bw[8];
+  lin_bias<F32>(p, Nw, e, col, bv);
+  if constexpr (GATED) lin_bias<F32>(p, Nw, e, p.N + col, bw);
+  Raw<F32> res{};
+  if (p.residual != nullptr) res = lin_raw<F32>(p.residual, row * p.N + col);
+  lin_finish<F32, GATED>(p, row, col, v, w, bv, bw, res);
 }
 
 // The tile of this workgroup: m-tiles of TM rows of every expert, in the order expert -> group of 8
@@ -152,7 +212,7 @@ __device__ __forceinline__ void lin_finish(const LinearArgs& p, int e, size_t ro
 // activation rows, run close together); contiguous ranges of the order go to the XCDs (workgroup i runs
 // on XCD i mod 8).  The launch has as many workgroups as any routing can need; false: nothing to do.
 struct LinTile {
-  int e, m0, mend, nblk;
+  int e, m0, mend, nblk, part;
 };
 template <int TM, int THREADS>
 __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* scan, LinTile& t) {
@@ -197,10 +257,16 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* s
     __syncthreads();
     total = scan[p.E];
   }
-  const long long tiles = static_cast<long long>(total) * nN;
-  const long long per = (tiles + kNumXcd - 1) / kNumXcd;
-  const long long slot = blockIdx.x / kNumXcd, L = (blockIdx.x % kNumXcd) * per + slot;
-  if (slot >= per || L >= tiles) return false;
+  const long long tiles = static_cast<long long>(total) * nN, all = tiles * p.split;
+  const long long per = (all + kNumXcd - 1) / kNumXcd;
+  const long long slot = blockIdx.x / kNumXcd;
+  long long L = (blockIdx.x % kNumXcd) * per + slot;
+  if (slot >= per || L >= all) return false;
+  t.part = 0;
+  if (p.split > 1) {   // (the parts of K outermost: an XCD holds few of them)
+    t.part = static_cast<int>(L / tiles);
+    L -= t.part * tiles;
+  }
   int e = 0, before = 0, mt = total;
   if (p.E > 1) {   // the last expert whose tiles start at or before L (an empty expert has none)
     int a = 0, b = p.E - 1;
@@ -222,23 +288,24 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* s
   t.e = e;
   int lo, hi;
   lin_segment(p, e, lo, hi);
-  t.m0 = lo + mtile * TM;
-  t.mend = t.m0 + TM < hi ? t.m0 + TM : hi;
-  return true;
+  const int rpt = ((hi - lo + mt - 1) / mt + 31) / 32 * 32;   // (at most TM, a multiple of 32)
+  t.m0 = lo + mtile * rpt;
+  t.mend = t.m0 + rpt < hi ? t.m0 + rpt : hi;
+  return t.m0 < t.mend;
 }
 
 // WM x WN waves; a wave's block is (TM / WM) x (TN / WN) as 32 x 32 products
-template <bool F32, bool GATED, int TM, int TN, int WM, int WN>
+template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p) {
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   constexpr int MB = TM / WM / 32, NB = TN / WN / 32;
-  constexpr int kLdA = TM / 8 / kWaves, kLdW = TN / 8 / kWaves;   // loads of 8 rows a wave and stage
-  constexpr int kStage = (TM + TN) * 128;
+  constexpr int kLdA = TM / 8 / kWaves, kLdW = TN / 8 / kWaves;   // loads a wave and stage
+  constexpr int kStage = (TM + TN) * kLinRow;
   constexpr int kEsz = F32 ? 4 : 2;
   static_assert(MB * WM * 32 == TM && NB * WN * 32 == TN && kLdA * kWaves * 8 == TM && kLdW * kWaves * 8 == TN, "tile");
   static_assert(!GATED || NB % 2 == 0, "a wave holds both factors");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
-  static_assert(2 * kStage >= (MOE_MAX_EXPERTS + 8) * 4, "the tile search shares the LDS");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[S * kStage];
+  static_assert(S * kStage >= (MOE_MAX_EXPERTS + 8) * 4, "the tile search shares the LDS");
 
   constexpr int kCols = GATED ? TN / 2 : TN;   // output columns of a tile
   const int nN = (p.N + kCols - 1) / kCols;
@@ -255,7 +322,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   const int c0 = t.nblk * kCols;
   const int ncols = p.N - c0 < kCols ? p.N - c0 : kCols;
   const int mrows = t.mend - t.m0;
-  const int nk = (rb + 127) / 128;
+  const int nkt = (rb + kLinRow - 1) / kLinRow;   // stages; this part's: [ks0, ks0 + nk)
+  const int ks0 = nkt * t.part / p.split, nk = nkt * (t.part + 1) / p.split - ks0;
 
   // windows: a's rows of the tile (gathered: all of a), the weight rows of either half
   const uint8_t* a_base = p.a_rows != nullptr ? p.a : p.a + static_cast<size_t>(t.m0) * rb;
@@ -264,44 +332,54 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   const uint32_t w_size = static_cast<uint32_t>(ncols) * rb;
   const uint8_t* w2_base = w_base + static_cast<size_t>(p.N) * rb;
 
-  // load j of a part fills the 8-row group wave + kWaves j: lane l slot l % 8 of row l / 8
+  // load j of an operand fills the 8-row group wave + kWaves j: lane l slot l % 8 of row l / 8, so chunk
+  // ch / 16 of it (kWaves is even: the group's parity is the wave's)
+  static_assert(kWaves % 2 == 0, "one chunk a lane");
   const int lrow = lane >> 3;
-  uint32_t va[kLdA], vw[kLdW], ca[kLdA], cw[kLdW];   // (ca, cw: the chunk's first byte in the stage)
+  const uint32_t ch = ((lane & 7) ^ lin_key((wave & 1) * 8 + lrow)) * 16;
+  uint32_t va[kLdA], vw[kLdW];
 #pragma unroll
   for (int j = 0; j < kLdA; ++j) {
     const int r = (wave + kWaves * j) * 8 + lrow;
-    ca[j] = ((lane & 7) ^ lin_key(r)) * 16;
-    if (r >= mrows) {
-      va[j] = kOutside;
-    } else {
+    va[j] = kOutside;
+    if (r < mrows) {
       int row = r;
       if (p.a_rows != nullptr) {
         row = p.a_rows[t.m0 + r] / p.a_div;
         row = row < 0 ? 0 : (row < p.a_nrows ? row : p.a_nrows - 1);
       }
-      va[j] = static_cast<uint32_t>(row) * rb + ca[j];
+      va[j] = static_cast<uint32_t>(row) * rb + ch;
     }
   }
 #pragma unroll
   for (int j = 0; j < kLdW; ++j) {
     const int r = (wave + kWaves * j) * 8 + lrow, c = GATED ? r % (TN / 2) : r;
-    cw[j] = ((lane & 7) ^ lin_key(r)) * 16;
-    vw[j] = c < ncols ? static_cast<uint32_t>(c) * rb + cw[j] : kOutside;
+    vw[j] = c < ncols ? static_cast<uint32_t>(c) * rb + ch : kOutside;
   }
-  auto load_stage = [&](int ks, int buf) __attribute__((always_inline)) {
-    const uint32_t k0 = static_cast<uint32_t>(ks) * 128;
-    const uint32_t left = rb - k0;   // bytes of a row from this stage on
-    const u32x4_t ra = buffer_window(a_base + k0, a_size - k0);
-    const u32x4_t rw = buffer_window(w_base + k0, w_size - k0);
-    const u32x4_t rw2 = buffer_window(w2_base + k0, w_size - k0);
-    const uint32_t at = lds0 + buf * kStage + wave * 1024;
-#pragma unroll
-    for (int j = 0; j < kLdA; ++j)
-      dma16_window(ra, left < 128 && ca[j] >= left ? kOutside : va[j], at + j * kWaves * 1024);
-#pragma unroll
-    for (int j = 0; j < kLdW; ++j)
-      dma16_window(GATED && (wave + kWaves * j) * 8 >= TN / 2 ? rw2 : rw, left < 128 && cw[j] >= left ? kOutside : vw[j],
-                   at + TM * 128 + j * kWaves * 1024);
+  // loads J of a stage into its slot: the rows of a first, then the weight rows
+  constexpr int kLoads = kLdA + kLdW;   // a wave and stage
+  struct Stage {
+    u32x4_t a, w, w2;
+    uint32_t left, at;   // bytes of a row from this stage on; the slot
+  };
+  auto stage_of = [&](int ks, int slot) __attribute__((always_inline)) {
+    const uint32_t k0 = static_cast<uint32_t>(ks) * kLinRow;
+    Stage g;
+    g.a = buffer_window(a_base + k0, a_size - k0);
+    g.w = buffer_window(w_base + k0, w_size - k0);
+    g.w2 = GATED ? buffer_window(w2_base + k0, w_size - k0) : g.w;
+    g.left = rb - k0;
+    g.at = lds0 + slot * kStage + wave * 1024;
+    return g;
+  };
+  auto load_one = [&](const Stage& g, int j) __attribute__((always_inline)) {   // (j is a constant after unrolling)
+    if (j < kLdA) {
+      dma16_window(g.a, ch >= g.left ? kOutside : va[j], g.at + j * kWaves * 1024);
+    } else {
+      const int i = j - kLdA;
+      dma16_window(GATED && (wave + kWaves * i) * 8 >= TN / 2 ? g.w2 : g.w,
+                   ch >= g.left ? kOutside : vw[i], g.at + TM * kLinRow + i * kWaves * 1024);
+    }
   };
 
   f32x16_t acc[MB][NB];
@@ -311,73 +389,477 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x16_t{};
   // first row of the wave's block m of activations, n of weight rows (gated: the first NB / 2 blocks
   // are of the first half)
-  auto a_row = [&](int m) { return (wm * MB + m) * 32; };
+  auto a_row = [&](int m) { return (m * WM + wm) * 32; };   // (dealt in turn: short tiles leave no wave idle)
   auto w_row = [&](int n) {
     return GATED ? (n / (NB / 2)) * (TN / 2) + (wn * (NB / 2) + n % (NB / 2)) * 32 : (wn * NB + n) * 32;
   };
   uint32_t fb[4];   // the lane's fragment of k-step s
 #pragma unroll
-  for (int s = 0; s < 4; ++s) fb[s] = (lane & 31) * 128 + ((2 * s + (lane >> 5)) ^ lin_key(lane & 31)) * 16;
+  for (int s = 0; s < 4; ++s)
+    fb[s] = (lane & 31) * kLinRow + ((2 * s + (lane >> 5)) ^ lin_key(lane & 31)) * 16;
 
-  load_stage(0, 0);
-  for (int ks = 0; ks < nk; ++ks) {
-    const int buf = ks & 1;
-    wait_vmcnt<0>();    // stage ks has landed; every wave is past its reads of the other buffer
-    block_barrier();
-    if (ks + 1 < nk) load_stage(ks + 1, buf ^ 1);
-    const uint8_t* la = lds + buf * kStage;
-    const uint8_t* lw = la + TM * 128;
+  static_assert(S * kLoads < 64, "the load counter");
+  for (int i = 0; i < S; ++i) {
+    if (i >= nk) break;
+    const Stage g = stage_of(ks0 + i, i);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint4 fa[MB], fw[NB];
+    for (int j = 0; j < kLoads; ++j) load_one(g, j);
+  }
+  if (nk >= S) wait_vmcnt<(S - 1) * kLoads>();
+  else wait_vmcnt<0>();
+  block_barrier();   // stage 0 has landed
+  auto k_loop = [&](auto act_c) __attribute__((always_inline)) {
+    constexpr int ACT = decltype(act_c)::value;   // row blocks of this wave that hold rows
+    constexpr int kSlots = ACT > 0 ? ACT * NB : 1, kReads = ACT > 0 ? ACT + NB : 0;
+    uint4 f0[ACT + NB], f1[ACT + NB];   // fragments of this k-step and of the next: rows of a, weight rows
+    auto read = [&](uint4(&f)[ACT + NB], int r, int slot, int s) __attribute__((always_inline)) {
+      const uint8_t* st = lds + slot * kStage;
+      f[r] = *reinterpret_cast<const uint4*>(
+          (r < ACT ? st + a_row(r) * kLinRow : st + TM * kLinRow + w_row(r - ACT) * kLinRow) + fb[s]);
+    };
+    // the products of a k-step; between them the reads of the next (slot, s) and the loads of a later stage
+    auto step = [&]<bool READ, bool LOAD>(const uint4(&f)[ACT + NB], uint4(&n)[ACT + NB], int slot, int s,
+                                          const Stage& g) __attribute__((always_inline)) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m) fa[m] = *reinterpret_cast<const uint4*>(la + a_row(m) * 128 + fb[s]);
+      for (int i = 0; i < kSlots; ++i) {
+        if constexpr (ACT > 0) acc[i / NB][i % NB] = lin_mma<F32>(f[ACT + i % NB], f[i / NB], acc[i / NB][i % NB]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (READ) {
 #pragma unroll
-      for (int n = 0; n < NB; ++n) fw[n] = *reinterpret_cast<const uint4*>(lw + w_row(n) * 128 + fb[s]);
+          for (int r = kReads * i / kSlots; r < kReads * (i + 1) / kSlots; ++r) read(n, r, slot, s);
+        }
+        if constexpr (LOAD) {
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+          for (int j = kLoads * i / kSlots; j < kLoads * (i + 1) / kSlots; ++j) load_one(g, j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    int slot = 0;
+    Stage none{};
 #pragma unroll
-        for (int n = 0; n < NB; ++n) acc[m][n] = lin_mma<F32>(fw[n], fa[m], acc[m][n]);
+    for (int r = 0; r < kReads; ++r) read(f0, r, 0, 0);
+    auto first = [&]() __attribute__((always_inline)) {   // k-steps 0 .. 2 of the stage in slot
+      step.template operator()<true, false>(f0, f1, slot, 1, none);
+      step.template operator()<true, false>(f1, f0, slot, 2, none);
+      step.template operator()<true, false>(f0, f1, slot, 3, none);
+    };
+    // this wave's reads of the stage are done, and its loads of the next have landed (all but those of the
+    // LEFT stages behind it); behind the barrier every wave's are and have
+    auto meet = [&]<int LEFT>() __attribute__((always_inline)) {
+      wait_lgkmcnt_all();
+      wait_vmcnt<LEFT * kLoads>();
+      block_barrier();
+    };
+    int ks = 0;
+    for (; ks < nk - S; ++ks) {
+      const int next = slot == S - 1 ? 0 : slot + 1;
+      first();
+      meet.template operator()<S - 2>();
+      const Stage g = stage_of(ks0 + ks + S, slot);
+      step.template operator()<true, true>(f1, f0, next, 0, g);
+      slot = next;
     }
-    wait_lgkmcnt_all();   // (this wave's reads of the stage are done before it meets the next barrier)
+    for (; ks < nk - 1; ++ks) {   // (no further stage to load)
+      const int next = slot == S - 1 ? 0 : slot + 1;
+      first();
+      meet.template operator()<0>();
+      step.template operator()<true, false>(f1, f0, next, 0, none);
+      slot = next;
+    }
+    first();
+    step.template operator()<false, false>(f1, f0, 0, 0, none);
+  };
+  const int nblk = (mrows + 31) / 32;
+  const int act = nblk > wm ? (nblk - wm + WM - 1) / WM : 0;
+  if (act >= MB) {
+    k_loop(std::integral_constant<int, MB>{});
+  } else {
+    [&]<int... A>(std::integer_sequence<int, A...>) {
+      ((act == A ? k_loop(std::integral_constant<int, A>{}) : void()), ...);
+    }(std::make_integer_sequence<int, MB>{});
   }
 
+  // epilogue: 8 columns (n, u) of row block m a lane; their biases once, a row block's residual together
   constexpr int kOutB = GATED ? NB / 2 : NB;
+  auto row_of = [&](int m) __attribute__((always_inline)) { return a_row(m) + (lane & 31); };
+  auto col_of = [&](int n, int u) __attribute__((always_inline)) {
+    return (wn * kOutB + n) * 32 + 16 * u + 8 * (lane >> 5);
+  };
+  if (p.part != nullptr) {   // one part of K: the sums join in another kernel
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int n = 0; n < kOutB; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float v[8], w[8];
+          pair8(acc[m][n], u, v);   // (every lane takes part in the exchange)
+          if constexpr (GATED) pair8(acc[m][n + kOutB], u, w);
+          if (row_of(m) >= mrows || col_of(n, u) >= ncols) continue;
+          float* q = p.part + (static_cast<size_t>(t.part) * p.rows + t.m0 + row_of(m)) * Nw + c0 + col_of(n, u);
+          lin_store8<true>(reinterpret_cast<uint8_t*>(q), 0, v);
+          if constexpr (GATED) lin_store8<true>(reinterpret_cast<uint8_t*>(q + p.N), 0, w);
+        }
+    return;
+  }
+  float bias[NB][2][8];   // (gated: [n + kOutB] the second half's)
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int col = col_of(n % kOutB, u);
+      lin_bias<F32>(p, Nw, t.e, (n < kOutB ? 0 : p.N) + c0 + (col < ncols ? col : 0), bias[n][u]);
+    }
 #pragma unroll
   for (int m = 0; m < MB; ++m) {
-    const int r = a_row(m) + (lane & 31);
+    Raw<F32> res[kOutB][2];
+    if (p.residual != nullptr) {
+#pragma unroll
+      for (int n = 0; n < kOutB; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (row_of(m) < mrows && col_of(n, u) < ncols)
+            res[n][u] = lin_raw<F32>(p.residual, (static_cast<size_t>(t.m0) + row_of(m)) * p.N + c0 + col_of(n, u));
+    }
 #pragma unroll
     for (int n = 0; n < kOutB; ++n)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float v[8], w[8];
-        pair8(acc[m][n], u, v);   // (every lane takes part in the exchange)
+        pair8(acc[m][n], u, v);
         if constexpr (GATED) pair8(acc[m][n + kOutB], u, w);
-        const int col = (wn * kOutB + n) * 32 + 16 * u + 8 * (lane >> 5);
-        if (r < mrows && col < ncols)
-          lin_finish<F32, GATED>(p, t.e, static_cast<size_t>(t.m0) + r, c0 + col, v, w);
+        if (row_of(m) < mrows && col_of(n, u) < ncols)
+          lin_finish<F32, GATED>(p, static_cast<size_t>(t.m0) + row_of(m), c0 + col_of(n, u), v, w, bias[n][u],
+                                 bias[GATED ? n + kOutB : n][u], res[n][u]);
       }
   }
 }
 
-template <bool F32, bool GATED, int TM, int TN, int WM, int WN>
-void launch_tiles(const LinearArgs& p, hipStream_t s) {
+// the parts of K joined in order: a lane 8 columns of a row
+template <bool F32, bool GATED>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p) {
+  const int groups = p.N / 8;
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = i / groups;
+  if (row >= p.rows) return;
+  const int col = static_cast<int>(i - row * groups) * 8;
+  int e = 0;
+  if (p.offsets != nullptr) {   // the row's expert: the last that starts at or before it
+    int a = 0, b = p.E - 1;
+    while (a < b) {
+      const int m = (a + b + 1) >> 1;
+      if (p.offsets[m] <= row) a = m;
+      else b = m - 1;
+    }
+    e = a;
+    if (row < p.offsets[e] || row >= p.offsets[e + 1]) return;
+  }
+  const int Nw = GATED ? 2 * p.N : p.N;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0}, w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int s = 0; s < p.split; ++s) {
+    const float* q = p.part + (static_cast<size_t>(s) * p.rows + row) * Nw + col;
+    float t[8];
+    lin_load8<true>(reinterpret_cast<const uint8_t*>(q), 0, t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += t[j];
+    if constexpr (GATED) {
+      lin_load8<true>(reinterpret_cast<const uint8_t*>(q + p.N), 0, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] += t[j];
+    }
+  }
+  lin_finish_one<F32, GATED>(p, e, row, col, v, w);
+}
+
+// ------------------------------------------------------------------------------------
+// Few rows an expert (serving: single tokens and small batches): bound by the weights' bytes.  A
+// workgroup takes 32 weight rows (gated: 16 of either half) and the rows of one expert, up to 32 at a
+// time; its 4 waves split K in contiguous parts.  Each wave streams its part through a ring of stages of its
+// own in LDS (128 bytes of the weight rows and of the rows of a), without meeting the others until the
+// end, when the four sums are added in order.
+// ------------------------------------------------------------------------------------
+
+constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves, kFewRows = 32;
+
+template <bool F32>
+__device__ __forceinline__ f32x4_t few_mma(uint4 a, uint4 b, f32x4_t c) {
+  if constexpr (F32) {
+    const f32x4_t x = __builtin_bit_cast(f32x4_t, a), y = __builtin_bit_cast(f32x4_t, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], y[i], c, 0, 0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
+}
+
+constexpr int kFewStage = (kFewRows + 32) * 128;   // bytes of a stage with 32 rows of a
+template <int MB>
+constexpr int kFewRing = MB == 1 ? 3 : 2;          // stages of a wave's ring (16 rows of a: 18 KB, 32: 16 KB)
+constexpr int kFewLds = kFewWaves * 3 * (kFewRows + 16) * 128;   // (two workgroups fit a CU)
+static_assert(kFewRing<2> * kFewStage * kFewWaves <= kFewLds, "the rings share the LDS");
+
+// rows [m0, m0 + 16 MB) of expert e against the workgroup's weight rows
+template <bool F32, bool GATED, int MB>
+__device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int mend, int c0, uint8_t* lds) {
+  constexpr int kCols = GATED ? 16 : 32, S = kFewRing<MB>, kLd = 4 + 2 * MB;
+  constexpr int kStage = (kFewRows + 16 * MB) * 128;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const mine = lds + wave * (kFewLds / kFewWaves);
+  const uint32_t at0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)mine));
+  const uint32_t rb = static_cast<uint32_t>(p.K) * (F32 ? 4 : 2);
+  const int Nw = GATED ? 2 * p.N : p.N;
+  const int ncols = p.N - c0 < kCols ? p.N - c0 : kCols;
+  const int mrows = mend - m0 < 16 * MB ? mend - m0 : 16 * MB;
+  const uint8_t* w_base = p.w + (static_cast<size_t>(e) * Nw + c0) * rb;
+  const uint8_t* w2_base = w_base + static_cast<size_t>(p.N) * rb;
+  const uint32_t w_size = static_cast<uint32_t>(ncols) * rb;
+  const uint8_t* a_base = p.a_rows != nullptr ? p.a : p.a + static_cast<size_t>(m0) * rb;
+  const uint32_t a_size = static_cast<uint32_t>(p.a_rows != nullptr ? p.a_nrows : mrows) * rb;
+  // a load fills 8 rows: lane l slot l % 8 of row l / 8
+  uint32_t vw[4], va[2 * MB], ch[2];   // (ch: the chunk's first byte, rows of even and odd groups)
+#pragma unroll
+  for (int j = 0; j < 2; ++j) ch[j] = ((lane & 7) ^ lin_key(j * 8 + (lane >> 3))) * 16;
+#pragma unroll
+  for (int j = 0; j < 2 * MB; ++j) {
+    const int r = j * 8 + (lane >> 3);
+    va[j] = kOutside;
+    if (r < mrows) {
+      int row = r;
+      if (p.a_rows != nullptr) {
+        row = p.a_rows[m0 + r] / p.a_div;
+        row = row < 0 ? 0 : (row < p.a_nrows ? row : p.a_nrows - 1);
+      }
+      va[j] = static_cast<uint32_t>(row) * rb + ch[j & 1];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = j * 8 + (lane >> 3), c = GATED ? r % 16 : r;
+    vw[j] = c < ncols ? static_cast<uint32_t>(c) * rb + ch[j & 1] : kOutside;
+  }
+  auto load = [&](int ks, int slot) __attribute__((always_inline)) {
+    const uint32_t k0 = static_cast<uint32_t>(ks) * 128, left = rb - k0;
+    const u32x4_t rw = buffer_window(w_base + k0, w_size - k0);
+    const u32x4_t rw2 = GATED ? buffer_window(w2_base + k0, w_size - k0) : rw;
+    const u32x4_t ra = buffer_window(a_base + k0, a_size - k0);
+    const uint32_t at = at0 + slot * kStage;
+    const bool in[2] = {left >= 128 || ch[0] < left, left >= 128 || ch[1] < left};   // (past K: zeros)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dma16_window(GATED && j >= 2 ? rw2 : rw, in[j & 1] ? vw[j] : kOutside, at + j * 1024);
+#pragma unroll
+    for (int j = 0; j < 2 * MB; ++j) dma16_window(ra, in[j & 1] ? va[j] : kOutside, at + (4 + j) * 1024);
+  };
+  const int nkt = (rb + 127) / 128;
+  const int s0 = nkt * wave / kFewWaves, nk = nkt * (wave + 1) / kFewWaves - s0;
+  f32x4_t acc[MB][2];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) acc[m][c] = f32x4_t{};
+  uint32_t fb[2];   // fragment of k-step s: row l % 16, chunk 4 s + l / 16
+#pragma unroll
+  for (int s = 0; s < 2; ++s) fb[s] = (lane & 15) * 128 + ((4 * s + (lane >> 4)) ^ lin_key(lane & 15)) * 16;
+  for (int i = 0; i < S - 1; ++i)
+    if (i < nk) load(s0 + i, i);
+  int slot = 0;
+  for (int ks = 0; ks < nk; ++ks) {
+    if (ks + S - 1 <= nk) wait_vmcnt<(S - 2) * kLd>();
+    else wait_vmcnt<0>();
+    __asm__ volatile("" ::: "memory");
+    // (the slot of stage ks - 1, whose fragments have been read)
+    if (ks + S - 1 < nk) load(s0 + ks + S - 1, slot == 0 ? S - 1 : slot - 1);
+    const uint8_t* st = mine + slot * kStage;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint4 fw[2], fa[MB];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) fw[c] = *reinterpret_cast<const uint4*>(st + c * 16 * 128 + fb[s]);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) fa[m] = *reinterpret_cast<const uint4*>(st + (kFewRows + m * 16) * 128 + fb[s]);
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[m][c] = few_mma<F32>(fw[c], fa[m], acc[m][c]);
+    }
+    wait_lgkmcnt_all();
+    __asm__ volatile("" ::: "memory");
+    slot = slot == S - 1 ? 0 : slot + 1;
+  }
+  // lane l holds weight rows 4 (l / 16) .. + 3 of block c for row l % 16: red[wave][m][row][weight row]
+  float* const red = reinterpret_cast<float*>(lds);
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      *reinterpret_cast<f32x4_t*>(red + ((wave * MB + m) * 16 + (lane & 15)) * 32 + c * 16 + 4 * (lane >> 4)) = acc[m][c];
+  __syncthreads();
+  constexpr int kGroups = kCols / 8;   // 8 columns of a row a lane
+  for (int i = threadIdx.x; i < MB * 16 * kGroups; i += kFewThreads) {
+    const int r = i / kGroups, col = (i % kGroups) * 8;
+    if (r >= mrows || col >= ncols) continue;
+    float v[8], w[8];
+#pragma unroll
+    for (int c = 0; c < (GATED ? 2 : 1); ++c) {
+      float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < kFewWaves; ++q) {
+        const float4* x = reinterpret_cast<const float4*>(red + (q * MB * 16 + r) * 32 + c * 16 + col);
+        const float4 a = x[0], b = x[1];
+        t[0] += a.x; t[1] += a.y; t[2] += a.z; t[3] += a.w;
+        t[4] += b.x; t[5] += b.y; t[6] += b.z; t[7] += b.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) (c == 0 ? v : w)[j] = t[j];
+    }
+    lin_finish_one<F32, GATED>(p, e, static_cast<size_t>(m0) + r, c0 + col, v, w);
+  }
+  __syncthreads();   // (the sums have been read before the next rows' stages land)
+}
+
+// workgroup x: 32 weight rows; y: an expert (slots < E: the y-th expert that has rows)
+template <bool F32, bool GATED>
+__global__ __launch_bounds__(kFewThreads) void linear_few_kernel(LinearArgs p, int slots) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kFewLds];
+  const int lane = threadIdx.x & 63;
+  int e = blockIdx.y;
+  if (slots < p.E) {
+    int seen = 0, found = -1;
+    for (int b = 0; b < p.E && found < 0; b += 64) {   // (every wave the same search)
+      int lo = 0, hi = 0;
+      if (b + lane < p.E) lin_segment(p, b + lane, lo, hi);
+      const uint64_t some = __ballot(hi > lo);
+      const int n = __popcll(some), want = static_cast<int>(blockIdx.y) - seen;
+      if (want < n) {
+        const uint64_t below = some & ((1ull << lane) - 1);
+        const uint64_t mine = __ballot(((some >> lane) & 1) != 0 && __popcll(below) == want);
+        found = b + __builtin_ctzll(mine);
+      }
+      seen += n;
+    }
+    if (found < 0) return;
+    e = __builtin_amdgcn_readfirstlane(found);
+  }
+  int lo, hi;
+  lin_segment(p, e, lo, hi);
+  const int c0 = blockIdx.x * (GATED ? 16 : 32);
+  for (int m0 = lo; m0 < hi; m0 += 32) {
+    if (hi - m0 <= 16) few_rows<F32, GATED, 1>(p, e, m0, hi, c0, lds);
+    else few_rows<F32, GATED, 2>(p, e, m0, hi, c0, lds);
+  }
+}
+
+template <bool F32, bool GATED>
+void launch_few(const LinearArgs& p, hipStream_t s) {
+  const int slots = p.E < p.rows ? p.E : p.rows;
+  constexpr int kCols = GATED ? 16 : 32;
+  hipLaunchKernelGGL((linear_few_kernel<F32, GATED>), dim3((p.N + kCols - 1) / kCols, slots), dim3(kFewThreads), 0, s, p,
+                     slots);
+}
+
+template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
+void launch_tiles(LinearArgs p, hipStream_t s, int split = 1, void* ws = nullptr) {
   constexpr int kCols = GATED ? TN / 2 : TN;
+  const int stages = (p.K * (F32 ? 4 : 2) + kLinRow - 1) / kLinRow;
+  if (split > stages) split = stages;   // (every part of K has a stage)
   const long long nN = (p.N + kCols - 1) / kCols;
   const long long mt = (p.rows + TM - 1) / TM + (p.E > 1 ? (p.E - 1 < p.rows ? p.E - 1 : p.rows) : 0);
-  const long long grid = (mt * nN + kNumXcd - 1) / kNumXcd * kNumXcd;
-  hipLaunchKernelGGL((linear_tile_kernel<F32, GATED, TM, TN, WM, WN>), dim3(static_cast<unsigned>(grid)),
+  const long long grid = (mt * nN * split + kNumXcd - 1) / kNumXcd * kNumXcd;
+  p.split = split;
+  p.part = split > 1 ? static_cast<float*>(ws) : nullptr;
+  hipLaunchKernelGGL((linear_tile_kernel<F32, GATED, TM, TN, WM, WN, S>), dim3(static_cast<unsigned>(grid)),
                      dim3(64 * WM * WN), 0, s, p);
+  if (split > 1) {
+    const long long lanes = static_cast<long long>(p.rows) * (p.N / 8);
+    hipLaunchKernelGGL((linear_join_kernel<F32, GATED>), dim3(static_cast<unsigned>((lanes + 255) / 256)), dim3(256), 0, s,
+                       p);
+  }
+}
+
+}  // namespace
+
+namespace {
+
+// Which kernel a call runs: the few-rows kernel, or tiles of a shape with K in `split` parts.  Known on
+// the host are the sizes, not the rows an expert gets; `each` rows of `hit` experts are expected.  The
+// estimate is us = overhead + rounds x stages x time of a stage, no less than the bytes at 5.2 TB/s, and
+// for a split the sums' way through memory.  Its constants are from measured runs (bf16, N 4096, one
+// expert, us; K 4096: 1, 64, 512, 1024, 2048 rows; K 14336: 64, 512, 1024, 2048):
+//     few               10   23    .    .    .     70    .    .    .
+//     64 x 64           22   23   33   58  111     90  130  240  439     split 4: 13, 14; K 14336: 35 at 64
+//     128 x 256         37   44   51   57   65    179  194  191  207     split 4, 512 rows: 33, 71; 2, 1024: 48, 120
+//     320 x 256         68   72   90   92  107    292  340  334  347     4096 rows of K 14336: 408 (128 x 256: 432)
+enum { LIN_FEW, LIN_64, LIN_128, LIN_320 };
+struct LinPlan {
+  int kind, split;
+};
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
+  const int esz = f32 ? 4 : 2;
+  const double row = 1.0 * K * esz;   // bytes of a row of a and of W
+  const double stages = static_cast<double>(ceil_div(1ll * K * esz, kLinRow));
+  const int hit = E < rows ? E : rows;
+  const double each = static_cast<double>(rows) / hit;
+  const double mem = (hit * Nw * row + rows * (row + 1.0 * Nw * esz)) / 5.2e6;
+  LinPlan best{LIN_64, 1};
+  double best_us = 1e30;
+  if (each <= 32) {
+    const double more = each > 16 ? 1.3 : E > 1 && each > 8 ? 1.05 : 1.0;   // (some experts' weights twice)
+    const double waves = ceil_div(hit * ceil_div(Nw, 32), 512) * stages / 4 * 0.3 * more * (f32 ? 1.5 : 1.0);
+    best = LinPlan{LIN_FEW, 1};
+    best_us = 4 + (mem * more > waves ? mem * more : waves);
+  }
+  struct Shape {
+    int kind, tm, tn, per_cu;
+    double overhead, latency, full;   // us of a launch; of a stage: without and with all rows
+  };
+  static const Shape bf16_shapes[] = {{LIN_64, 64, 64, 3, 5, 0.31, 0.4}, {LIN_128, 128, 256, 1, 6, 0.5, 1.02},
+                                      {LIN_320, 320, 256, 1, 8, 0.95, 1.75}};
+  static const Shape f32_shapes[] = {{LIN_64, 64, 64, 1, 5, 0.6, 0.6}, {LIN_128, 128, 128, 1, 6, 1.0, 2.0}};
+  for (int i = 0; i < (f32 ? 2 : 3); ++i) {
+    const Shape& s = f32 ? f32_shapes[i] : bf16_shapes[i];
+    // m-tiles of an expert: uneven experts, a standard deviation of random routes above the mean
+    const double mt = E == 1 ? static_cast<double>(ceil_div(rows, s.tm))
+                             : 1.0 * hit * ceil_div(static_cast<long long>(each + __builtin_sqrt(each)), s.tm);
+    const double tiles = mt * ceil_div(Nw, s.tn);
+    const double stage = s.latency + (s.full - s.latency) * (rows / (mt * s.tm));
+    const double l2 = tiles * (s.tm + s.tn) * row / 1.7e7;   // what the tiles load, at 17 TB/s
+    for (int split = 1; split <= 16 && split * 8 <= (stages > 8 ? stages : 8); split *= 2) {
+      const double turns = tiles * split / (256.0 * s.per_cu);
+      const double rounds = turns <= 1 ? 1.0
+                            : E == 1   ? static_cast<double>(ceil_div(static_cast<long long>(tiles * split), 256 * s.per_cu))
+                                       : turns + 0.15;
+      double us = rounds * stage * stages / split;
+      if (us < mem) us = mem;
+      if (us < l2) us = l2;
+      us += s.overhead;
+      if (split > 1) us += 3 + 8.0 * split * rows * Nw / 4e6;
+      if (us < best_us) {
+        best_us = us;
+        best = LinPlan{s.kind, split};
+      }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 // whether the tiles of the smallest shape fit a launch
 bool expert_linear_grid_fits(int rows, int N, int E) {
-  return (rows / 64ll + 1 + E) * (N / 32ll + 1) < (1ll << 31) - 8;
+  return (rows / 64ll + 1 + E) * (N / 32ll + 1) * 16 < (1ll << 31) - 8;
 }
 
-size_t expert_linear_ws_bytes(int rows, int K, int Nw, int E, bool f32) { return 0; }
+size_t expert_linear_ws_bytes(int rows, int K, int Nw, int E, bool f32) {
+  const int split = lin_plan(rows, K, Nw, E, f32).split;
+  return split > 1 ? static_cast<size_t>(split) * rows * Nw * sizeof(float) : 0;
+}
 
 hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int32_t* src_slot, int k,
                                 const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,
@@ -400,10 +882,21 @@ hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int3
   p.N = N;
   p.act = act;
   p.bias_f32 = bias_f32;
-  if (f32 && gated) launch_tiles<true, true, 128, 128, 2, 2>(p, s);
-  else if (f32) launch_tiles<true, false, 128, 128, 2, 2>(p, s);
-  else if (gated) launch_tiles<false, true, 128, 128, 2, 2>(p, s);
-  else launch_tiles<false, false, 128, 128, 2, 2>(p, s);
+  const LinPlan plan = lin_plan(rows, K, gated ? 2 * N : N, E, f32);
+  auto go = [&](auto f, auto g) {
+    constexpr bool F = decltype(f)::value, G = decltype(g)::value;
+    if (plan.kind == LIN_FEW) launch_few<F, G>(p, s);
+    else if (plan.kind == LIN_64) launch_tiles<F, G, 64, G ? 128 : 64, 2, 2, 3>(p, s, plan.split, ws);
+    else if constexpr (F) launch_tiles<F, G, 128, 128, 2, 2, 2>(p, s, plan.split, ws);
+    else if (plan.kind == LIN_128) launch_tiles<F, G, 128, 256, 2, 4, 3>(p, s, plan.split, ws);
+    else launch_tiles<F, G, 320, 256, 2, 4, 2>(p, s, plan.split, ws);
+  };
+  using T = std::true_type;
+  using U = std::false_type;
+  if (f32 && gated) go(T{}, T{});
+  else if (f32) go(T{}, U{});
+  else if (gated) go(U{}, T{});
+  else go(U{}, U{});
   return hipGetLastError();
 }
 
