@@ -19,10 +19,31 @@ __device__ __forceinline__ float sigmoid_act(float x) {
 constexpr float kGeluC = 1.5957691216057308f;    // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
+// Phi(x), the normal distribution function, and e = exp(-x^2 / 2).  fp32: Phi(x) = erfc(-x / sqrt 2) / 2 keeps
+// its digits where 1 + erf cancels.  For values that are rounded to bf16, the scaled tail exp(x^2 / 2)
+// Phi(-|x|) as a polynomial of degree 6 in t = 1 / (1 + 0.32 |x|) without a constant term, fitted to it for
+// the least largest relative error over 0 <= |x| <= 40 (1.2e-5, below 2^-16; the library's erfc took
+// 111 us where this takes 66 on 4585 rows of 12112, and its exponential is the density's too).
+template <bool F32>
+__device__ __forceinline__ float normal_cdf(float x, float& e) {
+  if (F32) {
+    e = expf(-0.5f * x * x);
+    return 0.5f * erfcf(x * -0.70710678118654752f);
+  }
+  e = __builtin_amdgcn_exp2f(-0.72134752044448170f * x * x);
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.32f, fabsf(x), 1.0f));
+  float q = fmaf(-0.06677503883838654f, t, 0.13958698511123657f);
+  q = fmaf(q, t, 0.049613259732723236f);
+  q = fmaf(q, t, 0.12305139005184174f);
+  q = fmaf(q, t, 0.12682823836803436f);
+  q = fmaf(q, t, 0.1276896893978119f);
+  q *= t * e;
+  return x > 0.0f ? 1.0f - q : q;
+}
+
 // act(x):
 //   none x | relu max(x, 0) | relu2 max(x, 0)^2 | gelu x Phi(x) | silu x s(x)
 //   gelu_tanh x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 = x s(2 sqrt(2/pi) (x + 0.044715 x^3))
-// Phi(x) = erfc(-x / sqrt 2) / 2 keeps its digits where 1 + erf cancels.
 template <bool F32>
 __device__ __forceinline__ void act8(int act, float (&v)[8]) {
   switch (act) {
@@ -36,7 +57,10 @@ __device__ __forceinline__ void act8(int act, float (&v)[8]) {
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.5f * v[i] * erfcf(v[i] * -0.70710678118654752f);
+      for (int i = 0; i < 8; ++i) {
+        float e;
+        v[i] *= normal_cdf<F32>(v[i], e);
+      }
       break;
     case MOE_ACT_GELU_TANH:
 #pragma unroll
@@ -73,8 +97,8 @@ __device__ __forceinline__ void act8_slope(int act, float (&v)[8], float (&s)[8]
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float x = v[i];
-        const float phi = 0.5f * erfcf(x * -0.70710678118654752f);
-        const float e = F32 ? expf(-0.5f * x * x) : __builtin_amdgcn_exp2f(-0.72134752044448170f * x * x);
+        float e;
+        const float phi = normal_cdf<F32>(x, e);
         s[i] = phi + x * 0.39894228040143268f * e;
         v[i] = x * phi;
       }

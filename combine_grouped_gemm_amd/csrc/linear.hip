@@ -786,7 +786,7 @@ namespace {
 
 // Which kernel a call runs: the few-rows kernel, or tiles of a shape with K in `split` parts.  Known on
 // the host are the sizes, not the rows an expert gets; `each` rows of `hit` experts are expected.  The
-// estimate is us = overhead + rounds x stages x time of a stage, no less than the bytes at 5.2 TB/s, and
+// estimate is us = rounds x (stages x time of a stage + overhead), no less than the bytes at 5.2 TB/s, and
 // for a split the sums' way through memory.  Its constants are from measured runs (bf16, N 4096, one
 // expert, us; K 4096: 1, 64, 512, 1024, 2048 rows; K 14336: 64, 512, 1024, 2048):
 //     few               10   23    .    .    .     70    .    .    .
@@ -816,12 +816,12 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
     best_us = 4 + (mem * more > waves ? mem * more : waves);
   }
   struct Shape {
-    int kind, tm, tn, per_cu;
-    double overhead, latency, full;   // us of a launch; of a stage: without and with all rows
+    int kind, tm, tn, per_cu, resident;   // tiles a CU works on at their full pace, and holds
+    double overhead, latency, full;   // us of a tile beside its stages; of a stage: without and with all rows
   };
-  static const Shape bf16_shapes[] = {{LIN_64, 64, 64, 3, 5, 0.31, 0.4}, {LIN_128, 128, 256, 1, 6, 0.5, 1.02},
-                                      {LIN_320, 320, 256, 1, 8, 0.95, 1.75}};
-  static const Shape f32_shapes[] = {{LIN_64, 64, 64, 1, 5, 0.6, 0.6}, {LIN_128, 128, 128, 1, 6, 1.0, 2.0}};
+  static const Shape bf16_shapes[] = {{LIN_64, 64, 64, 3, 3, 5, 0.31, 0.4}, {LIN_128, 128, 256, 1, 1, 6, 0.5, 1.02},
+                                      {LIN_320, 320, 256, 1, 1, 8, 0.95, 1.75}};
+  static const Shape f32_shapes[] = {{LIN_64, 64, 64, 1, 3, 5, 0.6, 0.6}, {LIN_128, 128, 128, 1, 2, 6, 1.0, 2.0}};
   for (int i = 0; i < (f32 ? 2 : 3); ++i) {
     const Shape& s = f32 ? f32_shapes[i] : bf16_shapes[i];
     // m-tiles of an expert: uneven experts, a standard deviation of random routes above the mean
@@ -832,13 +832,13 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
     const double l2 = tiles * (s.tm + s.tn) * row / 1.7e7;   // what the tiles load, at 17 TB/s
     for (int split = 1; split <= 16 && split * 8 <= (stages > 8 ? stages : 8); split *= 2) {
       const double turns = tiles * split / (256.0 * s.per_cu);
-      const double rounds = turns <= 1 ? 1.0
-                            : E == 1   ? static_cast<double>(ceil_div(static_cast<long long>(tiles * split), 256 * s.per_cu))
-                                       : turns + 0.15;
-      double us = rounds * stage * stages / split;
-      if (us < mem) us = mem;
-      if (us < l2) us = l2;
-      us += s.overhead;
+      const double rounds = turns <= 1               ? 1.0
+                            : E == 1 || turns < 4.0 ? static_cast<double>(static_cast<long long>(turns + (E == 1 ? 0.999 : 0.94)))
+                                                     : turns + 0.15;   // (the tiles of uneven experts are an estimate)
+      const double turn_overhead = s.overhead * (rounds * s.per_cu > s.resident ? rounds * s.per_cu / s.resident : 1.0);
+      double us = rounds * stage * stages / split + turn_overhead;
+      if (us < mem + s.overhead) us = mem + s.overhead;
+      if (us < l2 + s.overhead) us = l2 + s.overhead;
       if (split > 1) us += 3 + 8.0 * split * rows * Nw / 4e6;
       if (us < best_us) {
         best_us = us;

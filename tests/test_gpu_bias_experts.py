@@ -38,7 +38,12 @@ def _offsets(rows, E, seed):
     return torch.tensor([0, *cut.tolist(), rows], dtype=torch.int32)
 
 
-def _act_terms(act, z, ez):
+# Phi of values that are rounded to bf16 is a polynomial within 1.2e-5 of the tail (pinned by a test of its
+# coefficients against the scaled error function): what it adds to |x| Phi(x) and to the slope's Phi(x)
+TAIL = {BF: 1.2e-5, F32: 0.0}
+
+
+def _act_terms(act, z, ez, dt):
     """(act, its slope, the largest error of act at z + an error below ez, computed in fp32).
 
     The slope of every activation moves by at most 2 per unit of z (relu2 exactly, the others by less), so
@@ -48,14 +53,15 @@ def _act_terms(act, z, ez):
     argument of the exponential that act contains."""
     f, s = oracle.ACTIVATIONS[act](z), oracle.ACTIVATION_SLOPES[act](z)
     y = {"silu": np.abs(z), "gelu": z * z, "gelu_tanh": 1.6 * np.abs(z) * (1 + 0.05 * z * z)}.get(act, 0 * z)
-    return f, s, (np.abs(s) + 2 * ez) * ez + (6 * y + 16) * U32 * np.abs(f) + 1e-30
+    tail = TAIL[dt] * np.abs(f) if act == "gelu" else 0.0
+    return f, s, (np.abs(s) + 2 * ez) * ez + (6 * y + 16) * U32 * np.abs(f) + tail + 1e-30
 
 
 def _half_step(dt, v):
     return torch.finfo(dt).eps / 2 * v + (2.0 ** -133 if dt == BF else 2.0 ** -149)
 
 
-def _linear_reference(a, off, w, bias, act, gated, residual, tokens):
+def _linear_reference(a, off, w, bias, act, gated, residual, tokens, dt):
     """(out, its bound before rounding, z, its bound before rounding) in float64."""
     x = f64(a) if tokens is None else f64(a)[tokens]
     rows, K = x.shape
@@ -71,7 +77,7 @@ def _linear_reference(a, off, w, bias, act, gated, residual, tokens):
             mag[r] += np.abs(f64(bias[e]))
     # an fp32 sum of K products and a bias in any order, doubled for second order
     ez = 2 * (K + 16) * U32 * mag + 1e-37
-    f, _, ef = _act_terms(act, z[:, :N], ez[:, :N])
+    f, _, ef = _act_terms(act, z[:, :N], ez[:, :N], dt)
     if gated:
         u, eu = z[:, N:], ez[:, N:]
         out, eo = f * u, ef * (np.abs(u) + eu) + np.abs(f) * eu + U32 * np.abs(f * u)
@@ -113,7 +119,7 @@ def _run_linear(rows, E, K, N, dt, act="silu", gated=False, bias="f32", residual
     moe.moe_expert_linear(d(a), d(w), bias=d(b), offsets=None if dense else d(off), act=ACT[act], gated=gated,
                           src_slot=d(slot), k=max(k, 1), residual=d(res), out=out, z=z)
     sync()
-    ref, eo, zr, ez = _linear_reference(a, off, w, b, act, gated, res, tokens)
+    ref, eo, zr, ez = _linear_reference(a, off, w, b, act, gated, res, tokens, dt)
     _check("out", out, ref, eo, dt)
     if want_z:
         _check("z", z, zr, ez, dt)
@@ -279,7 +285,7 @@ def _run_act(rows, E, N, dt, act, gated, seed=0, db_dtype=F32, offsets=None):
     sync()
     zz, dd = f64(z), f64(d)
     rz, rb, rh = oracle.expert_act_backward(zz, dd, off.tolist(), act, gated)
-    f, s, ef = _act_terms(act, zz[:, :N], 0.0 * zz[:, :N])
+    f, s, ef = _act_terms(act, zz[:, :N], 0.0 * zz[:, :N], dt)
     # the slope: an exponential of argument y as above, times factors up to 1 + |y| + 2.4 z^2 in the tails
     g = zz[:, :N]
     y = {"silu": np.abs(g), "gelu": g * g, "gelu_tanh": 1.6 * np.abs(g) * (1 + 0.05 * g * g)}.get(act, 0 * g)
@@ -287,7 +293,7 @@ def _run_act(rows, E, N, dt, act, gated, seed=0, db_dtype=F32, offsets=None):
           "gelu_tanh": 1 / (1 + np.exp(-1.5957691 * (g + 0.044715 * g ** 3)))}.get(act, np.abs(s))
     # a logistic value or an exponential below 2^-126 is 0 on the GPU (the exponential in its denominator passes
     # 2^128, or the reciprocal's result is subnormal), so sg is off by up to 2^-126 there
-    es = ((6 * y + 24) * U32 * sg + 2.0 ** -126) * (1 + y + np.abs(g) * 1.6 * (1 + 0.15 * g * g))
+    es = (((6 * y + 24) * U32 + (TAIL[dt] if act == "gelu" else 0.0)) * sg + 2.0 ** -126) * (1 + y + np.abs(g) * 1.6 * (1 + 0.15 * g * g))
     u = np.abs(zz[:, N:]) if gated else 1.0
     e1 = (es + 3 * U32 * np.abs(s)) * np.abs(dd) * u
     ez = np.concatenate([e1, np.abs(dd) * (ef + 2 * U32 * np.abs(f))], axis=1) if gated else e1
