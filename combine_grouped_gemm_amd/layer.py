@@ -24,16 +24,27 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_BF16, MOE_BF16X3, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_BALANCE_LOSS, MOE_OP_DISPATCH_LAYOUT,
-               MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM, MOE_OP_GROUPED_FFN, MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD,
-               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_backward, moe_dequantize_fp8,
-               moe_dequantize_mxfp8, moe_dispatch_layout, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
+from . import (MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_SILU, MOE_BF16, MOE_BF16X3, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_ACT_BACKWARD, MOE_OP_BALANCE_LOSS,
+               MOE_OP_DISPATCH_LAYOUT, MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM, MOE_OP_EXPERT_LINEAR, MOE_OP_GROUPED_FFN,
+               MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD, moe_balance_loss, moe_balance_loss_backward, moe_combine,
+               moe_combine_backward, moe_combine_dropout, moe_combine_dropout_backward, moe_dequantize_fp8,
+               moe_dequantize_mxfp8, moe_dispatch_layout, moe_dropout, moe_expert_act_backward, moe_expert_linear, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
                moe_expert_down_shared_e4m3, moe_expert_gate_up, moe_expert_gate_up_gathered,
                moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3,
                moe_expert_gate_up_mxfp8, moe_expert_gate_up_preact, moe_expert_wgrad, moe_grouped_ffn, moe_permute,
                moe_quantize_fp8, moe_quantize_mxfp8, moe_route, moe_router_backward, moe_router_dense_dgrad,
                moe_router_dense_wgrad, moe_router_input_grad, moe_router_logits, moe_swiglu_backward,
                moe_swiglu_backward_mxfp8, moe_workspace_bytes, _balance_args, _expect)
+
+
+def _check_drop(N, H, dtype, device, residual, dropout, rng):
+    """Raises ValueError unless residual, dropout and rng fit a layer's forward."""
+    if not 0.0 <= dropout <= 1.0:
+        raise ValueError(f"dropout must lie in 0 .. 1, not {dropout}")
+    if dropout > 0.0 and rng is None:
+        raise ValueError("dropout needs rng, the generator's state (device int64 [2]: seed, offset)")
+    _expect("rng", rng, (2,), (torch.int64,), device)
+    _expect("residual", residual, (N, H), (dtype,), device)
 
 
 class MoELayer:
@@ -136,6 +147,8 @@ class MoELayer:
         self.balance = None
         self.balance_args = None
         self.balance_bufs = {}
+        self.drop_p = 0.0        # dropout of the last forward, and the generator's state that it used
+        self.rng_used = None
 
     _WEIGHTS = ("w13", "w2", "w13_scale", "w2_scale", "sw13", "sw2", "sw13_scale", "sw2_scale", "w_r", "bias")
     _WEIGHT_GRADS = ("dw13", "dw2", "dsw13", "dsw2", "dw_r")
@@ -261,7 +274,11 @@ class MoELayer:
         return moe_grouped_ffn(a, self.shared_offsets, self.sw13, self.sw2, a_scale, self.sw13_scale,
                                self.sw2_scale, self._shared_out, self.shared_ws)
 
-    def combine(self):
+    def combine(self, residual: Optional[torch.Tensor] = None):
+        if residual is not None or self.drop_p > 0.0:
+            return moe_combine_dropout(self.expert_out, self.layout[2], None if self.gate_in_down else self.topk_gate,
+                                       self.drop_p, self.rng_used, self.shared_out if self.shared else None, residual,
+                                       self.y, k=self.k)
         return moe_combine(self.expert_out, self.layout[2], None if self.gate_in_down else self.topk_gate,
                            self.shared_out if self.shared else None, self.y, k=self.k)
 
@@ -303,7 +320,8 @@ class MoELayer:
 
     def forward(self, x: torch.Tensor, z: Optional[torch.Tensor] = None, save_for_backward=False,
                 balance_alpha: Optional[float] = None, seq_start: Optional[torch.Tensor] = None,
-                token_mask: Optional[torch.Tensor] = None) -> torch.Tensor:
+                token_mask: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                dropout: float = 0.0, rng: Optional[torch.Tensor] = None) -> torch.Tensor:
         """y for tokens x; z: the router logits (computed from W_r when None).
 
         save_for_backward True: a bf16 layer that runs the shared expert inside the routed
@@ -313,7 +331,11 @@ class MoELayer:
         else of the forward but the routes, neither x nor the expert outputs.
         balance_alpha: also the balance loss of the batch's routes, into self.balance, and its
         gradient in the next backward (seq_start, token_mask: see moe_balance_loss; they, and z
-        if it was passed, stay as they are until then)."""
+        if it was passed, stay as they are until then).
+        residual [N, H] of y's type: y = residual + the layer's sum.  dropout: the sum (not the residual) is
+        dropped out with this probability, from the numbers of rng (device int64 [2]: seed, offset; see
+        moe_combine_dropout), whose state here is kept for the next backward; the caller advances the
+        offset from forward to forward.  The residual's gradient is dy."""
         if isinstance(save_for_backward, str) and save_for_backward != "mxfp8":
             raise ValueError('save_for_backward is False, True or "mxfp8"')
         if balance_alpha is None and (seq_start is not None or token_mask is not None):
@@ -333,6 +355,13 @@ class MoELayer:
             S = _balance_args(self.z if z is None else z, self.topk_idx, self.bias, seq_start, token_mask)[3]
             if S > 65535:
                 raise ValueError(f"a balance loss takes at most 65535 sequences, not {S}")
+        _check_drop(self.N, self.H, self.act_dtype, self.device, residual, dropout, rng)
+        self.drop_p = float(dropout)
+        if residual is not None or dropout > 0.0:
+            if self.rng_used is None:
+                self.rng_used = torch.zeros(2, dtype=torch.int64, device=self.device)
+            if rng is not None:
+                torch.add(rng, 0, out=self.rng_used)   # (the caller may advance rng before the backward)
         self.keep8 = keep8
         self.save_au = bool(save_for_backward and not keep8 and self.fuse and not self.fp8)
         if self.save_au and self.au_all is None:
@@ -360,7 +389,7 @@ class MoELayer:
                 torch.cuda.current_stream(self.device).wait_event(self.shared_done)
             else:
                 self.shared_expert(x)
-        self.combine()
+        self.combine(residual)
         return self.y
 
     # ---- backward (bf16 layers that gather their rows from x)
@@ -397,6 +426,8 @@ class MoELayer:
         need("dw2", (E, H, I), dw_dtype)
         need_ws("gemm_ws", moe_workspace_bytes(MOE_OP_EXPERT_GEMM, max(rows, N), H, I, E, 1, MOE_BF16))
         need_ws("dgrad_ws", moe_workspace_bytes(MOE_OP_EXPERT_DGRAD, max(rows, N), 0, 0, E, 0, 0))
+        if self.drop_p > 0.0 and (self.shared or self.keep8):
+            need("dy_d", (N, H), bf)   # dy behind the dropout
         if self.shared:
             # (the shared expert's steps have workspaces of their own: they may run on a
             # second stream beside the routed ones)
@@ -451,6 +482,11 @@ class MoELayer:
         rows = N * k
         offsets, send_pos, src_slot = self.layout[1], self.layout[2], self.layout[3]
         st = []
+        dy_all, p = dy, self.drop_p
+        if p > 0.0 and (self.shared or keep8):
+            dy = b["dy_d"]
+        if p > 0.0 and keep8:
+            st.append(("dy_dropout", lambda: moe_dropout(dy_all, p, self.rng_used, y=dy)))
         if keep8:
             # x's values from its codes; the upstream rows before the gates (they enter behind the
             # down projection, where the gates' own gradient is <dh, h>)
@@ -465,7 +501,7 @@ class MoELayer:
                                                                  self.topk_gate, b["d_au"], b["h"], b["dg"])),
             ]
         else:
-            st += self._preact_steps(x, dy)
+            st += self._preact_steps(x, dy_all)
         xp = ((lambda: moe_dequantize_mxfp8(kx[0], kx[1], out=b["x_perm"], send_pos=send_pos, k=k)) if keep8 else
               (lambda: moe_permute(x, send_pos, k, None, b["x_perm"])))
         st += [
@@ -527,8 +563,10 @@ class MoELayer:
         saved = self.au_saved
         au = self.au_all[:rows] if saved else b["au"]
         st = [
-            ("combine_bwd", lambda: moe_combine_backward(dy, send_pos, self.topk_gate, self.expert_out, b["d_eo"],
-                                                         b["dg"])),
+            ("combine_bwd", lambda: moe_combine_dropout_backward(
+                dy, send_pos, self.topk_gate, self.expert_out, self.drop_p, self.rng_used, b["d_eo"], b["dg"],
+                b["dy_d"] if self.shared else None) if self.drop_p > 0.0 else
+             moe_combine_backward(dy, send_pos, self.topk_gate, self.expert_out, b["d_eo"], b["dg"])),
         ]
         if not saved:
             st.append(("gate_up_preact", lambda: moe_expert_gate_up_preact(x, offsets, self.w13, rows, src_slot, k,
@@ -573,8 +611,10 @@ class MoELayer:
             self.bwd_side = torch.cuda.Stream(device=self.device)
             self.bwd_side_done = torch.cuda.Event()
         side = self.bwd_side
+        # what both streams read
+        both = ("x_values", "dy_dropout") + (("combine_bwd",) if self.drop_p > 0.0 else ())
         for name, f in steps:
-            if name == "x_values":   # (both streams read them)
+            if name in both:
                 f()
         side.wait_stream(main)
         with torch.cuda.stream(side):
@@ -583,7 +623,7 @@ class MoELayer:
                     f()
             self.bwd_side_done.record(side)
         for name, f in steps:
-            if name.startswith("shared_") or name == "x_values":
+            if name.startswith("shared_") or name in both:
                 continue
             if name in ("router_dx", "dx") and not getattr(self, "_waited", False):
                 main.wait_event(self.bwd_side_done)   # the shared expert's dx joins here
@@ -594,6 +634,138 @@ class MoELayer:
             if t is not None:
                 t.record_stream(side)
         return self._gradients()
+
+
+class BiasedMoELayer:
+    """Pre-planned MoE layer whose experts are act(x W1^T + b1) W2^T + b2.
+
+    The router, layout and combine of MoELayer around other experts: w1 [E, I, H] (gated: [E, 2I, H],
+    h = act of the first half times the second), w2 [E, H, I], biases b1 [E, I or 2I] and b2 [E, H]
+    (fp32 or the weights' type) or None, act one of MOE_ACT_*.  The weights' type (float32 or bfloat16) is the
+    layer's.  forward adds the residual stream and drops out as MoELayer's does; backward is
+    built for bf16 layers with H and I multiples of 128 (the sizes of moe_expert_dgrad and
+    moe_expert_wgrad).  All buffers are allocated at construction or on the first backward.
+    """
+
+    def __init__(self, N: int, H: int, E: int, k: int, I: int, w1: torch.Tensor, w2: torch.Tensor,
+                 b1: Optional[torch.Tensor] = None, b2: Optional[torch.Tensor] = None, act: int = MOE_ACT_GELU_TANH,
+                 gated: bool = False, n_group: int = 0, topk_group: int = 0, bias: Optional[torch.Tensor] = None,
+                 w_r: Optional[torch.Tensor] = None):
+        if not MOE_ACT_NONE <= act <= MOE_ACT_SILU:
+            raise ValueError(f"act must be one of MOE_ACT_*, not {act}")
+        dt, dev = w1.dtype, w1.device
+        Nw = 2 * I if gated else I
+        if dt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"w1 must be float32 or bfloat16, not {dt}")
+        _expect("w1", w1, (E, Nw, H), (dt,), dev)
+        _expect("w2", w2, (E, H, I), (dt,), dev)
+        _expect("b1", b1, (E, Nw), (torch.float32, dt), dev)
+        _expect("b2", b2, (E, H), (torch.float32, dt), dev)
+        _expect("bias", bias, (E,), (torch.float32,), dev)
+        _expect("w_r", w_r, (E, H), (dt,), dev)
+        self.N, self.H, self.E, self.k, self.I = N, H, E, k, I
+        self.w1, self.w2, self.b1, self.b2, self.act, self.gated = w1, w2, b1, b2, act, bool(gated)
+        self.n_group, self.topk_group, self.bias, self.w_r = n_group, topk_group, bias, w_r
+        self.act_dtype, self.device = dt, dev
+        c_dt = MOE_F32 if dt == torch.float32 else MOE_BF16
+        rows = N * k
+
+        def ws(*args):
+            return torch.empty(max(moe_workspace_bytes(*args), 256), dtype=torch.uint8, device=dev)
+
+        i32 = dict(dtype=torch.int32, device=dev)
+        if w_r is not None:
+            self.z = torch.empty((N, E), dtype=torch.float32, device=dev)
+            self.router_ws = ws(MOE_OP_ROUTER, N, H, 0, E, 0, c_dt)
+        self.topk_idx = torch.empty((N, k), **i32)
+        self.topk_gate = torch.empty((N, k), dtype=torch.float32, device=dev)
+        self.layout = (torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(rows, **i32),
+                       torch.empty(rows, **i32))
+        self.layout_ws = ws(MOE_OP_DISPATCH_LAYOUT, N, 0, 0, E, k, 0)
+        self.fc1_ws = ws(MOE_OP_EXPERT_LINEAR, rows, H, Nw, E, 0, c_dt)
+        self.fc2_ws = ws(MOE_OP_EXPERT_LINEAR, rows, I, H, E, 0, c_dt)
+        self.h = torch.empty((rows, I), dtype=dt, device=dev)
+        self.expert_out = torch.empty((rows, H), dtype=dt, device=dev)
+        self.y = torch.empty((N, H), dtype=dt, device=dev)
+        self.pre = None          # the pre-activations [rows, I or 2I] of a forward that keeps them
+        self.saved = False       # the last forward kept them
+        self.drop_p = 0.0
+        self.rng_used = torch.zeros(2, dtype=torch.int64, device=dev)
+        self.grads = None
+
+    def forward(self, x: torch.Tensor, z: Optional[torch.Tensor] = None, save_for_backward: bool = False,
+                residual: Optional[torch.Tensor] = None, dropout: float = 0.0,
+                rng: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y [N, H] for tokens x (z: the router logits, computed from w_r when None); residual, dropout and rng as
+        MoELayer.forward takes them.  save_for_backward keeps the pre-activations for backward."""
+        N, E, k, dt = self.N, self.E, self.k, self.act_dtype
+        _expect("x", x, (N, self.H), (dt,), self.device)
+        if z is None and self.w_r is None:
+            raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
+        _expect("z", z, (N, E), (torch.float32,), self.device)
+        _check_drop(N, self.H, dt, self.device, residual, dropout, rng)
+        self.drop_p = float(dropout)
+        if rng is not None:
+            torch.add(rng, 0, out=self.rng_used)   # (the caller may advance rng before the backward)
+        if save_for_backward and self.pre is None:
+            self.pre = torch.empty((N * k, self.w1.shape[1]), dtype=dt, device=self.device)
+        self.saved = bool(save_for_backward)
+        if z is None:
+            z = moe_router_logits(x, self.w_r, self.z, self.router_ws)
+        moe_route(z, k, self.bias, self.n_group, self.topk_group, self.topk_idx, self.topk_gate)
+        _, offsets, send_pos, src_slot = moe_dispatch_layout(self.topk_idx, E, self.layout, self.layout_ws)
+        moe_expert_linear(x, self.w1, self.b1, offsets, self.act, self.gated, src_slot, k, out=self.h,
+                          z=self.pre if self.saved else None, ws=self.fc1_ws)
+        moe_expert_linear(self.h, self.w2, self.b2, offsets, out=self.expert_out, ws=self.fc2_ws)
+        return moe_combine_dropout(self.expert_out, send_pos, self.topk_gate, self.drop_p, self.rng_used,
+                                   residual=residual, y=self.y)
+
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, dw_dtype: torch.dtype = torch.bfloat16) -> dict:
+        """Gradients of the last forward (with save_for_backward) for the upstream gradient dy [N, H] bf16: 'dx',
+        'dw1', 'dw2', 'db1', 'db2' (fp32), 'dg' (the gates'), with w_r 'dz' (the selected logits') and 'dw_r'.  The
+        residual's gradient is dy."""
+        N, H, E, k, I = self.N, self.H, self.E, self.k, self.I
+        bf, dev, rows = torch.bfloat16, self.device, self.N * self.k
+        if self.act_dtype != bf or H % 128 or I % 128:
+            raise ValueError("backward is built for bf16 layers with H and I multiples of 128")
+        if not self.saved:
+            raise ValueError("backward needs a forward with save_for_backward")
+        _expect("x", x, (N, H), (bf,), dev)
+        _expect("dy", dy, (N, H), (bf,), dev)
+        b = self.grads
+        if b is None or b["dw1"].dtype != dw_dtype:
+            def new(*shape, dtype=bf):
+                return torch.empty(shape, dtype=dtype, device=dev)
+
+            Nw = self.w1.shape[1]
+            b = dict(d_eo=new(rows, H), dg=new(N, k, dtype=torch.float32), dh=new(rows, I), dpre=new(rows, Nw),
+                     h=new(rows, I), x_perm=new(rows, H), d_perm=new(rows, H), dx=new(N, H),
+                     dw1=new(E, Nw, H, dtype=dw_dtype), dw2=new(E, H, I, dtype=dw_dtype),
+                     db1=new(E, Nw, dtype=torch.float32), db2=new(E, H, dtype=torch.float32))
+            for name, args in (("act_ws", (MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0)),
+                               ("b2_ws", (MOE_OP_ACT_BACKWARD, rows, 0, H, E, 0, 0)),
+                               ("dgrad_ws", (MOE_OP_EXPERT_DGRAD, rows, 0, 0, E, 0, 0))):
+                b[name] = torch.empty(max(moe_workspace_bytes(*args), 256), dtype=torch.uint8, device=dev)
+            if self.w_r is not None:
+                b.update(dz=new(N, k, dtype=torch.float32), dw_r=new(E, H, dtype=dw_dtype), dx_r=new(N, H))
+            self.grads = b
+        _, offsets, send_pos, src_slot = self.layout
+        moe_combine_dropout_backward(dy, send_pos, self.topk_gate, self.expert_out, self.drop_p, self.rng_used, b["d_eo"],
+                                     b["dg"])
+        moe_expert_act_backward(b["d_eo"], offsets=offsets, want_dz=False, db=b["db2"], ws=b["b2_ws"])
+        moe_expert_dgrad(b["d_eo"], offsets, self.w2, b["dh"], b["dgrad_ws"])
+        moe_expert_act_backward(b["dh"], self.pre, offsets, self.act, self.gated, dz=b["dpre"], db=b["db1"], h=b["h"],
+                                ws=b["act_ws"])
+        moe_expert_wgrad(b["d_eo"], b["h"], offsets, dw=b["dw2"], rows=rows)
+        moe_permute(x, send_pos, k, None, b["x_perm"])
+        moe_expert_wgrad(b["dpre"], b["x_perm"], offsets, dw=b["dw1"], rows=rows)
+        moe_expert_dgrad(b["dpre"], offsets, self.w1, b["d_perm"], b["dgrad_ws"])
+        rest = None
+        if self.w_r is not None:
+            moe_router_backward(self.topk_gate, b["dg"], offsets, src_slot, x, b["dz"], b["dw_r"])
+            rest = moe_router_input_grad(self.w_r, self.topk_idx, b["dz"], None, b["dx_r"])
+        moe_combine(b["d_perm"], send_pos, None, rest, b["dx"], k=k)
+        return b
 
 
 class PipelinedMoE:

@@ -320,3 +320,49 @@ def test_host_tensors_are_refused():
     dy, rng = torch.zeros(6, 16), torch.zeros(2, dtype=torch.int64)
     with pytest.raises(ValueError, match="device tensors"):
         moe.moe_dropout(dy, 0.1, rng)
+
+
+# ------------------------------------------------------------------------------- the layers
+
+def test_layers_refuse_dropout_without_a_state_and_stay_as_they_were():
+    from combine_grouped_gemm_amd.layer import BiasedMoELayer, MoELayer
+    N, H, E, k, I = 6, 128, 4, 2, 128
+    bf = torch.bfloat16
+    layer = MoELayer(N, H, E, k, I, "bf16", torch.zeros(E, 2 * I, H, dtype=bf), torch.zeros(E, H, I, dtype=bf),
+                     w_r=torch.zeros(E, H, dtype=bf))
+    biased = BiasedMoELayer(N, H, E, k, I, torch.zeros(E, I, H, dtype=bf), torch.zeros(E, H, I, dtype=bf),
+                            w_r=torch.zeros(E, H, dtype=bf))
+    x, rng = torch.zeros(N, H, dtype=bf), torch.zeros(2, dtype=torch.int64)
+    layer.drop_p, layer.keep8, biased.drop_p, biased.saved = 0.125, True, 0.125, True
+    for bad in (dict(dropout=-0.1, rng=rng), dict(dropout=1.5, rng=rng), dict(dropout=0.1), dict(dropout=0.1, rng=rng[:1]),
+                dict(dropout=0.1, rng=rng.int()), dict(residual=x.float()), dict(residual=x[:5]),
+                dict(dropout=0.1, rng=rng.to("meta")), dict(dropout=float("nan"), rng=rng)):
+        for lay in (layer, biased):
+            with pytest.raises(ValueError):
+                lay.forward(x, **bad)
+    assert layer.drop_p == 0.125 and layer.keep8 and layer.rng_used is None and biased.drop_p == 0.125 and biased.saved
+
+
+def test_biased_layer_refusals():
+    from combine_grouped_gemm_amd.layer import BiasedMoELayer
+    bf = torch.bfloat16
+    good = dict(N=6, H=128, E=4, k=2, I=64, w1=torch.zeros(4, 64, 128, dtype=bf), w2=torch.zeros(4, 128, 64, dtype=bf),
+                b1=torch.zeros(4, 64), b2=torch.zeros(4, 128, dtype=bf))
+    BiasedMoELayer(**good)
+    for bad in (dict(act=6), dict(act=-1), dict(gated=True), dict(w1=good["w1"].float()), dict(w2=good["w2"][:, :64]),
+                dict(w1=good["w1"].half(), w2=good["w2"].half()), dict(b1=torch.zeros(4, 128)), dict(b2=torch.zeros(4, 128).half()),
+                dict(w_r=torch.zeros(4, 128)), dict(bias=torch.zeros(4, dtype=bf))):
+        with pytest.raises(ValueError):
+            BiasedMoELayer(**{**good, **bad})
+    layer = BiasedMoELayer(**good)
+    x = torch.zeros(6, 128, dtype=bf)
+    with pytest.raises(ValueError, match="logits"):
+        layer.forward(x)
+    for bad in (dict(x=x[:5]), dict(x=x.float()), dict(z=torch.zeros(6, 5)), dict(z=torch.zeros(6, 4, dtype=bf))):
+        with pytest.raises(ValueError):
+            layer.forward(**{**dict(x=x, z=torch.zeros(6, 4)), **bad})
+    with pytest.raises(ValueError, match="multiples of 128"):
+        layer.backward(x, x)
+    fits = BiasedMoELayer(6, 128, 4, 2, 128, torch.zeros(4, 128, 128, dtype=bf), torch.zeros(4, 128, 128, dtype=bf))
+    with pytest.raises(ValueError, match="save_for_backward"):
+        fits.backward(x, x)
