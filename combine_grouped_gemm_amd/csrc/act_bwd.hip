@@ -8,6 +8,8 @@
 // over its lanes in a fixed order, and writes one row of partial sums per (range, expert) that meet;
 // a second kernel adds an expert's partial rows in order.  Range c and expert e meet in place c + e of
 // the partial rows: along the rows either c or e grows by one, so no two pairs share a place.
+#include <type_traits>
+
 #include "activation.h"
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -31,30 +33,13 @@ struct ActBwdArgs {
 
 template <bool F32>
 __device__ __forceinline__ void get8(const void* p, size_t i, float (&v)[8]) {   // 8 values of group i
-  Raw8<F32> r;
-  if (F32) {
-    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i);
-    r.w[F32 ? 1 : 0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i + 1);
-  } else {
-    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + i);
-  }
-  raw_values<F32>(r, v);
-}
-template <bool F32>
-__device__ __forceinline__ void put8(void* p, size_t i, const float (&v)[8]) {
-  if (F32) {
-    float4* q = reinterpret_cast<float4*>(p) + 2 * i;
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    reinterpret_cast<uint4*>(p)[i] =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
+  raw_values<F32>(load_group<F32>(p, i), v);
 }
 
 __device__ __forceinline__ int clamp_row(int r, int rows) { return r < 0 ? 0 : (r > rows ? rows : r); }
 
-template <bool F32, bool GATED>
+// NT: dz and h past the caches
+template <bool F32, bool GATED, bool NT>
 __global__ __launch_bounds__(kActThreads) void act_backward_kernel(ActBwdArgs p) {
   constexpr int kHalves = GATED ? 2 : 1;
   __shared__ float4 red[kActThreads * 2 * kHalves];
@@ -66,13 +51,8 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(ActBwdArgs p)
   const int r0 = c * p.range, r1 = p.rows - r0 < p.range ? p.rows : r0 + p.range;
   int e = 0, lo = 0, hi = p.rows;
   if (p.offsets != nullptr) {   // the first expert that ends behind r0
-    int a = 0, b = p.E;
-    while (a < b) {
-      const int m = (a + b) >> 1;
-      if (p.offsets[m + 1] > r0) b = m;
-      else a = m + 1;
-    }
-    e = a;
+    const int lane = threadIdx.x & 63;   // (every wave counts the experts that end at or before r0)
+    for (int b = 0; b < p.E; b += 64) e += __popcll(__ballot(b + lane < p.E && p.offsets[b + lane + 1] <= r0));
   }
   for (; e < p.E; ++e) {
     if (p.offsets != nullptr) {
@@ -103,10 +83,10 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(ActBwdArgs p)
             sum[kHalves - 1][i] += u[i];
           }
           if (p.dz != nullptr) {
-            put8<F32>(p.dz, static_cast<size_t>(r) * gw + g, s);
-            put8<F32>(p.dz, static_cast<size_t>(r) * gw + groups + g, u);
+            store_group<F32, NT>(p.dz, static_cast<size_t>(r) * gw + g, s);
+            store_group<F32, NT>(p.dz, static_cast<size_t>(r) * gw + groups + g, u);
           }
-          if (p.h != nullptr) put8<F32>(p.h, static_cast<size_t>(r) * groups + g, h);
+          if (p.h != nullptr) store_group<F32, NT>(p.h, static_cast<size_t>(r) * groups + g, h);
         } else if (p.z != nullptr) {
           get8<F32>(p.z, static_cast<size_t>(r) * groups + g, u);
           act8_slope<F32>(p.act, u, s);
@@ -115,12 +95,12 @@ __global__ __launch_bounds__(kActThreads) void act_backward_kernel(ActBwdArgs p)
             s[i] *= d[i];
             sum[0][i] += s[i];
           }
-          if (p.dz != nullptr) put8<F32>(p.dz, static_cast<size_t>(r) * groups + g, s);
-          if (p.h != nullptr) put8<F32>(p.h, static_cast<size_t>(r) * groups + g, u);
+          if (p.dz != nullptr) store_group<F32, NT>(p.dz, static_cast<size_t>(r) * groups + g, s);
+          if (p.h != nullptr) store_group<F32, NT>(p.h, static_cast<size_t>(r) * groups + g, u);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[0][i] += d[i];
-          if (p.dz != nullptr) put8<F32>(p.dz, static_cast<size_t>(r) * groups + g, d);
+          if (p.dz != nullptr) store_group<F32, NT>(p.dz, static_cast<size_t>(r) * groups + g, d);
         }
       }
     }
@@ -234,13 +214,19 @@ hipError_t launch_act_backward(const void* z, const void* d_out, bool f32, const
   p.act = act;
   p.db_f32 = db_f32;
   p.lx = act_lx(N);
+  const bool nt = stream_stores(static_cast<size_t>(rows) * N * (f32 ? 4 : 2) * (gated ? 2 : 1));
   p.range = rows > 0 ? act_range(rows, gated ? 2 * N : N) : 1;
   if (rows > 0) {
     const dim3 grid((N / 8 + p.lx - 1) / p.lx, (rows + p.range - 1) / p.range), block(kActThreads);
-    if (f32 && gated) hipLaunchKernelGGL((act_backward_kernel<true, true>), grid, block, 0, s, p);
-    else if (f32) hipLaunchKernelGGL((act_backward_kernel<true, false>), grid, block, 0, s, p);
-    else if (gated) hipLaunchKernelGGL((act_backward_kernel<false, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((act_backward_kernel<false, false>), grid, block, 0, s, p);
+    auto go = [&](auto f, auto g) {
+      constexpr bool F = decltype(f)::value, G = decltype(g)::value;
+      if (nt) hipLaunchKernelGGL((act_backward_kernel<F, G, true>), grid, block, 0, s, p);
+      else hipLaunchKernelGGL((act_backward_kernel<F, G, false>), grid, block, 0, s, p);
+    };
+    if (f32 && gated) go(std::true_type{}, std::true_type{});
+    else if (f32) go(std::true_type{}, std::false_type{});
+    else if (gated) go(std::false_type{}, std::true_type{});
+    else go(std::false_type{}, std::false_type{});
   }
   if (db != nullptr) {
     const int Nw = gated ? 2 * N : N;

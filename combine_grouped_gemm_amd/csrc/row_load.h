@@ -1,4 +1,4 @@
-// Row loads shared by the combine kernels: 8 adjacent columns of a row of fp32 or bf16.
+// Loads and stores of 8 adjacent columns of a row of fp32 or bf16, shared by the kernels that move rows.
 #pragma once
 
 #include "moe_common.h"
@@ -72,6 +72,45 @@ __device__ __forceinline__ void raw_values(const Raw8<kEoF32>& r, float (&v)[8])
       v[2 * i + 1] = bf16_to_f32(static_cast<uint16_t>(w[i] >> 16));
     }
   }
+}
+
+// 8 values (8 adjacent elements) to group i of a matrix of fp32 or bf16; NT: with the non-temporal hint (a
+// constant: of two branches that differ in the hint alone the compiler makes one, without it)
+template <bool F32, bool NT = false>
+__device__ __forceinline__ void store_group(void* p, size_t i, const float (&v)[8]) {
+  typedef float f32x4s_t __attribute__((ext_vector_type(4)));
+  if (F32) {
+    f32x4s_t* q = reinterpret_cast<f32x4s_t*>(p) + 2 * i;
+    const f32x4s_t a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+    if constexpr (NT) {
+      __builtin_nontemporal_store(a, q);
+      __builtin_nontemporal_store(b, q + 1);
+    } else {
+      q[0] = a;
+      q[1] = b;
+    }
+  } else {
+    const stream_word_t w{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                          pack_bf16x2(v[6], v[7])};
+    stream_word_t* q = reinterpret_cast<stream_word_t*>(p) + i;
+    if constexpr (NT) __builtin_nontemporal_store(w, q);
+    else *q = w;
+  }
+}
+// whether an output of this many bytes is written past the caches: from the 256 MB that the last-level
+// cache holds on, what is written first is gone before the next kernel reads it
+__host__ inline bool stream_stores(size_t bytes) { return bytes >= (size_t{256} << 20); }
+
+template <bool F32>
+__device__ __forceinline__ Raw8<F32> load_group(const void* p, size_t i) {   // 8 values of group i, read once
+  Raw8<F32> r;
+  if (F32) {
+    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i);
+    r.w[F32 ? 1 : 0] = load_stream(reinterpret_cast<const uint4*>(p) + 2 * i + 1);
+  } else {
+    r.w[0] = load_stream(reinterpret_cast<const uint4*>(p) + i);
+  }
+  return r;
 }
 
 }  // namespace moe

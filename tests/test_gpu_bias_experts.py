@@ -371,3 +371,25 @@ def test_bias_gradient_of_many_rows():
     _, db, _ = moe.moe_expert_act_backward(d, offsets=off, want_dz=False)
     sync()
     assert [db[e].unique().tolist() for e in range(4)] == [[1.0], [200000.0], [0.0], [99999.0]]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_act_backward_of_large_calls(gated):
+    """From 256 MB on dz and h are stored past the caches: the same bits as for a few rows at a time."""
+    rows, N = (17000, 4104) if gated else (34000, 4104)
+    say(f"act backward of large calls gated={gated}")
+    z = torch.randn(rows, 2 * N if gated else N, device=DEV).to(BF)
+    d = torch.randn(rows, N, device=DEV).to(BF)
+    off = torch.tensor([0, 5000, rows], dtype=torch.int32, device=DEV)
+    kw = dict(act=ACT["silu"], gated=gated, want_h=True)
+    dz, db, h = moe.moe_expert_act_backward(d, z=z, offsets=off, **kw)
+    sync()
+    sums = torch.zeros(2, z.shape[1], dtype=torch.float64, device=DEV)
+    for a in range(0, rows, 1000):
+        dz1, db1, h1 = moe.moe_expert_act_backward(d[a:a + 1000], z=z[a:a + 1000], **kw)
+        sync()
+        assert torch.equal(dz1, dz[a:a + 1000]) and torch.equal(h1, h[a:a + 1000])
+        sums[int(a >= 5000)] += db1[0].double()
+    mag = torch.stack([dz[:5000].abs().double().sum(dim=0), dz[5000:].abs().double().sum(dim=0)])
+    # two fp32 sums of the same values in other orders: at most rows + 8 roundings of the magnitudes' sum each
+    assert ((db.double() - sums).abs() <= 2 * (rows + 8) * U32 * mag).all()
