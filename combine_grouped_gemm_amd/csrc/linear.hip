@@ -207,55 +207,50 @@ __device__ __forceinline__ void lin_finish_one(const LinearArgs& p, int e, size_
   lin_finish<F32, GATED>(p, row, col, v, w, bv, bw, res);
 }
 
-// The tile of this workgroup: m-tiles of TM rows of every expert, in the order expert -> group of 8
+// The tile of this workgroup: m-tiles of at most TM rows of every expert, in the order expert -> group of 8
 // m-tiles -> column block -> m-tile of the group (the tiles that share weight rows, and those that share
 // activation rows, run close together); contiguous ranges of the order go to the XCDs (workgroup i runs
 // on XCD i mod 8).  The launch has as many workgroups as any routing can need; false: nothing to do.
+// Every wave searches for itself, an expert a lane (E > 64: first the run of up to 16 experts, a run a
+// lane), so that the search costs one or two memory latencies and no barrier.
 struct LinTile {
   int e, m0, mend, nblk, part;
 };
-template <int TM, int THREADS>
-__device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* scan, LinTile& t) {
-  int total = 0;
-  const int tid = threadIdx.x;
-  if (p.E == 1) {
-    int lo, hi;
-    lin_segment(p, 0, lo, hi);
-    total = (hi - lo + TM - 1) / TM;
-  } else {
-    // scan[e]: m-tiles before expert e; 4 experts a thread (E <= 1024), 256 threads
-    int32_t* part = scan + MOE_MAX_EXPERTS + 1;
-    int n[4], sum = 0;
-    if (tid < 256) {
+
+__device__ __forceinline__ int wave_prefix(int v) {   // sum over lanes up to this one
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 4 * tid + i;
-        int lo = 0, hi = 0;
-        if (e < p.E) lin_segment(p, e, lo, hi);
-        n[i] = (hi - lo + TM - 1) / TM;
-        sum += n[i];
-      }
+  for (int off = 1; off < 64; off <<= 1) {
+    const int u = __shfl_up(v, off, 64);
+    if (lane >= off) v += u;
+  }
+  return v;
+}
+
+template <int TM>
+__device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t) {
+  const int lane = threadIdx.x & 63;
+  auto tiles_of = [](int lo, int hi) { return (hi - lo + TM - 1) / TM; };
+  int run = 1, run_sum = 0, run_end = 0, total = 0;
+  if (p.E > 64) {
+    run = (p.E + 63) / 64;
+    for (int i = 0; i < run; ++i) {
+      int lo = 0, hi = 0;
+      if (lane * run + i < p.E) lin_segment(p, lane * run + i, lo, hi);
+      run_sum += tiles_of(lo, hi);
     }
-    int inc = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(inc, off, 64);
-      if ((tid & 63) >= off) inc += v;
-    }
-    if ((tid & 63) == 63 && tid < 256) part[tid >> 6] = inc;
-    __syncthreads();
-    if (tid < 256) {
-      int at = inc - sum;
-      for (int w = 0; w < (tid >> 6); ++w) at += part[w];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (4 * tid + i <= p.E) scan[4 * tid + i] = at;
-        at += n[i];
-      }
-      if (tid == 255 && p.E == MOE_MAX_EXPERTS) scan[MOE_MAX_EXPERTS] = at;
-    }
-    __syncthreads();
-    total = scan[p.E];
+    run_end = wave_prefix(run_sum);
+    total = __builtin_amdgcn_readlane(run_end, 63);
+  }
+  int e0 = 0, before = 0, lo = 0, hi = 0, end = 0;
+  auto expert_lanes = [&](int n) __attribute__((always_inline)) {   // experts e0 .. e0 + n - 1
+    lo = hi = 0;
+    if (lane < n) lin_segment(p, e0 + lane, lo, hi);
+    end = before + wave_prefix(tiles_of(lo, hi));
+  };
+  if (p.E <= 64) {
+    expert_lanes(p.E);
+    total = __builtin_amdgcn_readlane(end, 63);
   }
   const long long tiles = static_cast<long long>(total) * nN, all = tiles * p.split;
   const long long per = (all + kNumXcd - 1) / kNumXcd;
@@ -267,27 +262,24 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* s
     t.part = static_cast<int>(L / tiles);
     L -= t.part * tiles;
   }
-  int e = 0, before = 0, mt = total;
-  if (p.E > 1) {   // the last expert whose tiles start at or before L (an empty expert has none)
-    int a = 0, b = p.E - 1;
-    while (a < b) {
-      const int m = (a + b + 1) >> 1;
-      if (static_cast<long long>(scan[m]) * nN <= L) a = m;
-      else b = m - 1;
-    }
-    e = __builtin_amdgcn_readfirstlane(a);
-    before = __builtin_amdgcn_readfirstlane(scan[e]);
-    mt = __builtin_amdgcn_readfirstlane(scan[e + 1]) - before;
+  if (p.E > 64) {
+    const int l = __builtin_ctzll(__ballot(static_cast<long long>(run_end) * nN > L));
+    e0 = l * run;
+    before = __builtin_amdgcn_readlane(run_end - run_sum, l);
+    expert_lanes(p.E - e0 < run ? p.E - e0 : run);
   }
-  const int local = static_cast<int>(L - static_cast<long long>(before) * nN);
+  // the expert: the first whose tiles end behind L (of an empty expert nothing does)
+  const int l = __builtin_ctzll(__ballot(static_cast<long long>(end) * nN > L));
+  lo = __builtin_amdgcn_readlane(lo, l);
+  hi = __builtin_amdgcn_readlane(hi, l);
+  t.e = e0 + l;
+  const int mt = tiles_of(lo, hi);
+  const int local = static_cast<int>(L - static_cast<long long>(__builtin_amdgcn_readlane(end, l) - mt) * nN);
   constexpr int kGroup = 8;
   const int grp = local / (kGroup * nN), in = local - grp * kGroup * nN;
   const int gm = mt - grp * kGroup < kGroup ? mt - grp * kGroup : kGroup;
   const int mtile = grp * kGroup + in % gm;
   t.nblk = in / gm;
-  t.e = e;
-  int lo, hi;
-  lin_segment(p, e, lo, hi);
   const int rpt = ((hi - lo + mt - 1) / mt + 31) / 32 * 32;   // (at most TM, a multiple of 32)
   t.m0 = lo + mtile * rpt;
   t.mend = t.m0 + rpt < hi ? t.m0 + rpt : hi;
@@ -297,7 +289,7 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int32_t* s
 // WM x WN waves; a wave's block is (TM / WM) x (TN / WN) as 32 x 32 products
 template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p) {
-  constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  constexpr int kWaves = WM * WN;
   constexpr int MB = TM / WM / 32, NB = TN / WN / 32;
   constexpr int kLdA = TM / 8 / kWaves, kLdW = TN / 8 / kWaves;   // loads a wave and stage
   constexpr int kStage = (TM + TN) * kLinRow;
@@ -305,13 +297,11 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   static_assert(MB * WM * 32 == TM && NB * WN * 32 == TN && kLdA * kWaves * 8 == TM && kLdW * kWaves * 8 == TN, "tile");
   static_assert(!GATED || NB % 2 == 0, "a wave holds both factors");
   __shared__ __attribute__((aligned(16))) uint8_t lds[S * kStage];
-  static_assert(S * kStage >= (MOE_MAX_EXPERTS + 8) * 4, "the tile search shares the LDS");
 
   constexpr int kCols = GATED ? TN / 2 : TN;   // output columns of a tile
   const int nN = (p.N + kCols - 1) / kCols;
   LinTile t;
-  if (!lin_tile<TM, kThreads>(p, nN, reinterpret_cast<int32_t*>(lds), t)) return;
-  __syncthreads();   // (the search's words have been read)
+  if (!lin_tile<TM>(p, nN, t)) return;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
