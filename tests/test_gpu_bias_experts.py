@@ -70,8 +70,8 @@ def _linear_reference(a, off, w, bias, act, gated, residual, tokens, dt):
     z, mag = np.full((rows, Nw), np.nan), np.full((rows, Nw), np.nan)
     for e in range(E):
         r = slice(int(off[e]), int(off[e + 1]))
-        we = f64(w[e])
-        z[r], mag[r] = x[r] @ we.T, np.abs(x[r]) @ np.abs(we).T
+        xe, we = torch.from_numpy(x[r]).to(DEV), w[e].double().to(DEV)   # (64-bit products on the GPU)
+        z[r], mag[r] = (xe @ we.T).cpu().numpy(), (xe.abs() @ we.abs().T).cpu().numpy()
         if bias is not None:
             z[r] += f64(bias[e])
             mag[r] += np.abs(f64(bias[e]))
@@ -139,6 +139,41 @@ SIZES = [(1, 1, 8, 8), (1, 8, 64, 264), (2, 3, 72, 40), (7, 2, 136, 8), (16, 1, 
 @pytest.mark.parametrize("rows,E,K,N", SIZES)
 def test_sizes(rows, E, K, N, gated, dt):
     _run_linear(rows, E, K, N, dt, gated=gated, seed=rows)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,E,K,Nw,k,dt", [
+    # 320 x 256 tiles: whole ones, ragged experts of every row-block count, one column block more than whole
+    (4000, 1, 2048, 2304, 0, BF), (5000, 8, 1032, 4112, 0, BF), (4100, 1, 1032, 4112, 3, BF),
+    # 128 x 256 tiles, alone and with K in parts
+    (3000, 1, 1024, 2304, 0, BF), (1100, 4, 1032, 4112, 2, BF), (512, 1, 14336, 4096, 0, BF),
+    # K in parts under 320 x 256 tiles
+    (1024, 1, 14336, 4096, 0, BF), (900, 2, 14336, 4112, 2, BF),
+    # 64 x 64 tiles with K in 4, 8 and 16 parts; a last part of one partial stage
+    (600, 1, 8200, 1040, 0, BF), (64, 1, 4104, 272, 2, BF), (33, 1, 3336, 48, 0, BF),
+    # fp32: 128 x 128 tiles, alone and with K in parts; 64 x 64 ones with K in parts
+    (3000, 4, 520, 2064, 0, F32), (1000, 1, 14336, 1040, 0, F32), (200, 1, 4104, 528, 2, F32)])
+def test_every_kernel(rows, E, K, Nw, k, dt, gated):
+    """Sizes that take each of the tile kernels, with residual, kept z and a gated or plain epilogue."""
+    _run_linear(rows, E, K, Nw // 2 if gated else Nw, dt, "gelu" if gated else "silu", gated, "f32", True, k, seed=rows)
+
+
+def test_operands_past_32_bits():
+    """Rows of a and of out whose byte offsets pass 2^32."""
+    rows, n = 300000, 40
+    for K, N in ((8200, 8), (8, 8200)):
+        say(f"linear rows={rows} K={K} N={N}")
+        a, w = torch.randn(rows, K, device=DEV, dtype=BF), torch.randn(2, N, K, device=DEV, dtype=BF)
+        off = torch.tensor([0, rows - 100, rows], dtype=torch.int32, device=DEV)
+        out, _ = moe.moe_expert_linear(a, w, offsets=off, act=ACT["relu"])
+        few, _ = moe.moe_expert_linear(a[-n:], w[1:], act=ACT["relu"])
+        sync()
+        # other tiles sum K in another order: two fp32 sums of K products each, then a rounding each
+        x64, w64 = a[-n:].double(), w[1].double()
+        err = 4 * (K + 16) * U32 * (x64.abs() @ w64.abs().T) + 2 * 2.0 ** -8 * few.double().abs()
+        assert ((out[-n:].double() - few.double()).abs() <= err).all()
+        del a, out
+        torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("dt", [F32, BF])
