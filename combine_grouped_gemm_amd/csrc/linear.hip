@@ -402,27 +402,35 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
     constexpr int ACT = decltype(act_c)::value;   // row blocks of this wave that hold rows
     constexpr int kSlots = ACT > 0 ? ACT * NB : 1, kReads = ACT > 0 ? ACT + NB : 0;
     uint4 f0[ACT + NB], f1[ACT + NB];   // fragments of this k-step and of the next: rows of a, weight rows
+    // fragment r in the order of its first use: a's block 0, the weight blocks, a's other blocks
     auto read = [&](uint4(&f)[ACT + NB], int r, int slot, int s) __attribute__((always_inline)) {
       const uint8_t* st = lds + slot * kStage;
-      f[r] = *reinterpret_cast<const uint4*>(
-          (r < ACT ? st + a_row(r) * kLinRow : st + TM * kLinRow + w_row(r - ACT) * kLinRow) + fb[s]);
+      const int m = r == 0 ? 0 : r - NB, n = r - 1;
+      if (r >= 1 && r <= NB)
+        f[ACT + n] = *reinterpret_cast<const uint4*>(st + TM * kLinRow + w_row(n) * kLinRow + fb[s]);
+      else
+        f[m] = *reinterpret_cast<const uint4*>(st + a_row(m) * kLinRow + fb[s]);
     };
-    // the products of a k-step; between them the reads of the next (slot, s) and the loads of a later stage
+    // the products of a k-step; ahead of each the next reads of the k-step after it (slot, s), so that the
+    // last have landed when that begins, and behind each the next loads of a later stage
+    constexpr int kReadEach = (kReads + kSlots - 1) / kSlots, kLoadEach = (kLoads + kSlots - 1) / kSlots;
     auto step = [&]<bool READ, bool LOAD>(const uint4(&f)[ACT + NB], uint4(&n)[ACT + NB], int slot, int s,
                                           const Stage& g) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kSlots; ++i) {
-        if constexpr (ACT > 0) acc[i / NB][i % NB] = lin_mma<F32>(f[ACT + i % NB], f[i / NB], acc[i / NB][i % NB]);
-        __builtin_amdgcn_sched_barrier(0);
         if constexpr (READ) {
 #pragma unroll
-          for (int r = kReads * i / kSlots; r < kReads * (i + 1) / kSlots; ++r) read(n, r, slot, s);
-        }
-        if constexpr (LOAD) {
-#pragma unroll
-          for (int j = kLoads * i / kSlots; j < kLoads * (i + 1) / kSlots; ++j) load_one(g, j);
+          for (int r = kReadEach * i; r < kReadEach * (i + 1); ++r)
+            if (r < kReads) read(n, r, slot, s);
         }
         __builtin_amdgcn_sched_barrier(0);
+        if constexpr (ACT > 0) acc[i / NB][i % NB] = lin_mma<F32>(f[ACT + i % NB], f[i / NB], acc[i / NB][i % NB]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (LOAD) {
+#pragma unroll
+          for (int j = kLoadEach * i; j < kLoadEach * (i + 1); ++j)
+            if (j < kLoads) load_one(g, j);
+        }
       }
     };
     int slot = 0;
