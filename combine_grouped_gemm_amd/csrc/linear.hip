@@ -49,6 +49,7 @@ struct LinearArgs {
   const int32_t* a_rows;     // [rows] or null: row r is row a_rows[r] / a_div of a
   int a_div, a_nrows;
   int E, rows, K, N, act, bias_f32;
+  int tile_rows;             // rows of a tile at most: the tile's, or fewer (linear_tile_kernel)
   float* part;               // split K: [split, rows, Nw] sums instead of the epilogue, or null
   int split;
 };
@@ -207,7 +208,7 @@ __device__ __forceinline__ void lin_finish_one(const LinearArgs& p, int e, size_
   lin_finish<F32, GATED>(p, row, col, v, w, bv, bw, res);
 }
 
-// The tile of this workgroup: m-tiles of at most TM rows of every expert, in the order expert -> group of 8
+// The tile of this workgroup: m-tiles of at most tile_rows rows of every expert, in the order expert -> group of 8
 // m-tiles -> column block -> m-tile of the group (the tiles that share weight rows, and those that share
 // activation rows, run close together); contiguous ranges of the order go to the XCDs (workgroup i runs
 // on XCD i mod 8).  The launch has as many workgroups as any routing can need; false: nothing to do.
@@ -227,10 +228,9 @@ __device__ __forceinline__ int wave_prefix(int v) {   // sum over lanes up to th
   return v;
 }
 
-template <int TM>
 __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t) {
   const int lane = threadIdx.x & 63;
-  auto tiles_of = [](int lo, int hi) { return (hi - lo + TM - 1) / TM; };
+  auto tiles_of = [&](int lo, int hi) { return (hi - lo + p.tile_rows - 1) / p.tile_rows; };
   int run = 1, run_sum = 0, run_end = 0, total = 0;
   if (p.E > 64) {
     run = (p.E + 63) / 64;
@@ -280,7 +280,7 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t
   const int gm = mt - grp * kGroup < kGroup ? mt - grp * kGroup : kGroup;
   const int mtile = grp * kGroup + in % gm;
   t.nblk = in / gm;
-  const int rpt = ((hi - lo + mt - 1) / mt + 31) / 32 * 32;   // (at most TM, a multiple of 32)
+  const int rpt = ((hi - lo + mt - 1) / mt + 31) / 32 * 32;   // (at most tile_rows, which 32 divides)
   t.m0 = lo + mtile * rpt;
   t.mend = t.m0 + rpt < hi ? t.m0 + rpt : hi;
   return t.m0 < t.mend;
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   constexpr int kCols = GATED ? TN / 2 : TN;   // output columns of a tile
   const int nN = (p.N + kCols - 1) / kCols;
   LinTile t;
-  if (!lin_tile<TM>(p, nN, t)) return;
+  if (!lin_tile(p, nN, t)) return;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -760,12 +760,13 @@ void launch_few(const LinearArgs& p, hipStream_t s) {
 }
 
 template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
-void launch_tiles(LinearArgs p, hipStream_t s, int split = 1, void* ws = nullptr) {
+void launch_tiles(LinearArgs p, hipStream_t s, int split, int tile_rows, void* ws) {
   constexpr int kCols = GATED ? TN / 2 : TN;
   const int stages = (p.K * (F32 ? 4 : 2) + kLinRow - 1) / kLinRow;
   if (split > stages) split = stages;   // (every part of K has a stage)
   const long long nN = (p.N + kCols - 1) / kCols;
-  const long long mt = (p.rows + TM - 1) / TM + (p.E > 1 ? (p.E - 1 < p.rows ? p.E - 1 : p.rows) : 0);
+  p.tile_rows = tile_rows > 0 && tile_rows < TM ? tile_rows : TM;
+  const long long mt = (p.rows + p.tile_rows - 1) / p.tile_rows + (p.E > 1 ? (p.E - 1 < p.rows ? p.E - 1 : p.rows) : 0);
   const long long grid = (mt * nN * split + kNumXcd - 1) / kNumXcd * kNumXcd;
   p.split = split;
   p.part = split > 1 ? static_cast<float*>(ws) : nullptr;
@@ -793,7 +794,7 @@ namespace {
 //     320 x 256         68   72   90   92  107    292  340  334  347     4096 rows of K 14336: 408 (128 x 256: 432)
 enum { LIN_FEW, LIN_64, LIN_128, LIN_320 };
 struct LinPlan {
-  int kind, split;
+  int kind, split, tile_rows;
 };
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
@@ -805,12 +806,12 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
   const int hit = E < rows ? E : rows;
   const double each = static_cast<double>(rows) / hit;
   const double mem = (hit * Nw * row + rows * (row + 1.0 * Nw * esz)) / 5.2e6;
-  LinPlan best{LIN_64, 1};
+  LinPlan best{LIN_64, 1, 0};
   double best_us = 1e30;
   if (each <= 32) {
     const double more = each > 16 ? 1.3 : E > 1 && each > 8 ? 1.05 : 1.0;   // (some experts' weights twice)
     const double waves = ceil_div(hit * ceil_div(Nw, 32), 512) * stages / 4 * 0.3 * more * (f32 ? 1.5 : 1.0);
-    best = LinPlan{LIN_FEW, 1};
+    best = LinPlan{LIN_FEW, 1, 0};
     best_us = 4 + (mem * more > waves ? mem * more : waves);
   }
   struct Shape {
@@ -822,17 +823,30 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
   static const Shape f32_shapes[] = {{LIN_64, 64, 64, 1, 3, 5, 0.6, 0.6}, {LIN_128, 128, 128, 1, 2, 6, 1.0, 2.0}};
   for (int i = 0; i < (f32 ? 2 : 3); ++i) {
     const Shape& s = f32 ? f32_shapes[i] : bf16_shapes[i];
-    // m-tiles of an expert: uneven experts, a standard deviation of random routes above the mean
-    const double mt = E == 1 ? static_cast<double>(ceil_div(rows, s.tm))
-                             : 1.0 * hit * ceil_div(static_cast<long long>(each + __builtin_sqrt(each)), s.tm);
-    const double tiles = mt * ceil_div(Nw, s.tn);
-    const double stage = s.latency + (s.full - s.latency) * (rows / (mt * s.tm));
-    const double l2 = tiles * (s.tm + s.tn) * row / 1.7e7;   // what the tiles load, at 17 TB/s
+    // m-tiles: uneven experts, a standard deviation of random routes above the mean
+    const double even = E == 1 ? static_cast<double>(ceil_div(rows, s.tm))
+                               : 1.0 * hit * ceil_div(static_cast<long long>(each + __builtin_sqrt(each)), s.tm);
+    const long long nN = ceil_div(Nw, s.tn);
+    const double l2 = even * nN * (s.tm + s.tn) * row / 1.7e7;   // what the tiles load, at 17 TB/s
     for (int split = 1; split <= 16 && split * 8 <= (stages > 8 ? stages : 8); split *= 2) {
-      const double turns = tiles * split / (256.0 * s.per_cu);
+      const double turns = even * nN * split / (256.0 * s.per_cu);
       const double rounds = turns <= 1               ? 1.0
                             : E == 1 || turns < 4.0 ? static_cast<double>(static_cast<long long>(turns + (E == 1 ? 0.999 : 0.94)))
                                                      : turns + 0.15;   // (the tiles of uneven experts are an estimate)
+      // one expert on 320-row tiles: as many as the rounds have room for, so shorter ones (4096 x 14336 x
+      // 4096: 256 tiles of 256 rows 375 us, 208 of 320 389; where the rounds are full 320 rows win: N 14336
+      // of K 4096, 728 tiles 370 us, 896 of 256 rows 419)
+      int tile_rows = 0;
+      double mt = even;
+      if (E == 1 && s.kind == LIN_320 && rounds * 256 / (nN * split) > mt) {
+        const long long room = static_cast<long long>(rounds) * 256 / (nN * split);
+        const long long tr = ceil_div(ceil_div(rows, room), 64) * 64;
+        if (tr >= 192 && tr < s.tm) {
+          tile_rows = static_cast<int>(tr);
+          mt = static_cast<double>(ceil_div(rows, tr));
+        }
+      }
+      const double stage = s.latency + (s.full - s.latency) * (rows / (mt * s.tm));
       const double turn_overhead = s.overhead * (rounds * s.per_cu > s.resident ? rounds * s.per_cu / s.resident : 1.0);
       double us = rounds * stage * stages / split + turn_overhead;
       if (us < mem + s.overhead) us = mem + s.overhead;
@@ -840,7 +854,7 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
       if (split > 1) us += 3 + 8.0 * split * rows * Nw / 4e6;
       if (us < best_us) {
         best_us = us;
-        best = LinPlan{s.kind, split};
+        best = LinPlan{s.kind, split, tile_rows};
       }
     }
   }
@@ -884,10 +898,10 @@ hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int3
   auto go = [&](auto f, auto g) {
     constexpr bool F = decltype(f)::value, G = decltype(g)::value;
     if (plan.kind == LIN_FEW) launch_few<F, G>(p, s);
-    else if (plan.kind == LIN_64) launch_tiles<F, G, 64, G ? 128 : 64, 2, 2, 3>(p, s, plan.split, ws);
-    else if constexpr (F) launch_tiles<F, G, 128, 128, 2, 2, 2>(p, s, plan.split, ws);
-    else if (plan.kind == LIN_128) launch_tiles<F, G, 128, 256, 2, 4, 3>(p, s, plan.split, ws);
-    else launch_tiles<F, G, 320, 256, 2, 4, 2>(p, s, plan.split, ws);
+    else if (plan.kind == LIN_64) launch_tiles<F, G, 64, G ? 128 : 64, 2, 2, 3>(p, s, plan.split, 0, ws);
+    else if constexpr (F) launch_tiles<F, G, 128, 128, 2, 2, 2>(p, s, plan.split, 0, ws);
+    else if (plan.kind == LIN_128) launch_tiles<F, G, 128, 256, 2, 4, 3>(p, s, plan.split, 0, ws);
+    else launch_tiles<F, G, 320, 256, 2, 4, 2>(p, s, plan.split, plan.tile_rows, ws);
   };
   using T = std::true_type;
   using U = std::false_type;
