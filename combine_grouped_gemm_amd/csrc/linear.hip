@@ -280,7 +280,9 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t
   const int gm = mt - grp * kGroup < kGroup ? mt - grp * kGroup : kGroup;
   const int mtile = grp * kGroup + in % gm;
   t.nblk = in / gm;
-  const int rpt = ((hi - lo + mt - 1) / mt + 31) / 32 * 32;   // (at most tile_rows, which 32 divides)
+  // (a multiple of the 64 rows that two row waves share: 288 rows take a wave's five blocks as 320 do; at
+  // most tile_rows, which 64 divides)
+  const int rpt = ((hi - lo + mt - 1) / mt + 63) / 64 * 64;
   t.m0 = lo + mtile * rpt;
   t.mend = t.m0 + rpt < hi ? t.m0 + rpt : hi;
   return t.m0 < t.mend;
@@ -296,6 +298,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   constexpr int kEsz = F32 ? 4 : 2;
   static_assert(MB * WM * 32 == TM && NB * WN * 32 == TN && kLdA * kWaves * 8 == TM && kLdW * kWaves * 8 == TN, "tile");
   static_assert(!GATED || NB % 2 == 0, "a wave holds both factors");
+  static_assert(WM == 2 && TM % 64 == 0, "lin_tile deals rows to two row waves");
   __shared__ __attribute__((aligned(16))) uint8_t lds[S * kStage];
 
   constexpr int kCols = GATED ? TN / 2 : TN;   // output columns of a tile
@@ -786,12 +789,19 @@ namespace {
 // Which kernel a call runs: the few-rows kernel, or tiles of a shape with K in `split` parts.  Known on
 // the host are the sizes, not the rows an expert gets; `each` rows of `hit` experts are expected.  The
 // estimate is us = rounds x (stages x time of a stage + overhead), no less than the bytes at 5.2 TB/s, and
-// for a split the sums' way through memory.  Its constants are from measured runs (bf16, N 4096, one
-// expert, us; K 4096: 1, 64, 512, 1024, 2048 rows; K 14336: 64, 512, 1024, 2048):
-//     few               10   23    .    .    .     70    .    .    .
-//     64 x 64           22   23   33   58  111     90  130  240  439     split 4: 13, 14; K 14336: 35 at 64
-//     128 x 256         37   44   51   57   65    179  194  191  207     split 4, 512 rows: 33, 71; 2, 1024: 48, 120
-//     320 x 256         68   72   90   92  107    292  340  334  347     4096 rows of K 14336: 408 (128 x 256: 432)
+// for a split the sums' way through memory.  Its constants are from measured runs of every kernel on the
+// same sizes; bf16, one expert, N 4096 (us; the smallest of each column is what the estimate takes, or
+// within 3% of it):
+//     K, rows           4096: 1   16   64  512 1024 2048    14336: 64  512 1024 2048 4096
+//     few rows              10   10   23  162  320  637            85  605 1200 2390 4770
+//     64 x 64               22   22   23   33   58  111            90  129  243  449  851
+//       K in 4 parts        13   14   15   47   85  176            35  139  253  456  822
+//     128 x 256             37   37   43   54   56   69           179  192  190  219  438
+//       K in 2 parts        24   24   28   40   49   94            98  109  124  243  438
+//       K in 4 parts        17   17   20   35   68  121            58   74  140  272  435
+//     320 x 256             69   69   72   94   94  110           297  343  333  347  401
+//       K in 4 parts        25   25   27   43   56  109            85  108  125  256  404
+// fp32, N 4096, K 4096: 2000 rows 64 x 64 594, 128 x 128 495; 200 rows 82 (4 parts 80), 256 (4 parts 80).
 enum { LIN_FEW, LIN_64, LIN_128, LIN_320 };
 struct LinPlan {
   int kind, split, tile_rows;
