@@ -100,8 +100,8 @@ _SIGS = {
     "moe_swiglu_backward_mxfp8": [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P],
     "moe_expert_linear": [_P, _I, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _SZ, _P],
     "moe_expert_act_backward": [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P, _P, _SZ, _P],
-    "moe_combine_dropout": [_P, _I, _I, _I, _I, _P, _P, _P, _P, ctypes.c_double, _P, _P, _I, _P],
-    "moe_combine_dropout_backward": [_P, _I, _I, _I, _I, _I, _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P],
+    "moe_combine_dropout": [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, ctypes.c_double, _P, _P, _I, _P],
+    "moe_combine_dropout_backward": [_P, _I, _I, _I, _I, _I, _I, _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P],
     "moe_dropout": [_P, _I, ctypes.c_int64, ctypes.c_double, _P, _P, _P, _I, _P],
     "moe_status_str": [_I],
     "moe_version": [],
@@ -1029,7 +1029,7 @@ def moe_combine_dropout(expert_out: torch.Tensor, send_pos: torch.Tensor, topk_g
     else:
         _expect("y", y, (N, H), _ACT, dev)
     _expect("residual", residual, (N, H), (y.dtype,), dev)
-    _run("moe_combine_dropout", dev, _ptr(expert_out), _dt(expert_out), N, H, k, _ptr(send_pos), _ptr(topk_gate),
+    _run("moe_combine_dropout", dev, _ptr(expert_out), _dt(expert_out), expert_out.shape[0], N, H, k, _ptr(send_pos), _ptr(topk_gate),
          _ptr(shared_out), _ptr(residual), p, _ptr(rng), _ptr(y), _dt(y), _stream(expert_out))
     return y
 
@@ -1071,7 +1071,7 @@ def moe_combine_dropout_backward(dy: torch.Tensor, send_pos: torch.Tensor, topk_
         d_shared = torch.empty((N, H), dtype=dt, device=dev) if want_shared else None
     else:
         _expect("d_shared", d_shared, (N, H), (dt,), dev)
-    _run("moe_combine_dropout_backward", dev, _ptr(dy), _dt(dy), _dt(like), N, H, k, _ptr(send_pos), _ptr(topk_gate),
+    _run("moe_combine_dropout_backward", dev, _ptr(dy), _dt(dy), _dt(like), rows, N, H, k, _ptr(send_pos), _ptr(topk_gate),
          _ptr(expert_out), p, _ptr(rng), _ptr(d_expert_out), _ptr(d_gate), _ptr(d_shared), _stream(dy))
     return d_expert_out, d_gate, d_shared
 

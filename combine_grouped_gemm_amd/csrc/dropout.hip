@@ -16,11 +16,14 @@ namespace {
 
 constexpr int kDropThreads = 256;
 
+__device__ __forceinline__ int in_rows(int r, int rows) { return r < rows ? r : -1; }   // (-1: no row)
+
 // One workgroup takes a token and a span of its columns, a lane 8 columns; the rows are summed in slot
 // order in batches of KMAX whose loads go out together, then the shared row, in fp32.
 template <int KMAX, bool EO32, bool Y32>
 __global__ __launch_bounds__(kDropThreads) void combine_dropout_kernel(
-    const void* __restrict__ eo, int H, int k, const int32_t* __restrict__ send_pos, const float* __restrict__ gate,
+    const void* __restrict__ eo, int rows, int H, int k, const int32_t* __restrict__ send_pos,
+    const float* __restrict__ gate,
     const void* __restrict__ shared, const void* residual, DropArgs drop, void* y, int spans) {
   const int t = blockIdx.x / spans, span = blockIdx.x % spans;
   const DropState ds = drop_state(drop);
@@ -40,7 +43,7 @@ __global__ __launch_bounds__(kDropThreads) void combine_dropout_kernel(
       Raw8<EO32> b[KMAX];
       int r[KMAX];
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j) r[j] = j0 + j < k ? sp[j0 + j] : -1;
+      for (int j = 0; j < KMAX; ++j) r[j] = j0 + j < k ? in_rows(sp[j0 + j], rows) : -1;
 #pragma unroll
       for (int j = 0; j < KMAX; ++j)
         if (r[j] >= 0) b[j] = load_group<EO32>(eo, static_cast<size_t>(r[j]) * groups8 + g8);
@@ -76,7 +79,7 @@ __global__ __launch_bounds__(kDropThreads) void combine_dropout_kernel(
 // summed over the workgroup at the end of a batch, in a fixed order.  8192 tokens of 7168, k 8, shared
 // rows: 398 us (5.3 TB/s) with non-temporal stores of d_expert_out, 428 without.
 template <int KMAX, bool DT32, bool DY32, bool NT>
-__global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int H, int k,
+__global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int rows, int H, int k,
                                                 const int32_t* __restrict__ send_pos, const float* __restrict__ gate,
                                                 const void* __restrict__ eo, DropArgs drop, void* __restrict__ d_eo,
                                                 float* __restrict__ d_gate, void* __restrict__ d_shared) {
@@ -91,7 +94,7 @@ __global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int
     float g[KMAX], dot[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      r[j] = j0 + j < k ? sp[j0 + j] : -1;
+      r[j] = j0 + j < k ? in_rows(sp[j0 + j], rows) : -1;
       g[j] = gate != nullptr && j0 + j < k ? gate[static_cast<size_t>(t) * k + j0 + j] : 1.0f;
       dot[j] = 0.0f;
     }
@@ -191,7 +194,7 @@ void two(bool a, bool b, F&& f) {
 
 }  // namespace
 
-hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int N, int H, int k, const int32_t* send_pos,
+hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int rows, int N, int H, int k, const int32_t* send_pos,
                                   const float* gate, const void* shared, const void* residual, double p,
                                   const uint64_t* rng, void* y, bool y_f32, hipStream_t s) {
   const int groups8 = H / 8;
@@ -206,19 +209,19 @@ hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int N, int H, int
   two(eo_f32, y_f32, [&](auto a, auto b) {
     constexpr bool A = decltype(a)::value, B = decltype(b)::value;
     if (k <= 2)
-      hipLaunchKernelGGL((combine_dropout_kernel<2, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+      hipLaunchKernelGGL((combine_dropout_kernel<2, A, B>), grid, block, 0, s, eo, rows, H, k, send_pos, gate, shared,
                          residual, d, y, spans);
     else if (k <= 4)
-      hipLaunchKernelGGL((combine_dropout_kernel<4, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+      hipLaunchKernelGGL((combine_dropout_kernel<4, A, B>), grid, block, 0, s, eo, rows, H, k, send_pos, gate, shared,
                          residual, d, y, spans);
     else
-      hipLaunchKernelGGL((combine_dropout_kernel<8, A, B>), grid, block, 0, s, eo, H, k, send_pos, gate, shared,
+      hipLaunchKernelGGL((combine_dropout_kernel<8, A, B>), grid, block, 0, s, eo, rows, H, k, send_pos, gate, shared,
                          residual, d, y, spans);
   });
   return hipGetLastError();
 }
 
-hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int N, int H, int k,
+hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int rows, int N, int H, int k,
                                            const int32_t* send_pos, const float* gate, const void* eo, double p,
                                            const uint64_t* rng, void* d_eo, float* d_gate, void* d_shared,
                                            hipStream_t s) {
@@ -233,7 +236,7 @@ hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32
     constexpr bool A = decltype(a)::value, B = decltype(b)::value;
     auto go = [&](auto kmax, auto stream) {
       hipLaunchKernelGGL((combine_dropout_backward_kernel<decltype(kmax)::value, A, B, decltype(stream)::value>), grid,
-                         block, 0, s, dy, H, k, send_pos, gate, eo, d, d_eo, d_gate, d_shared);
+                         block, 0, s, dy, rows, H, k, send_pos, gate, eo, d, d_eo, d_gate, d_shared);
     };
     auto size = [&](auto stream) {
       if (k <= 2) go(std::integral_constant<int, 2>{}, stream);

@@ -707,33 +707,34 @@ moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype d
                                              db_dt == MOE_F32, h, ws, stream));
 }
 
-moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, int H, int k, const int32_t* send_pos,
-                               const float* topk_gate, const void* shared_out, const void* residual, double p,
+moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows, int N, int H, int k,
+                               const int32_t* send_pos, const float* topk_gate, const void* shared_out, const void* residual, double p,
                                const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream) {
-  if (N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
   if (!act_type(eo_dt) || !act_type(y_dt)) return MOE_ERR_UNSUPPORTED;
   if (k > MOE_MAX_TOPK || N >= kMaxRowsPerLaunch || H % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
   if (N == 0) return MOE_OK;
-  if (expert_out == nullptr || send_pos == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(expert_out) || !aligned16(y) || !fits16(shared_out) || !fits16(residual)) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_combine_dropout(expert_out, eo_dt == MOE_F32, N, H, k, send_pos, topk_gate, shared_out,
+  if ((rows > 0 && expert_out == nullptr) || send_pos == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+  if (!fits16(expert_out) || !aligned16(y) || !fits16(shared_out) || !fits16(residual)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine_dropout(expert_out, eo_dt == MOE_F32, rows, N, H, k, send_pos, topk_gate, shared_out,
                                                 residual, p, rng, y, y_dt == MOE_F32, stream));
 }
 
-moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int N, int H, int k,
+moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int rows, int N, int H, int k,
                                         const int32_t* send_pos, const float* topk_gate, const void* expert_out,
                                         double p, const uint64_t* rng, void* d_expert_out, float* d_gate,
                                         void* d_shared, hipStream_t stream) {
-  if (N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
   if (!act_type(dt) || (dy_dt != MOE_F32 && dy_dt != dt)) return MOE_ERR_UNSUPPORTED;
   if (k > MOE_MAX_TOPK || N >= kMaxRowsPerLaunch || H % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (static_cast<long long>(N) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
   if (N == 0) return MOE_OK;
-  if (dy == nullptr || send_pos == nullptr || d_expert_out == nullptr || (expert_out == nullptr && d_gate != nullptr))
+  if (dy == nullptr || send_pos == nullptr ||
+      (rows > 0 && (d_expert_out == nullptr || (expert_out == nullptr && d_gate != nullptr))))
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(dy) || !aligned16(d_expert_out) || !fits16(expert_out) || !fits16(d_shared)) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_combine_dropout_backward(dy, dy_dt == MOE_F32, dt == MOE_F32, N, H, k, send_pos,
+  if (!aligned16(dy) || !fits16(d_expert_out) || !fits16(expert_out) || !fits16(d_shared)) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_combine_dropout_backward(dy, dy_dt == MOE_F32, dt == MOE_F32, rows, N, H, k, send_pos,
                                                          topk_gate, expert_out, p, rng, d_expert_out, d_gate, d_shared,
                                                          stream));
 }

@@ -97,10 +97,10 @@ hipError_t launch_act_backward(const void* z, const void* d_out, bool f32, const
                                hipStream_t s);
 
 // dropout (dropout.hip); gate, shared, residual, d_gate (and then eo) and d_shared may be null
-hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int N, int H, int k, const int32_t* send_pos,
+hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int rows, int N, int H, int k, const int32_t* send_pos,
                                   const float* gate, const void* shared, const void* residual, double p,
                                   const uint64_t* rng, void* y, bool y_f32, hipStream_t s);
-hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int N, int H, int k,
+hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32, int rows, int N, int H, int k,
                                            const int32_t* send_pos, const float* gate, const void* eo, double p,
                                            const uint64_t* rng, void* d_eo, float* d_gate, void* d_shared,
                                            hipStream_t s);

@@ -707,7 +707,7 @@ moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scal
  *   w         [E, Nw, K] of dt, Nw = N (gated: 2N, the activated half first).
  *   bias      [E, Nw] of bias_dt (MOE_F32, or dt), or NULL.
  *   residual  [rows, N] of dt, or NULL; added after the activation.
- *   out       [rows, N] of dt; may be residual.
+ *   out       [rows, N] of dt; may be residual.  Otherwise out and z overlap no other argument.
  *   z         [rows, Nw] of dt: the pre-activations for moe_expert_act_backward, or NULL.
  *   ws        workspace of moe_workspace_bytes(MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt) bytes
  *             (may be 0: then ws may be NULL).
@@ -755,7 +755,8 @@ moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype d
  * by 65536 / (65536 - c); the others become 0, whatever they held.  The numbers are 16 bits: element i takes half
  * i % 8 (low halves first) of the four words of Philox 4x32-10 with counter (i / 8, offset) and key
  * seed, each as two 32-bit words, low first.  So the mask depends on rng and the place alone.
- *   expert_out ... shared_out  as for moe_combine (topk_gate NULL: weight 1).
+ *   expert_out ... shared_out  as for moe_combine (topk_gate NULL: weight 1); slots whose send_pos lies
+ *              outside [0, rows) are skipped.
  *   residual   [N, H] of y_dt, or NULL.
  *   p          dropout probability in [0, 1]; 1 drops everything.
  *   rng        device [2] uint64: seed, offset, read when the work runs.  The caller gives every
@@ -764,8 +765,8 @@ moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype d
  * The sum is fp32 in slot order, then the shared row, dropout, the residual; one rounding.  Requires what
  * moe_combine does, residual included; rng 8-byte aligned.
  */
-moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, int H, int k, const int32_t* send_pos,
-                               const float* topk_gate, const void* shared_out, const void* residual, double p,
+moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows, int N, int H, int k,
+                               const int32_t* send_pos, const float* topk_gate, const void* shared_out, const void* residual, double p,
                                const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream);
 
 /*
@@ -776,6 +777,7 @@ moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, i
  *     d_expert_out[send_pos[s]] = g_s d_t,   d_gate[s] = <d_t, expert_out[send_pos[s]]>,   d_shared_t = d_t
  *
  *   dy         [N, H] of dy_dt (MOE_F32, or dt).
+ *   send_pos   as for moe_combine_dropout; no row is named twice.
  *   expert_out, d_expert_out  [rows, H] of dt (MOE_F32 or MOE_BF16); rows that no slot names are left
  *              as they are.  expert_out may be NULL when d_gate is.
  *   topk_gate  [N, k] fp32, or NULL (1).
@@ -783,7 +785,7 @@ moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int N, i
  *   d_shared   [N, H] of dt out, or NULL.
  * Dot products are fp32 in a fixed order.  Requires H % 8 == 0; 16-byte aligned arrays.
  */
-moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int N, int H, int k,
+moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int rows, int N, int H, int k,
                                         const int32_t* send_pos, const float* topk_gate, const void* expert_out,
                                         double p, const uint64_t* rng, void* d_expert_out, float* d_gate,
                                         void* d_shared, hipStream_t stream);

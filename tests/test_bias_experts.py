@@ -212,14 +212,14 @@ def test_act_backward_workspace():
 
 
 def _cd(**kw):
-    v = dict(eo=FAKE, eo_dt=MOE_BF16, N=16, H=64, k=2, pos=FAKE, gate=FAKE, sh=FAKE, res=FAKE, p=0.1, rng=FAKE, y=FAKE,
+    v = dict(eo=FAKE, eo_dt=MOE_BF16, rows=32, N=16, H=64, k=2, pos=FAKE, gate=FAKE, sh=FAKE, res=FAKE, p=0.1, rng=FAKE, y=FAKE,
              y_dt=MOE_F32)
     v.update(kw)
     return moe.lib().moe_combine_dropout(*v.values(), None)
 
 
 def _cdb(**kw):
-    v = dict(dy=FAKE, dy_dt=MOE_F32, dt=MOE_BF16, N=16, H=64, k=2, pos=FAKE, gate=FAKE, eo=FAKE, p=0.1, rng=FAKE,
+    v = dict(dy=FAKE, dy_dt=MOE_F32, dt=MOE_BF16, rows=32, N=16, H=64, k=2, pos=FAKE, gate=FAKE, eo=FAKE, p=0.1, rng=FAKE,
              d_eo=FAKE, dg=FAKE, dsh=FAKE)
     v.update(kw)
     return moe.lib().moe_combine_dropout_backward(*v.values(), None)
@@ -228,7 +228,7 @@ def _cdb(**kw):
 @pytest.mark.parametrize("f", [_cd, _cdb])
 def test_combine_dropout_refusals(f):
     inv, un = MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED
-    for bad in (dict(N=-1), dict(H=0), dict(k=0), dict(p=-0.1), dict(p=1.001), dict(p=float("nan")), dict(rng=None),
+    for bad in (dict(rows=-1), dict(N=-1), dict(H=0), dict(k=0), dict(p=-0.1), dict(p=1.001), dict(p=float("nan")), dict(rng=None),
                 dict(rng=FAKE + 4), dict(pos=None)):
         assert f(**bad) == inv, bad
     for bad in (dict(k=33), dict(H=60), dict(N=1 << 24)):

@@ -129,6 +129,26 @@ def test_dropout_rows(n, dt, ydt):
         assert np.all(np.abs(f64(z) - tot) <= e + _half(ydt, np.abs(tot) + e))
 
 
+def test_slots_without_a_row():
+    """Slots whose row lies outside the expert outputs are skipped, in either direction; with no rows at all y is the
+    residual alone."""
+    N, k, H = 40, 3, 72
+    eo, g, res, dy = (_t(s, i, BF).to(DEV) for i, s in enumerate(((N * k, H), (N, k), (N, H), (N, H))))
+    g = g.float()
+    pos = torch.arange(N * k, dtype=torch.int32, device=DEV)
+    bad = pos.clone()
+    bad[::7], bad[3::7], bad[5::7] = N * k, 2 ** 31 - 1, -2 ** 31
+    none = torch.where(bad == pos, pos, torch.full_like(pos, -1))
+    rng = _state(2, 3)
+    a, b = (moe.moe_combine_dropout(eo, q, g, 0.2, rng, residual=res) for q in (bad, none))
+    ga, gb = (moe.moe_combine_dropout_backward(dy, q, g, eo, 0.2, rng, d_expert_out=torch.zeros_like(eo)) for q in (bad, none))
+    alone = moe.moe_combine_dropout(eo[:0], torch.full_like(pos, -1), g, 0.2, rng, residual=res)
+    _, dg, dsh = moe.moe_combine_dropout_backward(dy, pos, g, eo[:0], 0.2, rng, want_shared=True)
+    sync()
+    assert torch.equal(a, b) and torch.equal(ga[0], gb[0]) and torch.equal(ga[1], gb[1]) and torch.equal(alone, res)
+    assert not dg.any() and torch.equal(dsh, moe.moe_dropout(dy, 0.2, rng))
+
+
 def test_dropped_infinities_and_nan_are_gone():
     x = torch.full((4096,), float("inf"), device=DEV)
     x[::2] = float("nan")
