@@ -575,13 +575,11 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs p) {
 
 // ------------------------------------------------------------------------------------
 // Few rows an expert (serving: single tokens and small batches): bound by the weights' bytes.  A
-// workgroup takes 32 weight rows (gated: 16 of either half) and the rows of one expert, up to 32 at a
-// time; its 4 waves split K in contiguous parts.  Each wave streams its part through a ring of stages of its
+// workgroup takes 32 weight rows (gated: 16 of either half) or half as many, and the rows of one expert, up
+// to 32 at a time; its waves split K in contiguous parts.  Each wave streams its part through a ring of stages of its
 // own in LDS (128 bytes of the weight rows and of the rows of a), without meeting the others until the
-// end, when the four sums are added in order.
+// end, when their sums are added in order.
 // ------------------------------------------------------------------------------------
-
-constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves, kFewRows = 32;
 
 template <bool F32>
 __device__ __forceinline__ f32x4_t few_mma(uint4 a, uint4 b, f32x4_t c) {
@@ -596,20 +594,28 @@ __device__ __forceinline__ f32x4_t few_mma(uint4 a, uint4 b, f32x4_t c) {
   }
 }
 
-constexpr int kFewStage = (kFewRows + 32) * 128;   // bytes of a stage with 32 rows of a
-template <int MB>
-constexpr int kFewRing = MB == 1 ? 3 : 2;          // stages of a wave's ring (16 rows of a: 18 KB, 32: 16 KB)
-constexpr int kFewLds = kFewWaves * 3 * (kFewRows + 16) * 128;   // (two workgroups fit a CU)
-static_assert(kFewRing<2> * kFewStage * kFewWaves <= kFewLds, "the rings share the LDS");
+// Weight rows and waves of a workgroup: 32 and 4 (two workgroups a CU), or, where those would leave CUs
+// idle, 16 and 8 (one).  RING: stages of a wave's ring with 16 MB rows of a.
+template <int WB>
+struct Few {
+  static constexpr int kRows = 16 * WB, kWaves = WB == 2 ? 4 : 8, kThreads = 64 * kWaves;
+  static constexpr int kLds = WB == 2 ? 72 * 1024 : 144 * 1024;
+  template <int MB>
+  static constexpr int kStage = (kRows + 16 * MB) * kLinRow;
+  template <int MB>
+  static constexpr int kRing = WB == 2 ? (MB == 1 ? 3 : 2) : (MB == 1 ? 4 : 3);
+  static_assert(kRing<1> * kStage<1> * kWaves <= kLds && kRing<2> * kStage<2> * kWaves <= kLds, "the rings' LDS");
+};
 
 // rows [m0, m0 + 16 MB) of expert e against the workgroup's weight rows
-template <bool F32, bool GATED, int MB>
+template <bool F32, bool GATED, int MB, int WB>
 __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int mend, int c0, uint8_t* lds) {
-  constexpr int kCols = GATED ? 16 : 32, S = kFewRing<MB>, kLd = 4 + 2 * MB;
-  constexpr int kStage = (kFewRows + 16 * MB) * 128;
+  using F = Few<WB>;
+  constexpr int kCols = GATED ? 8 * WB : 16 * WB, S = F::template kRing<MB>, kLdW = 2 * WB, kLd = kLdW + 2 * MB;
+  constexpr int kStage = F::template kStage<MB>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  uint8_t* const mine = lds + wave * (kFewLds / kFewWaves);
+  uint8_t* const mine = lds + wave * (F::kLds / F::kWaves);
   const uint32_t at0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)mine));
   const uint32_t rb = static_cast<uint32_t>(p.K) * (F32 ? 4 : 2);
   const int Nw = GATED ? 2 * p.N : p.N;
@@ -621,7 +627,7 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
   const uint8_t* a_base = p.a_rows != nullptr ? p.a : p.a + static_cast<size_t>(m0) * rb;
   const uint32_t a_size = static_cast<uint32_t>(p.a_rows != nullptr ? p.a_nrows : mrows) * rb;
   // a load fills 8 rows: lane l slot l % 8 of row l / 8
-  uint32_t vw[4], va[2 * MB], ch[2];   // (ch: the chunk's first byte, rows of even and odd groups)
+  uint32_t vw[kLdW], va[2 * MB], ch[2];   // (ch: the chunk's first byte, rows of even and odd groups)
 #pragma unroll
   for (int j = 0; j < 2; ++j) ch[j] = ((lane & 7) ^ lin_key(j * 8 + (lane >> 3))) * 16;
 #pragma unroll
@@ -638,8 +644,8 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
     }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = j * 8 + (lane >> 3), c = GATED ? r % 16 : r;
+  for (int j = 0; j < kLdW; ++j) {
+    const int r = j * 8 + (lane >> 3), c = GATED ? r % kCols : r;
     vw[j] = c < ncols ? static_cast<uint32_t>(c) * rb + ch[j & 1] : kOutside;
   }
   auto load = [&](int ks, int slot) __attribute__((always_inline)) {
@@ -650,17 +656,17 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
     const uint32_t at = at0 + slot * kStage;
     const bool in[2] = {left >= 128 || ch[0] < left, left >= 128 || ch[1] < left};   // (past K: zeros)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dma16_window(GATED && j >= 2 ? rw2 : rw, in[j & 1] ? vw[j] : kOutside, at + j * 1024);
+    for (int j = 0; j < kLdW; ++j) dma16_window(GATED && j >= WB ? rw2 : rw, in[j & 1] ? vw[j] : kOutside, at + j * 1024);
 #pragma unroll
-    for (int j = 0; j < 2 * MB; ++j) dma16_window(ra, in[j & 1] ? va[j] : kOutside, at + (4 + j) * 1024);
+    for (int j = 0; j < 2 * MB; ++j) dma16_window(ra, in[j & 1] ? va[j] : kOutside, at + (kLdW + j) * 1024);
   };
   const int nkt = (rb + 127) / 128;
-  const int s0 = nkt * wave / kFewWaves, nk = nkt * (wave + 1) / kFewWaves - s0;
-  f32x4_t acc[MB][2];
+  const int s0 = nkt * wave / F::kWaves, nk = nkt * (wave + 1) / F::kWaves - s0;
+  f32x4_t acc[MB][WB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) acc[m][c] = f32x4_t{};
+    for (int c = 0; c < WB; ++c) acc[m][c] = f32x4_t{};
   uint32_t fb[2];   // fragment of k-step s: row l % 16, chunk 4 s + l / 16
 #pragma unroll
   for (int s = 0; s < 2; ++s) fb[s] = (lane & 15) * 128 + ((4 * s + (lane >> 4)) ^ lin_key(lane & 15)) * 16;
@@ -676,15 +682,15 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
     const uint8_t* st = mine + slot * kStage;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      uint4 fw[2], fa[MB];
+      uint4 fw[WB], fa[MB];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) fw[c] = *reinterpret_cast<const uint4*>(st + c * 16 * 128 + fb[s]);
+      for (int c = 0; c < WB; ++c) fw[c] = *reinterpret_cast<const uint4*>(st + c * 16 * 128 + fb[s]);
 #pragma unroll
-      for (int m = 0; m < MB; ++m) fa[m] = *reinterpret_cast<const uint4*>(st + (kFewRows + m * 16) * 128 + fb[s]);
+      for (int m = 0; m < MB; ++m) fa[m] = *reinterpret_cast<const uint4*>(st + (F::kRows + m * 16) * 128 + fb[s]);
 #pragma unroll
       for (int m = 0; m < MB; ++m)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) acc[m][c] = few_mma<F32>(fw[c], fa[m], acc[m][c]);
+        for (int c = 0; c < WB; ++c) acc[m][c] = few_mma<F32>(fw[c], fa[m], acc[m][c]);
     }
     wait_lgkmcnt_all();
     __asm__ volatile("" ::: "memory");
@@ -696,11 +702,11 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      *reinterpret_cast<f32x4_t*>(red + ((wave * MB + m) * 16 + (lane & 15)) * 32 + c * 16 + 4 * (lane >> 4)) = acc[m][c];
+    for (int c = 0; c < WB; ++c)
+      *reinterpret_cast<f32x4_t*>(red + ((wave * MB + m) * 16 + (lane & 15)) * F::kRows + c * 16 + 4 * (lane >> 4)) = acc[m][c];
   __syncthreads();
   constexpr int kGroups = kCols / 8;   // 8 columns of a row a lane
-  for (int i = threadIdx.x; i < MB * 16 * kGroups; i += kFewThreads) {
+  for (int i = threadIdx.x; i < MB * 16 * kGroups; i += F::kThreads) {
     const int r = i / kGroups, col = (i % kGroups) * 8;
     if (r >= mrows || col >= ncols) continue;
     float v[8], w[8];
@@ -708,8 +714,8 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
     for (int c = 0; c < (GATED ? 2 : 1); ++c) {
       float t[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-      for (int q = 0; q < kFewWaves; ++q) {
-        const float4* x = reinterpret_cast<const float4*>(red + (q * MB * 16 + r) * 32 + c * 16 + col);
+      for (int q = 0; q < F::kWaves; ++q) {
+        const float4* x = reinterpret_cast<const float4*>(red + (q * MB * 16 + r) * F::kRows + c * kCols + col);
         const float4 a = x[0], b = x[1];
         t[0] += a.x; t[1] += a.y; t[2] += a.z; t[3] += a.w;
         t[4] += b.x; t[5] += b.y; t[6] += b.z; t[7] += b.w;
@@ -722,10 +728,10 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
   __syncthreads();   // (the sums have been read before the next rows' stages land)
 }
 
-// workgroup x: 32 weight rows; y: an expert (slots < E: the y-th expert that has rows)
-template <bool F32, bool GATED>
-__global__ __launch_bounds__(kFewThreads) void linear_few_kernel(LinearArgs p, int slots) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kFewLds];
+// workgroup x: 16 WB weight rows; y: an expert (slots < E: the y-th expert that has rows)
+template <bool F32, bool GATED, int WB>
+__global__ __launch_bounds__(Few<WB>::kThreads) void linear_few_kernel(LinearArgs p, int slots) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Few<WB>::kLds];
   const int lane = threadIdx.x & 63;
   int e = blockIdx.y;
   if (slots < p.E) {
@@ -747,19 +753,28 @@ __global__ __launch_bounds__(kFewThreads) void linear_few_kernel(LinearArgs p, i
   }
   int lo, hi;
   lin_segment(p, e, lo, hi);
-  const int c0 = blockIdx.x * (GATED ? 16 : 32);
+  const int c0 = blockIdx.x * (GATED ? 8 * WB : 16 * WB);
   for (int m0 = lo; m0 < hi; m0 += 32) {
-    if (hi - m0 <= 16) few_rows<F32, GATED, 1>(p, e, m0, hi, c0, lds);
-    else few_rows<F32, GATED, 2>(p, e, m0, hi, c0, lds);
+    if (hi - m0 <= 16) few_rows<F32, GATED, 1, WB>(p, e, m0, hi, c0, lds);
+    else few_rows<F32, GATED, 2, WB>(p, e, m0, hi, c0, lds);
   }
+}
+
+template <bool F32, bool GATED, int WB>
+void launch_few(const LinearArgs& p, int slots, hipStream_t s) {
+  constexpr int kCols = GATED ? 8 * WB : 16 * WB;
+  hipLaunchKernelGGL((linear_few_kernel<F32, GATED, WB>), dim3((p.N + kCols - 1) / kCols, slots),
+                     dim3(Few<WB>::kThreads), 0, s, p, slots);
 }
 
 template <bool F32, bool GATED>
 void launch_few(const LinearArgs& p, hipStream_t s) {
   const int slots = p.E < p.rows ? p.E : p.rows;
-  constexpr int kCols = GATED ? 16 : 32;
-  hipLaunchKernelGGL((linear_few_kernel<F32, GATED>), dim3((p.N + kCols - 1) / kCols, slots), dim3(kFewThreads), 0, s, p,
-                     slots);
+  const long long groups = (static_cast<long long>(GATED ? 2 * p.N : p.N) + 31) / 32 * slots;
+  // half as many weight rows where 256 CUs then get a workgroup each (one row, N 4096, K 14336: 28 -> 22 us,
+  // fp32 K 4096 17 -> 13; with twice the rows, N 8192, K 4096, they took 14 against 13)
+  if (groups <= 128) launch_few<F32, GATED, 1>(p, slots, s);
+  else launch_few<F32, GATED, 2>(p, slots, s);
 }
 
 template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
@@ -819,8 +834,11 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
   LinPlan best{LIN_64, 1, 0};
   double best_us = 1e30;
   if (each <= 32) {
-    const double more = each > 16 ? 1.3 : E > 1 && each > 8 ? 1.05 : 1.0;   // (some experts' weights twice)
-    const double waves = ceil_div(hit * ceil_div(Nw, 32), 512) * stages / 4 * 0.3 * more * (f32 ? 1.5 : 1.0);
+    const long long groups = hit * ceil_div(Nw, 32);
+    const double more = each > 16 ? (E == 1 && groups <= 128 ? 1.1 : 1.3)
+                                  : E > 1 && each > 8 ? 1.05 : 1.0;   // (some experts' weights twice)
+    const double waves = (groups <= 128 ? 0.5 : static_cast<double>(ceil_div(groups, 512))) * stages / 4 * 0.3 * more *
+                         (f32 ? 1.5 : 1.0);
     best = LinPlan{LIN_FEW, 1, 0};
     best_us = 4 + (mem * more > waves ? mem * more : waves);
   }
