@@ -808,7 +808,7 @@ namespace {
 // same sizes; bf16, one expert, N 4096 (us; the smallest of each column is what the estimate takes, or
 // within 3% of it):
 //     K, rows           4096: 1   16   64  512 1024 2048    14336: 64  512 1024 2048 4096
-//     few rows              10   10   23  162  320  637            85  605 1200 2390 4770
+//     few rows               9   10   16  100  194  385            54  336  659 1309 2592
 //     64 x 64               22   22   23   33   58  111            90  129  243  449  851
 //       K in 4 parts        13   14   15   47   85  176            35  139  253  456  822
 //     128 x 256             37   37   43   54   56   69           179  192  190  219  438
@@ -816,7 +816,9 @@ namespace {
 //       K in 4 parts        17   17   20   35   68  121            58   74  140  272  435
 //     320 x 256             69   69   72   94   94  110           297  343  333  347  401
 //       K in 4 parts        25   25   27   43   56  109            85  108  125  256  404
-// fp32, N 4096, K 4096: 2000 rows 64 x 64 594, 128 x 128 495; 200 rows 82 (4 parts 80), 256 (4 parts 80).
+// (K 14336, 2048 rows: 320 x 256 with 256-row tiles in 2 parts, 214 where 128 x 256 takes 212 in the same
+// process.)  fp32, N 4096, K 4096: 2000 rows 64 x 64 594, 128 x 128 495, few rows 852; 200 rows 82 (4 parts
+// 80), 256 (4 parts 80), 96.
 enum { LIN_FEW, LIN_64, LIN_128, LIN_320 };
 struct LinPlan {
   int kind, split, tile_rows;
