@@ -1029,8 +1029,8 @@ def moe_combine_dropout(expert_out: torch.Tensor, send_pos: torch.Tensor, topk_g
     else:
         _expect("y", y, (N, H), _ACT, dev)
     _expect("residual", residual, (N, H), (y.dtype,), dev)
-    _run("moe_combine_dropout", dev, _ptr(expert_out), _dt(expert_out), expert_out.shape[0], N, H, k, _ptr(send_pos), _ptr(topk_gate),
-         _ptr(shared_out), _ptr(residual), p, _ptr(rng), _ptr(y), _dt(y), _stream(expert_out))
+    _run("moe_combine_dropout", dev, _ptr(expert_out), _dt(expert_out), expert_out.shape[0], N, H, k, _ptr(send_pos),
+         _ptr(topk_gate), _ptr(shared_out), _ptr(residual), p, _ptr(rng), _ptr(y), _dt(y), _stream(expert_out))
     return y
 
 

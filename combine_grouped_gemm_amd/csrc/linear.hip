@@ -9,8 +9,8 @@
 //
 // A workgroup computes TM rows x TN weight rows (gated: TN / 2 rows of either half, so that a lane holds
 // both factors); an expert's rows are split evenly into as few tiles as hold them, and a wave skips the
-// products of 32-row blocks without rows.  K advances in stages of 128 bytes a row (64 bf16, 32 fp32), loaded straight to LDS
-// through buffer windows: rows past the segment, weight rows past the matrix and columns past K read as
+// products of 32-row blocks without rows.  K advances in stages of 128 bytes a row (64 bf16, 32 fp32),
+// loaded straight to LDS through buffer windows: rows past the segment, weight rows past the matrix and columns past K read as
 // zeros, so no size needs a kernel of its own.  Chunk c of 16 bytes of row r lies in slot c ^ key(r), so
 // that a load (8 rows) and a fragment read (32 rows, two chunks) touch every bank once.  A fragment is one
 // chunk a lane for either type: 8 bf16 for one 32x32x16 product, 4 fp32 for four 32x32x2 ones (both
@@ -703,7 +703,8 @@ __device__ __forceinline__ void few_rows(const LinearArgs& p, int e, int m0, int
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int c = 0; c < WB; ++c)
-      *reinterpret_cast<f32x4_t*>(red + ((wave * MB + m) * 16 + (lane & 15)) * F::kRows + c * 16 + 4 * (lane >> 4)) = acc[m][c];
+      *reinterpret_cast<f32x4_t*>(red + ((wave * MB + m) * 16 + (lane & 15)) * F::kRows + c * 16 + 4 * (lane >> 4)) =
+          acc[m][c];
   __syncthreads();
   constexpr int kGroups = kCols / 8;   // 8 columns of a row a lane
   for (int i = threadIdx.x; i < MB * 16 * kGroups; i += F::kThreads) {
@@ -860,9 +861,8 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
     const double l2 = even * nN * (s.tm + s.tn) * row / 1.7e7;   // what the tiles load, at 17 TB/s
     for (int split = 1; split <= 16 && split * 8 <= (stages > 8 ? stages : 8); split *= 2) {
       const double turns = even * nN * split / (256.0 * s.per_cu);
-      const double rounds = turns <= 1               ? 1.0
-                            : E == 1 || turns < 4.0 ? static_cast<double>(static_cast<long long>(turns + (E == 1 ? 0.999 : 0.94)))
-                                                     : turns + 0.15;   // (the tiles of uneven experts are an estimate)
+      const double whole = static_cast<double>(static_cast<long long>(turns + (E == 1 ? 0.999 : 0.94)));
+      const double rounds = turns <= 1 ? 1.0 : E == 1 || turns < 4.0 ? whole : turns + 0.15;   // (uneven experts: an estimate)
       // one expert on 320-row tiles: as many as the rounds have room for, so shorter ones (4096 x 14336 x
       // 4096: 256 tiles of 256 rows 375 us, 208 of 320 389; where the rounds are full 320 rows win: N 14336
       // of K 4096, 728 tiles 370 us, 896 of 256 rows 419)

@@ -708,8 +708,8 @@ moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype d
 }
 
 moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows, int N, int H, int k,
-                               const int32_t* send_pos, const float* topk_gate, const void* shared_out, const void* residual, double p,
-                               const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream) {
+                               const int32_t* send_pos, const float* topk_gate, const void* shared_out,
+                               const void* residual, double p, const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream) {
   if (rows < 0 || N < 0 || H <= 0 || k < 1 || !drop_ok(p, rng)) return MOE_ERR_INVALID_ARG;
   if (!act_type(eo_dt) || !act_type(y_dt)) return MOE_ERR_UNSUPPORTED;
   if (k > MOE_MAX_TOPK || N >= kMaxRowsPerLaunch || H % 8 != 0) return MOE_ERR_UNSUPPORTED;
@@ -717,8 +717,8 @@ moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows
   if (N == 0) return MOE_OK;
   if ((rows > 0 && expert_out == nullptr) || send_pos == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
   if (!fits16(expert_out) || !aligned16(y) || !fits16(shared_out) || !fits16(residual)) return MOE_ERR_INVALID_ARG;
-  return hip_status(moe::launch_combine_dropout(expert_out, eo_dt == MOE_F32, rows, N, H, k, send_pos, topk_gate, shared_out,
-                                                residual, p, rng, y, y_dt == MOE_F32, stream));
+  return hip_status(moe::launch_combine_dropout(expert_out, eo_dt == MOE_F32, rows, N, H, k, send_pos, topk_gate,
+                                                shared_out, residual, p, rng, y, y_dt == MOE_F32, stream));
 }
 
 moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int rows, int N, int H, int k,

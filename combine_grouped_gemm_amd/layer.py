@@ -24,14 +24,15 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_SILU, MOE_BF16, MOE_BF16X3, MOE_F32, MOE_FP8_E4M3, MOE_MX_BLOCK, MOE_OP_ACT_BACKWARD, MOE_OP_BALANCE_LOSS,
-               MOE_OP_DISPATCH_LAYOUT, MOE_OP_EXPERT_DGRAD, MOE_OP_EXPERT_GEMM, MOE_OP_EXPERT_LINEAR, MOE_OP_GROUPED_FFN,
-               MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD, moe_balance_loss, moe_balance_loss_backward, moe_combine,
-               moe_combine_backward, moe_combine_dropout, moe_combine_dropout_backward, moe_dequantize_fp8,
-               moe_dequantize_mxfp8, moe_dispatch_layout, moe_dropout, moe_expert_act_backward, moe_expert_linear, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
+from . import (MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_SILU, MOE_BF16, MOE_BF16X3, MOE_F32, MOE_FP8_E4M3,
+               MOE_MX_BLOCK, MOE_OP_ACT_BACKWARD, MOE_OP_BALANCE_LOSS, MOE_OP_DISPATCH_LAYOUT, MOE_OP_EXPERT_DGRAD,
+               MOE_OP_EXPERT_GEMM, MOE_OP_EXPERT_LINEAR, MOE_OP_GROUPED_FFN, MOE_OP_ROUTER, MOE_OP_ROUTER_WGRAD,
+               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_backward, moe_combine_dropout,
+               moe_combine_dropout_backward, moe_dequantize_fp8, moe_dequantize_mxfp8, moe_dispatch_layout,
+               moe_dropout, moe_expert_act_backward, moe_expert_dgrad, moe_expert_down, moe_expert_down_shared,
                moe_expert_down_shared_e4m3, moe_expert_gate_up, moe_expert_gate_up_gathered,
-               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3,
-               moe_expert_gate_up_mxfp8, moe_expert_gate_up_preact, moe_expert_wgrad, moe_grouped_ffn, moe_permute,
+               moe_expert_gate_up_gathered_shared, moe_expert_gate_up_gathered_shared_e4m3, moe_expert_gate_up_mxfp8,
+               moe_expert_gate_up_preact, moe_expert_linear, moe_expert_wgrad, moe_grouped_ffn, moe_permute,
                moe_quantize_fp8, moe_quantize_mxfp8, moe_route, moe_router_backward, moe_router_dense_dgrad,
                moe_router_dense_wgrad, moe_router_input_grad, moe_router_logits, moe_swiglu_backward,
                moe_swiglu_backward_mxfp8, moe_workspace_bytes, _balance_args, _expect)

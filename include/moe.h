@@ -766,8 +766,8 @@ moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype d
  * moe_combine does, residual included; rng 8-byte aligned.
  */
 moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows, int N, int H, int k,
-                               const int32_t* send_pos, const float* topk_gate, const void* shared_out, const void* residual, double p,
-                               const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream);
+                               const int32_t* send_pos, const float* topk_gate, const void* shared_out,
+                               const void* residual, double p, const uint64_t* rng, void* y, moe_dtype y_dt, hipStream_t stream);
 
 /*
  * moe_combine_dropout_backward -- the gradients of moe_combine_dropout (residual's is dy).

@@ -158,6 +158,25 @@ def test_every_kernel(rows, E, K, Nw, k, dt, gated):
     _run_linear(rows, E, K, Nw // 2 if gated else Nw, dt, "gelu" if gated else "silu", gated, "f32", True, k, seed=rows)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("rows,E,K,Nw,k,dt", [
+    # 16 weight rows by eight waves (up to 128 groups of 32 weight rows): up to 16 and up to 32 rows of a at a time
+    (16, 1, 8200, 2064, 0, BF), (31, 1, 8200, 2064, 2, BF), (57, 5, 1032, 400, 0, BF), (29, 1, 2056, 2064, 0, F32),
+    # 32 by four
+    (1, 1, 14336, 4112, 0, BF), (32, 1, 4096, 4112, 3, BF), (57, 5, 1032, 1040, 0, BF), (3, 9, 4104, 2064, 2, BF),
+    (1, 1, 4096, 4112, 0, F32), (45, 3, 2056, 4112, 2, F32)])
+def test_few_rows(rows, E, K, Nw, k, dt, gated):
+    """Few rows an expert: either shape of the kernel that streams the weights, K that ends inside a stage."""
+    _run_linear(rows, E, K, Nw // 2 if gated else Nw, dt, "gelu_tanh" if gated else "silu", gated, "f32", True, k, seed=rows)
+
+
+def test_few_rows_of_one_expert():
+    """All rows on one of many experts: 32 at a time, the last of them fewer."""
+    off = torch.tensor([0, 0, 0, 117, 117, 117, 117, 117, 117], dtype=torch.int32)
+    for dt in (BF, F32):
+        _run_linear(117, 8, 1032, 528, dt, "gelu", False, "f32", True, seed=117, offsets=off)
+
+
 def test_operands_past_32_bits():
     """Rows of a and of out whose byte offsets pass 2^32."""
     rows, n = 300000, 40

@@ -11,6 +11,7 @@ from oracle import moe_oracle as oracle
 from tests.gpu_util import f64, say, sync, token_rel_err, with_logits
 from tests.test_gpu_backward import GRAD_BAR, SMALL, mat_rel_err
 from tests.test_gpu_bias_experts import ACT
+from tests.test_gpu_layer import SMALL as FORWARD
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -226,3 +227,28 @@ def test_swiglu_layer_with_dropout_and_residual(name, save):
     plain_gr = plain.backward(None if save == "mxfp8" else x, dy, F32)
     sync()
     assert torch.equal(layer.y, y0) and all(torch.equal(again[n], plain_gr[n]) for n in ("dx", "dw13", "dw2", "dw_r"))
+
+
+@pytest.mark.parametrize("name,gate_in_down", [("tiny_f32", False), ("decode_fp8_small", False), ("dsv3_fp8_small", False),
+                                               ("dsv3_small", True)])
+def test_other_layers_with_dropout_and_residual(name, gate_in_down):
+    """fp32 and fp8 layers, and gates applied in the down projection: the same sum, dropped out onto the residual."""
+    cfg = FORWARD[name]
+    say(f"layer with dropout {name} gate_in_down={gate_in_down}")
+    inp = with_logits(w.make_layer_inputs(cfg, DEV))
+    layer = MoELayer(cfg.N, cfg.H, cfg.E, cfg.k, cfg.I, cfg.dtype, inp["w13"], inp["w2"], inp.get("sw13"), inp.get("sw2"),
+                     cfg.n_group, cfg.topk_group, inp["bias"], gate_in_down=gate_in_down)
+    y0 = layer.forward(inp["x"], inp["z"]).clone()
+    res = _t((cfg.N, cfg.H), 82, y0.dtype)
+    rng = torch.tensor([7, 3], dtype=torch.int64, device=DEV)
+    y = layer.forward(inp["x"], inp["z"], residual=res, dropout=0.5, rng=rng).clone()
+    sync()
+    gate = np.ones((cfg.N, cfg.k)) if layer.gate_in_down else f64(layer.topk_gate)
+    args = (f64(layer.expert_out), layer.layout[2].cpu().numpy(), gate, 0.5, 7, 3,
+            f64(layer.shared_out) if layer.shared else None, f64(res))
+    ref = oracle.combine_dropout(*args)
+    mag = oracle.combine_dropout(*[np.abs(v) if isinstance(v, np.ndarray) and v.dtype == np.float64 else v for v in args])
+    # y's rounding; at most k + 3 fp32 ones (k slots, the shared row, the scale, the residual less the last)
+    half = 2.0 ** -24 if y.dtype == F32 else 2.0 ** -8
+    assert np.all(np.abs(f64(y) - ref) <= half * np.abs(ref) + (cfg.k + 3) * 2.0 ** -23 * mag)
+    assert torch.equal(layer.forward(inp["x"], inp["z"]), y0)
