@@ -177,7 +177,7 @@ def test_linear_workspace():
 
 
 def _act(**kw):
-    v = dict(z=FAKE, d=FAKE, dt=MOE_BF16, off=FAKE, E=4, rows=128, N=64, act=moe.MOE_ACT_SILU, gated=0, dz=FAKE, db=FAKE,
+    v = dict(z=FAKE, d=FAKE, dt=MOE_BF16, off=FAKE, E=4, rows=1280, N=64, act=moe.MOE_ACT_SILU, gated=0, dz=FAKE, db=FAKE,
              db_dt=MOE_F32, h=FAKE, ws=FAKE, ws_bytes=1 << 40)
     v.update(kw)
     return moe.lib().moe_expert_act_backward(*v.values(), None)
@@ -205,7 +205,11 @@ def test_act_backward_workspace():
     for rows in (1, 31, 300, 65536, 2 ** 31 - 2 ** 16 - 1):
         for Nw in (8, 520, 4096, 1 << 24):
             need = moe.moe_workspace_bytes(moe.MOE_OP_ACT_BACKWARD, rows, 0, Nw, 16, 0, 0)
-            # a partial row is written for every expert and every range of at least 4 rows
+            # a partial row is written for every expert and every range of at least 4 rows, but for the few rows that
+            # one launch sums
+            if rows <= 300 and Nw <= 520:
+                assert need == 0
+                continue
             assert 17 * Nw * 4 <= need <= (rows // 4 + 17) * Nw * 4
             if Nw < 1 << 24 and Nw % 8 == 0:
                 assert _act(rows=rows, N=Nw, E=16, ws_bytes=need - 1) == MOE_ERR_WORKSPACE

@@ -286,7 +286,7 @@ def test_no_rows():
     assert dz.shape == (0, 64) and not db.any()
 
 
-@pytest.mark.parametrize("rows,K,N", [(4, 64, 72), (300, 136, 264)])
+@pytest.mark.parametrize("rows,K,N", [(4, 64, 72), (300, 136, 264), (700, 136, 264)])
 def test_other_stream_and_captured(rows, K, N):
     """On a second stream, and captured and replayed on new inputs with eager work between."""
     a, w, off = _t((rows, K), 1, BF).to(DEV), _t((2, N, K), 2, BF, 0.1).to(DEV), _offsets(rows, 2, 3).to(DEV)
@@ -380,7 +380,11 @@ def test_act_backward(act, gated, dt):
 
 @pytest.mark.parametrize("dt", [F32, BF])
 @pytest.mark.parametrize("rows,E,N", [(1, 1, 8), (1, 5, 1032), (3, 1, 520), (40, 40, 72), (257, 3, 136), (301, 1024, 16),
-                                      (2000, 6, 264), (5000, 1, 8), (4100, 2, 4104), (9000, 30, 512)])
+                                      (2000, 6, 264), (5000, 1, 8), (4100, 2, 4104), (9000, 30, 512),
+                                      # one launch: 129 and 512 rows of few experts, its largest row and most workgroups
+                                      (129, 2, 72), (512, 1, 2048), (512, 7, 40), (64, 1, 16392), (300, 19, 1032),
+                                      # two: one row, one expert, some columns more
+                                      (513, 7, 40), (300, 20, 1032), (512, 1, 4104)])
 def test_act_backward_sizes(rows, E, N, dt):
     _run_act(rows, E, N, dt, "silu", True, seed=rows)
     _run_act(rows, E, N, dt, "gelu_tanh", False, seed=rows, db_dtype=BF)
