@@ -1084,7 +1084,7 @@ def moe_dropout(x: torch.Tensor, p: float, rng: torch.Tensor, residual: Optional
     _act_dtype("x", x)
     _expect("rng", rng, (2,), _RNG, dev)
     if y is None:
-        y = torch.empty(x.shape, dtype=y_dtype or (x.dtype if residual is None else residual.dtype), device=dev)
+        y = torch.empty_like(x, dtype=y_dtype or (None if residual is None else residual.dtype))
     else:
         _expect("y", y, x.shape, _ACT, dev)
     _expect("residual", residual, x.shape, (y.dtype,), dev)
