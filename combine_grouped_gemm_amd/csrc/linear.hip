@@ -25,7 +25,11 @@
 // two stages, one workgroup a CU) reads 0.7 fragments a product and loads least: 256 x 256 took 1.13
 // times as long on 4096 x 14336 x 4096, 128 x 128 with two workgroups a CU 1.2 times; 128 x 256 (three
 // stages) for fewer rows; 64 x 64 (three stages, three workgroups a CU) where there are few tiles,
-// with K in parts when even those leave CUs idle.  Stages of 64 bytes took as long or longer.
+// with K in parts when even those leave CUs idle.  Stages of 64 bytes took as long or longer.  fp32: 128 x
+// 128 (four waves), and 32 x 64 whose wave pairs share a stage's k-steps: the fp32 products bound it, so
+// small tiles, dealt more evenly, win over fewer loads (64 x 64 against it: 999 rows of 6 experts, K 520,
+// N 1016 26.7 and 23.0 us; 500 x 1024 x 1024 24.3 and 17.6; 32 experts of 125 rows, gated, K 1024, N 512
+// 113 and 101; 512 x 4096 x 4096 145 and 153).
 #include <type_traits>
 #include <utility>
 
@@ -228,7 +232,7 @@ __device__ __forceinline__ int wave_prefix(int v) {   // sum over lanes up to th
   return v;
 }
 
-__device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t) {
+__device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, int unit, LinTile& t) {
   const int lane = threadIdx.x & 63;
   auto tiles_of = [&](int lo, int hi) { return (hi - lo + p.tile_rows - 1) / p.tile_rows; };
   int run = 1, run_sum = 0, run_end = 0, total = 0;
@@ -280,35 +284,36 @@ __device__ __forceinline__ bool lin_tile(const LinearArgs& p, int nN, LinTile& t
   const int gm = mt - grp * kGroup < kGroup ? mt - grp * kGroup : kGroup;
   const int mtile = grp * kGroup + in % gm;
   t.nblk = in / gm;
-  // (a multiple of the 64 rows that two row waves share: 288 rows take a wave's five blocks as 320 do; at
-  // most tile_rows, which 64 divides)
-  const int rpt = ((hi - lo + mt - 1) / mt + 63) / 64 * 64;
+  // (a multiple of the rows that the row waves share, 64 of two: 288 rows take a wave's five blocks as 320
+  // do; at most tile_rows, which unit divides)
+  const int rpt = ((hi - lo + mt - 1) / mt + unit - 1) / unit * unit;
   t.m0 = lo + mtile * rpt;
   t.mend = t.m0 + rpt < hi ? t.m0 + rpt : hi;
   return t.m0 < t.mend;
 }
 
-// WM x WN waves; a wave's block is (TM / WM) x (TN / WN) as 32 x 32 products
-template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p) {
-  constexpr int kWaves = WM * WN;
+// WM x WN waves; a wave's block is (TM / WM) x (TN / WN) as 32 x 32 products.  WK times as many waves: they
+// share a stage's four k-steps, and the first WM x WN add the others' sums in order.
+template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S, int WK>
+__global__ __launch_bounds__(64 * WM * WN * WK) void linear_tile_kernel(LinearArgs p) {
+  constexpr int kWaves = WM * WN * WK, kSteps = 4 / WK;   // k-steps of a wave and stage
   constexpr int MB = TM / WM / 32, NB = TN / WN / 32;
   constexpr int kLdA = TM / 8 / kWaves, kLdW = TN / 8 / kWaves;   // loads a wave and stage
   constexpr int kStage = (TM + TN) * kLinRow;
   constexpr int kEsz = F32 ? 4 : 2;
   static_assert(MB * WM * 32 == TM && NB * WN * 32 == TN && kLdA * kWaves * 8 == TM && kLdW * kWaves * 8 == TN, "tile");
   static_assert(!GATED || NB % 2 == 0, "a wave holds both factors");
-  static_assert(WM == 2 && TM % 64 == 0, "lin_tile deals rows to two row waves");
+  static_assert(WK == 1 || WK == 2, "k-steps are taken in pairs");
   __shared__ __attribute__((aligned(16))) uint8_t lds[S * kStage];
 
   constexpr int kCols = GATED ? TN / 2 : TN;   // output columns of a tile
   const int nN = (p.N + kCols - 1) / kCols;
   LinTile t;
-  if (!lin_tile(p, nN, t)) return;
+  if (!lin_tile(p, nN, 32 * WM, t)) return;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave / WN % WM, wn = wave % WN, wk = wave / (WM * WN);
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)lds));
   const uint32_t rb = static_cast<uint32_t>(p.K) * kEsz;   // bytes of a row of a and of W
   const int Nw = GATED ? 2 * p.N : p.N;
@@ -386,10 +391,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
   auto w_row = [&](int n) {
     return GATED ? (n / (NB / 2)) * (TN / 2) + (wn * (NB / 2) + n % (NB / 2)) * 32 : (wn * NB + n) * 32;
   };
-  uint32_t fb[4];   // the lane's fragment of k-step s
+  uint32_t fb[kSteps];   // the lane's fragment of the wave's k-step s
 #pragma unroll
-  for (int s = 0; s < 4; ++s)
-    fb[s] = (lane & 31) * kLinRow + ((2 * s + (lane >> 5)) ^ lin_key(lane & 31)) * 16;
+  for (int s = 0; s < kSteps; ++s)
+    fb[s] = (lane & 31) * kLinRow + ((2 * (kSteps * wk + s) + (lane >> 5)) ^ lin_key(lane & 31)) * 16;
 
   static_assert(S * kLoads < 64, "the load counter");
   for (int i = 0; i < S; ++i) {
@@ -440,10 +445,12 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
     Stage none{};
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(f0, r, 0, 0);
-    auto first = [&]() __attribute__((always_inline)) {   // k-steps 0 .. 2 of the stage in slot
+    auto first = [&]() __attribute__((always_inline)) {   // all k-steps but the last of the stage in slot
       step.template operator()<true, false>(f0, f1, slot, 1, none);
-      step.template operator()<true, false>(f1, f0, slot, 2, none);
-      step.template operator()<true, false>(f0, f1, slot, 3, none);
+      if constexpr (WK == 1) {
+        step.template operator()<true, false>(f1, f0, slot, 2, none);
+        step.template operator()<true, false>(f0, f1, slot, 3, none);
+      }
     };
     // this wave's reads of the stage are done, and its loads of the next have landed (all but those of the
     // LEFT stages behind it); behind the barrier every wave's are and have
@@ -479,6 +486,19 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile_kernel(LinearArgs p)
     [&]<int... A>(std::integer_sequence<int, A...>) {
       ((act == A ? k_loop(std::integral_constant<int, A>{}) : void()), ...);
     }(std::make_integer_sequence<int, MB>{});
+  }
+
+  if constexpr (WK == 2) {
+    static_assert(MB * NB * WM * WN * 4096 <= S * kStage, "the sums' LDS");
+    float* const red = reinterpret_cast<float*>(lds) + (wm * WN + wn) * MB * NB * 1024 + lane;
+    __syncthreads();   // (every wave's reads of the last stage are done)
+#pragma unroll
+    for (int i = 0; i < MB * NB * 16; ++i)
+      if (wk != 0) red[i * 64] = acc[i / 16 / NB][i / 16 % NB][i % 16];
+    __syncthreads();
+    if (wk != 0) return;
+#pragma unroll
+    for (int i = 0; i < MB * NB * 16; ++i) acc[i / 16 / NB][i / 16 % NB][i % 16] += red[i * 64];
   }
 
   // epilogue: 8 columns (n, u) of row block m a lane; their biases once, a row block's residual together
@@ -778,7 +798,7 @@ void launch_few(const LinearArgs& p, hipStream_t s) {
   else launch_few<F32, GATED, 2>(p, slots, s);
 }
 
-template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S>
+template <bool F32, bool GATED, int TM, int TN, int WM, int WN, int S, int WK = 1>
 void launch_tiles(LinearArgs p, hipStream_t s, int split, int tile_rows, void* ws) {
   constexpr int kCols = GATED ? TN / 2 : TN;
   const int stages = (p.K * (F32 ? 4 : 2) + kLinRow - 1) / kLinRow;
@@ -789,8 +809,8 @@ void launch_tiles(LinearArgs p, hipStream_t s, int split, int tile_rows, void* w
   const long long grid = (mt * nN * split + kNumXcd - 1) / kNumXcd * kNumXcd;
   p.split = split;
   p.part = split > 1 ? static_cast<float*>(ws) : nullptr;
-  hipLaunchKernelGGL((linear_tile_kernel<F32, GATED, TM, TN, WM, WN, S>), dim3(static_cast<unsigned>(grid)),
-                     dim3(64 * WM * WN), 0, s, p);
+  hipLaunchKernelGGL((linear_tile_kernel<F32, GATED, TM, TN, WM, WN, S, WK>), dim3(static_cast<unsigned>(grid)),
+                     dim3(64 * WM * WN * WK), 0, s, p);
   if (split > 1) {
     const long long lanes = static_cast<long long>(p.rows) * (p.N / 8);
     hipLaunchKernelGGL((linear_join_kernel<F32, GATED>), dim3(static_cast<unsigned>((lanes + 255) / 256)), dim3(256), 0, s,
@@ -818,9 +838,9 @@ namespace {
 //     320 x 256             69   69   72   94   94  110           297  343  333  347  401
 //       K in 4 parts        25   25   27   43   56  109            85  108  125  256  404
 // (K 14336, 2048 rows: 320 x 256 with 256-row tiles in 2 parts, 214 where 128 x 256 takes 212 in the same
-// process.)  fp32, N 4096, K 4096: 2000 rows 64 x 64 594, 128 x 128 495, few rows 852; 200 rows 82 (4 parts
-// 80), 256 (4 parts 80), 96.
-enum { LIN_FEW, LIN_64, LIN_128, LIN_320 };
+// process.)  fp32, N 4096, K 4096: 2000 rows 32 x 64 560, 128 x 128 491, few rows 842; 512 rows 153, 257 (2
+// parts 145), 226; 200 rows 82, 257 (4 parts 77), 96.
+enum { LIN_FEW, LIN_64, LIN_128, LIN_320, LIN_32 };   // (bf16: 64, 128, 320; fp32: 32, 128)
 struct LinPlan {
   int kind, split, tile_rows;
 };
@@ -851,7 +871,7 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
   };
   static const Shape bf16_shapes[] = {{LIN_64, 64, 64, 3, 3, 5, 0.31, 0.4}, {LIN_128, 128, 256, 1, 1, 6, 0.5, 1.02},
                                       {LIN_320, 320, 256, 1, 1, 8, 0.95, 1.75}};
-  static const Shape f32_shapes[] = {{LIN_64, 64, 64, 1, 3, 5, 0.6, 0.6}, {LIN_128, 128, 128, 1, 2, 6, 1.0, 2.0}};
+  static const Shape f32_shapes[] = {{LIN_32, 32, 64, 1, 4, 6, 0.28, 0.28}, {LIN_128, 128, 128, 1, 2, 6, 2.0, 2.0}};
   for (int i = 0; i < (f32 ? 2 : 3); ++i) {
     const Shape& s = f32 ? f32_shapes[i] : bf16_shapes[i];
     // m-tiles: uneven experts, a standard deviation of random routes above the mean
@@ -928,10 +948,14 @@ hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int3
   auto go = [&](auto f, auto g) {
     constexpr bool F = decltype(f)::value, G = decltype(g)::value;
     if (plan.kind == LIN_FEW) launch_few<F, G>(p, s);
-    else if (plan.kind == LIN_64) launch_tiles<F, G, 64, G ? 128 : 64, 2, 2, 3>(p, s, plan.split, 0, ws);
-    else if constexpr (F) launch_tiles<F, G, 128, 128, 2, 2, 2>(p, s, plan.split, 0, ws);
-    else if (plan.kind == LIN_128) launch_tiles<F, G, 128, 256, 2, 4, 3>(p, s, plan.split, 0, ws);
-    else launch_tiles<F, G, 320, 256, 2, 4, 2>(p, s, plan.split, plan.tile_rows, ws);
+    else if constexpr (F) {
+      if (plan.kind == LIN_32) launch_tiles<F, G, 32, G ? 128 : 64, 1, 2, 3, 2>(p, s, plan.split, 0, ws);
+      else launch_tiles<F, G, 128, 128, 2, 2, 2>(p, s, plan.split, 0, ws);
+    } else {
+      if (plan.kind == LIN_64) launch_tiles<F, G, 64, G ? 128 : 64, 2, 2, 3>(p, s, plan.split, 0, ws);
+      else if (plan.kind == LIN_128) launch_tiles<F, G, 128, 256, 2, 4, 3>(p, s, plan.split, 0, ws);
+      else launch_tiles<F, G, 320, 256, 2, 4, 2>(p, s, plan.split, plan.tile_rows, ws);
+    }
   };
   using T = std::true_type;
   using U = std::false_type;

@@ -151,8 +151,9 @@ def test_sizes(rows, E, K, N, gated, dt):
     (1024, 1, 14336, 4096, 0, BF), (900, 2, 14336, 4112, 2, BF),
     # 64 x 64 tiles with K in 4, 8 and 16 parts; a last part of one partial stage
     (600, 1, 8200, 1040, 0, BF), (64, 1, 4104, 272, 2, BF), (33, 1, 3336, 48, 0, BF),
-    # fp32: 128 x 128 tiles, alone and with K in parts; 64 x 64 ones with K in parts
-    (3000, 4, 520, 2064, 0, F32), (1000, 1, 14336, 1040, 0, F32), (200, 1, 4104, 528, 2, F32)])
+    # fp32: 128 x 128 tiles, alone and with K in parts; 32 x 64 ones, alone and with K in parts
+    (3000, 4, 520, 2064, 0, F32), (512, 1, 4096, 4096, 0, F32), (700, 3, 264, 2064, 2, F32), (1000, 1, 14336, 1040, 0, F32),
+    (200, 1, 4104, 528, 2, F32), (33, 1, 3336, 48, 0, F32)])
 def test_every_kernel(rows, E, K, Nw, k, dt, gated):
     """Sizes that take each of the tile kernels, with residual, kept z and a gated or plain epilogue."""
     _run_linear(rows, E, K, Nw // 2 if gated else Nw, dt, "gelu" if gated else "silu", gated, "f32", True, k, seed=rows)
