@@ -914,9 +914,9 @@ LinPlan lin_plan(int rows, int K, int Nw, int E, bool f32) {
 
 }  // namespace
 
-// whether the tiles of the smallest shape fit a launch
+// whether the tiles of every shape fit a launch: 32 rows and 32 columns or more a tile, K in up to 16 parts
 bool expert_linear_grid_fits(int rows, int N, int E) {
-  return (rows / 64ll + 1 + E) * (N / 32ll + 1) * 16 < (1ll << 31) - 8;
+  return (rows / 32ll + 1 + E) * (N / 32ll + 1) * 16 < (1ll << 31) - 8;
 }
 
 size_t expert_linear_ws_bytes(int rows, int K, int Nw, int E, bool f32) {

@@ -712,8 +712,9 @@ moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scal
  *   ws        workspace of moe_workspace_bytes(MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt) bytes
  *             (may be 0: then ws may be NULL).
  * Sums are fp32 in a fixed order; out comes from the unrounded z, with one rounding.  Requires
- * K % 8 == 0 and N % 8 == 0, K < 2^20, N < 2^24 and rows < 2^31 - 2^16, with src_slot a_nrows * K * sizeof(dt) <
- * 2^32 - 4096 (MOE_ERR_UNSUPPORTED otherwise); 16-byte aligned a, w, bias, residual, out, z, ws.
+ * K % 8 == 0 and N % 8 == 0, K < 2^20, N < 2^24, rows < 2^31 - 2^16 and (rows / 32 + E + 1) (N / 32 + 1) <
+ * 2^27 - 1, with src_slot a_nrows * K * sizeof(dt) < 2^32 - 4096 (MOE_ERR_UNSUPPORTED otherwise); 16-byte aligned a,
+ * w, bias, residual, out, z, ws.
  */
 moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int32_t* src_slot, int k,
                              const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,

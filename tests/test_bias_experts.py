@@ -151,7 +151,8 @@ def _linear(**kw):
     (dict(K=60), MOE_ERR_UNSUPPORTED), (dict(N=60), MOE_ERR_UNSUPPORTED), (dict(E=1025), MOE_ERR_UNSUPPORTED),
     (dict(K=1 << 20), MOE_ERR_UNSUPPORTED), (dict(N=1 << 24), MOE_ERR_UNSUPPORTED),
     (dict(a_nrows=1 << 20, K=2048), MOE_ERR_UNSUPPORTED), (dict(rows=2 ** 31 - 2 ** 16, N=8), MOE_ERR_UNSUPPORTED),
-    (dict(rows=2 ** 31 - 2 ** 16 - 1, N=1 << 20), MOE_ERR_UNSUPPORTED)])
+    (dict(rows=2 ** 31 - 2 ** 16 - 1, N=1 << 20), MOE_ERR_UNSUPPORTED),
+    (dict(rows=2 ** 31 - 2 ** 16 - 1, N=88), MOE_ERR_UNSUPPORTED)])
 def test_linear_refusals(bad, status):
     assert _linear(**bad) == status
 
