@@ -675,7 +675,7 @@ moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int
     return MOE_ERR_UNSUPPORTED;   // (32-bit offsets into the gathered operand)
   const int Nw = gated ? 2 * N : N;
   if (rows == 0) return MOE_OK;
-  if (!moe::expert_linear_grid_fits(rows, N, E)) return MOE_ERR_UNSUPPORTED;
+  if (!moe::expert_linear_grid_fits(rows, K, N, E, dt == MOE_F32, gated != 0)) return MOE_ERR_UNSUPPORTED;
   if (a == nullptr || w == nullptr || out == nullptr || (src_slot != nullptr && a_nrows == 0)) return MOE_ERR_INVALID_ARG;
   const size_t need = moe::expert_linear_ws_bytes(rows, K, Nw, E, dt == MOE_F32);
   if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;

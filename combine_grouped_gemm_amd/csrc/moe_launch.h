@@ -85,7 +85,7 @@ hipError_t launch_swiglu_backward_mx(const uint8_t* au, const uint8_t* au_scale,
                                      float* d_gate, hipStream_t s);
 
 // experts with biases (linear.hip, act_bwd.hip); src_slot, offsets, bias, residual, z, dz, db, h may be null
-bool expert_linear_grid_fits(int rows, int N, int E);
+bool expert_linear_grid_fits(int rows, int K, int N, int E, bool f32, bool gated);
 size_t expert_linear_ws_bytes(int rows, int K, int Nw, int E, bool f32);
 hipError_t launch_expert_linear(const void* a, bool f32, int a_nrows, const int32_t* src_slot, int k,
                                 const int32_t* offsets, int E, int rows, int K, int N, const void* w, const void* bias,

@@ -712,8 +712,9 @@ moe_status moe_swiglu_backward_mxfp8(const uint8_t* au_q, const uint8_t* au_scal
  *   ws        workspace of moe_workspace_bytes(MOE_OP_EXPERT_LINEAR, rows, K, Nw, E, 0, dt) bytes
  *             (may be 0: then ws may be NULL).
  * Sums are fp32 in a fixed order; out comes from the unrounded z, with one rounding.  Requires
- * K % 8 == 0 and N % 8 == 0, K < 2^20, N < 2^24, rows < 2^31 - 2^16 and (rows / 32 + E + 1) (N / 32 + 1) <
- * 2^27 - 1, with src_slot a_nrows * K * sizeof(dt) < 2^32 - 4096 (MOE_ERR_UNSUPPORTED otherwise); 16-byte aligned a,
+ * K % 8 == 0 and N % 8 == 0, K < 2^20, N < 2^24, rows < 2^31 - 2^16, (rows / 32 + E + 1) (N / 32 + 1) <
+ * 2^27 - 1, launches below 2^32 work-items (256 or 512 for every tile that a routing can need, of at least 32 rows of
+ * an expert and 64 columns, and every part of K: some 2^23 to 2^24 tiles), with src_slot a_nrows * K * sizeof(dt) < 2^32 - 4096 (MOE_ERR_UNSUPPORTED otherwise); 16-byte aligned a,
  * w, bias, residual, out, z, ws.
  */
 moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int32_t* src_slot, int k,
