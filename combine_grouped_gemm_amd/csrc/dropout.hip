@@ -15,6 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kDropThreads = 256;
+constexpr long long kMostItems = (1ll << 32) - 1;   // work-items of a launch
 
 __device__ __forceinline__ int in_rows(int r, int rows) { return r < rows ? r : -1; }   // (-1: no row)
 
@@ -143,14 +144,16 @@ __global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int
   }
 }
 
-// 8 elements a lane; the last n % 8 elements one by one
+// groups of 8 elements, one a lane (more where n needs more lanes than a launch takes); the last n % 8
+// elements one by one
 template <bool X32, bool Y32>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(const void* x, long long n, DropArgs drop,
                                                                const void* residual,
                                                                void* y) {
   const DropState ds = drop_state(drop);
-  const long long i = static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x;
-  if (i < n / 8) {
+  const long long step = static_cast<long long>(gridDim.x) * kDropThreads;
+  long long i = static_cast<long long>(blockIdx.x) * kDropThreads + threadIdx.x;
+  for (; i < n / 8; i += step) {
     const Raw8<X32> a = load_group<X32>(x, i);
     Raw8<Y32> re;
     if (residual != nullptr) re = load_group<Y32>(residual, i);
@@ -165,7 +168,8 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(const void* x, lo
       for (int j = 0; j < 8; ++j) v[j] += q[j];
     }
     store_group<Y32>(y, i, v);
-  } else if (i == n / 8 && n % 8 != 0) {
+  }
+  if (i == n / 8 && n % 8 != 0) {
     const uint4 w = philox(ds, i);
     float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     const int tail = static_cast<int>(n % 8);
@@ -251,8 +255,9 @@ hipError_t launch_combine_dropout_backward(const void* dy, bool dy_f32, bool f32
 
 hipError_t launch_dropout(const void* x, bool x_f32, long long n, double p, const uint64_t* rng, const void* residual,
                           void* y, bool y_f32, hipStream_t s) {
-  const long long lanes = (n + 7) / 8;
-  const dim3 grid(static_cast<unsigned>((lanes + kDropThreads - 1) / kDropThreads)), block(kDropThreads);
+  const long long groups = ((n + 7) / 8 + kDropThreads - 1) / kDropThreads;
+  const dim3 grid(static_cast<unsigned>(groups < kMostItems / kDropThreads ? groups : kMostItems / kDropThreads));
+  const dim3 block(kDropThreads);
   const DropArgs d = drop_args(p, rng);
   two(x_f32, y_f32, [&](auto a, auto b) {
     constexpr bool A = decltype(a)::value, B = decltype(b)::value;

@@ -274,3 +274,24 @@ def test_other_stream():
         got = moe.moe_dropout(x, 0.4, rng)
     side.synchronize()
     assert torch.equal(want, got)
+
+
+def _numbers(seed, offset, at, n):
+    """The numbers of elements at .. at + n - 1 (at a multiple of 8)."""
+    words = [w for i in range(at // 8, (at + n + 7) // 8) for w in oracle.philox((i & 0xFFFFFFFF, i >> 32, offset, 0), (seed, 0))]
+    return np.array([v for w in words for v in (w & 0xFFFF, w >> 16)])[:n]
+
+
+def test_rows_of_more_groups_than_a_launch_has_lanes():
+    """2^35 elements and some more: lanes take a second group, and the last elements follow the last whole one."""
+    n = 2 ** 35 + 2 ** 12 + 5
+    say(f"dropout n={n}")
+    x = torch.ones(n, dtype=BF, device=DEV)
+    moe.moe_dropout(x, 0.5, _state(1, 2), y=x)
+    sync()
+    starts = [0, 2 ** 34, 2 ** 35 - 4096, 2 ** 35 - 2048, 2 ** 35, n // 8 * 8 - 64]
+    parts = [x[a:a + 69].cpu() for a in starts]
+    del x
+    torch.cuda.empty_cache()
+    for a, part in zip(starts, parts):
+        assert np.array_equal(f64(part) * 0.5, (_numbers(1, 2, a, len(part)) >= 32768).astype(float)), a
