@@ -206,7 +206,7 @@ hipError_t launch_combine_dropout(const void* eo, bool eo_f32, int rows, int N, 
   // 128 lanes a token, 300 with one of 7 passes; 256 lanes leave more of the last pass idle (270).  Few
   // tokens: workgroups of one wave
   const int threads = N < 1024 || groups8 <= 64 ? 64 : 128;
-  const long long passes = (groups8 + threads - 1) / threads, most = ((1ll << 31) - 1) / N;
+  const long long passes = (groups8 + threads - 1) / threads, most = kMostItems / threads / N;   // (N < 2^24: 2 or more)
   const int spans = static_cast<int>(passes < most ? passes : most);
   const dim3 grid(static_cast<unsigned>(static_cast<long long>(N) * spans)), block(threads);
   const DropArgs d = drop_args(p, rng);

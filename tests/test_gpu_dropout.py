@@ -295,3 +295,21 @@ def test_rows_of_more_groups_than_a_launch_has_lanes():
     torch.cuda.empty_cache()
     for a, part in zip(starts, parts):
         assert np.array_equal(f64(part) * 0.5, (_numbers(1, 2, a, len(part)) >= 32768).astype(float)), a
+
+
+def test_combine_of_more_columns_than_a_launch_has_lanes():
+    """Tokens times columns past what one pass of a launch covers: the workgroups of a token take further columns."""
+    N, H = 11300000, 2056   # three passes of 128 lanes a token: 2^32 lanes and some more
+    say(f"combine dropout N={N} H={H}")
+    eo = torch.ones(3, H, dtype=BF, device=DEV)
+    eo[1], eo[2] = 2, 4
+    pos = (torch.arange(N, device=DEV) % 3).to(torch.int32)
+    y = torch.zeros(N, H, dtype=BF, device=DEV)
+    moe.moe_combine_dropout(eo, pos, None, 0.5, _state(1, 2), y=y, k=1)
+    sync()
+    rows = [0, 1, N // 2, N - 7, N - 1]
+    got = [y[t].cpu() for t in rows]
+    del y
+    torch.cuda.empty_cache()
+    for t, row in zip(rows, got):
+        assert np.array_equal(f64(row), np.where(_numbers(1, 2, t * H, H) >= 32768, 2.0 * 2 ** (t % 3), 0.0)), t
