@@ -117,7 +117,9 @@ inline long long lin_tile_groups(int rows, int E, int N, int tile_rows, int cols
 // Whether the launches of a call stay below 2^32 work-items each, the most that one takes, and the tiles of every
 // shape below the kernels' 32-bit numbers.  (The few-rows kernel's: N / 8 workgroups of 512 lanes at most.)
 inline bool lin_fits(int rows, int K, int N, int E, bool f32, bool gated) {
-  if ((rows / 32ll + 1 + E) * (N / 32ll + 1) * 16 >= (1ll << 31) - 8) return false;
+  const long long most = (rows / 32ll + 1 + E) * (N / 32ll + 1) * 16;   // workgroups of any shape and split, but for 8
+  if (most >= (1ll << 31) - 8) return false;
+  if (most < (1ll << 23) - 8) return true;   // (512 lanes each; a lane of the join has 8 columns of a row)
   const LinPlan plan = lin_plan(rows, K, gated ? 2 * N : N, E, f32);
   if (plan.kind == LIN_FEW) return true;
   const LinShape s = lin_shape(plan.kind, f32, gated);
