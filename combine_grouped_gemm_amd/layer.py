@@ -275,13 +275,23 @@ class MoELayer:
         return moe_grouped_ffn(a, self.shared_offsets, self.sw13, self.sw2, a_scale, self.sw13_scale,
                                self.sw2_scale, self._shared_out, self.shared_ws)
 
-    def combine(self, residual: Optional[torch.Tensor] = None):
-        if residual is not None or self.drop_p > 0.0:
+    def combine(self, residual: Optional[torch.Tensor] = None, dropout: float = 0.0,
+                rng: Optional[torch.Tensor] = None):
+        """y of the experts' outputs; residual, dropout and rng as forward takes them (what an earlier forward was
+        given does not count)."""
+        if residual is not None or dropout != 0.0:
+            _check_drop(self.N, self.H, self.act_dtype, self.device, residual, dropout, rng)
             return moe_combine_dropout(self.expert_out, self.layout[2], None if self.gate_in_down else self.topk_gate,
-                                       self.drop_p, self.rng_used, self.shared_out if self.shared else None, residual,
-                                       self.y, k=self.k)
+                                       dropout, self._drop_state() if rng is None else rng,
+                                       self.shared_out if self.shared else None, residual, self.y, k=self.k)
         return moe_combine(self.expert_out, self.layout[2], None if self.gate_in_down else self.topk_gate,
                            self.shared_out if self.shared else None, self.y, k=self.k)
+
+    def _drop_state(self) -> torch.Tensor:
+        """The buffer of the generator's state that the last forward used."""
+        if self.rng_used is None:
+            self.rng_used = torch.zeros(2, dtype=torch.int64, device=self.device)
+        return self.rng_used
 
     def launch_shared_side(self, x: torch.Tensor):
         """Enqueue the shared expert on the side stream, after the work queued so far."""
@@ -358,11 +368,8 @@ class MoELayer:
                 raise ValueError(f"a balance loss takes at most 65535 sequences, not {S}")
         _check_drop(self.N, self.H, self.act_dtype, self.device, residual, dropout, rng)
         self.drop_p = float(dropout)
-        if residual is not None or dropout > 0.0:
-            if self.rng_used is None:
-                self.rng_used = torch.zeros(2, dtype=torch.int64, device=self.device)
-            if rng is not None:
-                torch.add(rng, 0, out=self.rng_used)   # (the caller may advance rng before the backward)
+        if rng is not None and (residual is not None or dropout > 0.0):
+            torch.add(rng, 0, out=self._drop_state())   # (the caller may advance rng before the backward)
         self.keep8 = keep8
         self.save_au = bool(save_for_backward and not keep8 and self.fuse and not self.fp8)
         if self.save_au and self.au_all is None:
@@ -390,7 +397,7 @@ class MoELayer:
                 torch.cuda.current_stream(self.device).wait_event(self.shared_done)
             else:
                 self.shared_expert(x)
-        self.combine(residual)
+        self.combine(residual, self.drop_p, self.rng_used)
         return self.y
 
     # ---- backward (bf16 layers that gather their rows from x)

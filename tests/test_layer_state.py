@@ -74,3 +74,29 @@ def test_balance_buffers_are_bounded(monkeypatch):
     first = {}
     for S, at in calls:
         assert first.setdefault(S, at) == at
+
+
+def test_combine_alone_goes_by_its_own_arguments(monkeypatch):
+    """A combine call beside a forward (a step taken alone) drops out and adds what it is given, not what the last
+    forward was; a residual needs no generator's state."""
+    calls = []
+    monkeypatch.setattr(layer_module, "moe_combine", lambda *a, **kw: calls.append(("plain",)))
+    monkeypatch.setattr(layer_module, "moe_combine_dropout",
+                        lambda eo, pos, g, p, rng, sh=None, res=None, y=None, k=None: calls.append((p, rng, res)))
+    layer = _layer()
+    res, rng = torch.zeros(6, 128, dtype=torch.bfloat16), torch.tensor([1, 2])
+    layer.combine(res)
+    assert calls[-1][0] == 0.0 and calls[-1][1].shape == (2,) and calls[-1][2] is res
+    layer.drop_p, layer.rng_used = 0.25, torch.tensor([3, 4])     # as a forward with dropout leaves them
+    layer.combine()
+    assert calls[-1] == ("plain",)
+    layer.combine(res)
+    assert calls[-1][0] == 0.0 and calls[-1][2] is res
+    layer.combine(res, 0.5, rng)
+    assert calls[-1][0] == 0.5 and calls[-1][1] is rng and calls[-1][2] is res
+    before = len(calls)
+    for bad in (dict(dropout=0.5), dict(dropout=1.5, rng=rng), dict(dropout=-0.5, rng=rng), dict(dropout=float("nan"), rng=rng),
+                dict(residual=res.float()), dict(residual=res[:5])):
+        with pytest.raises(ValueError):
+            layer.combine(**bad)
+    assert len(calls) == before and layer.drop_p == 0.25
