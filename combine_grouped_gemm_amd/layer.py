@@ -38,6 +38,13 @@ from . import (MOE_ACT_GELU_TANH, MOE_ACT_NONE, MOE_ACT_SILU, MOE_BF16, MOE_BF16
                moe_swiglu_backward_mxfp8, moe_workspace_bytes, _balance_args, _expect)
 
 
+def _expect_dense(name: str, t: Optional[torch.Tensor], align: int = 16) -> None:
+    """Raises ValueError unless t (if given) lies in one piece, at a multiple of align bytes."""
+    if t is None or (t.is_contiguous() and t.data_ptr() % align == 0):
+        return
+    raise ValueError(f"{name} must be contiguous" if not t.is_contiguous() else f"{name} must be {align}-byte aligned")
+
+
 def _check_drop(N, H, dtype, device, residual, dropout, rng):
     """Raises ValueError unless residual, dropout and rng fit a layer's forward."""
     if not 0.0 <= dropout <= 1.0:
@@ -46,6 +53,7 @@ def _check_drop(N, H, dtype, device, residual, dropout, rng):
         raise ValueError("dropout needs rng, the generator's state (device int64 [2]: seed, offset)")
     _expect("rng", rng, (2,), (torch.int64,), device)
     _expect("residual", residual, (N, H), (dtype,), device)
+    _expect_dense("residual", residual)
 
 
 class MoELayer:
@@ -362,6 +370,8 @@ class MoELayer:
             _expect("x", x, (self.N, self.H), (torch.bfloat16,), self.device)
         if z is None and self.w_r is None:
             raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
+        _expect_dense("x", x)
+        _expect_dense("z", z, 4)
         if balance_alpha is not None:
             S = _balance_args(self.z if z is None else z, self.topk_idx, self.bias, seq_start, token_mask)[3]
             if S > 65535:
@@ -671,6 +681,9 @@ class BiasedMoELayer:
         _expect("b2", b2, (E, H), (torch.float32, dt), dev)
         _expect("bias", bias, (E,), (torch.float32,), dev)
         _expect("w_r", w_r, (E, H), (dt,), dev)
+        for name, t in (("w1", w1), ("w2", w2), ("b1", b1), ("b2", b2), ("w_r", w_r)):
+            _expect_dense(name, t)
+        _expect_dense("bias", bias, 4)
         self.N, self.H, self.E, self.k, self.I = N, H, E, k, I
         self.w1, self.w2, self.b1, self.b2, self.act, self.gated = w1, w2, b1, b2, act, bool(gated)
         self.n_group, self.topk_group, self.bias, self.w_r = n_group, topk_group, bias, w_r
@@ -711,6 +724,8 @@ class BiasedMoELayer:
         if z is None and self.w_r is None:
             raise ValueError("forward needs the logits z, or a layer built with the router weight w_r")
         _expect("z", z, (N, E), (torch.float32,), self.device)
+        _expect_dense("x", x)
+        _expect_dense("z", z, 4)
         _check_drop(N, self.H, dt, self.device, residual, dropout, rng)
         self.drop_p = float(dropout)
         if rng is not None:

@@ -100,3 +100,36 @@ def test_combine_alone_goes_by_its_own_arguments(monkeypatch):
         with pytest.raises(ValueError):
             layer.combine(**bad)
     assert len(calls) == before and layer.drop_p == 0.25
+
+
+def test_tensors_that_the_launches_would_refuse_leave_the_last_forward_in_place():
+    """Strided or unaligned tokens, logits and residuals are refused before anything changes, in either layer."""
+    from combine_grouped_gemm_amd.layer import BiasedMoELayer
+    bf = torch.bfloat16
+    biased = BiasedMoELayer(6, 128, 4, 2, 128, torch.zeros(4, 128, 128, dtype=bf), torch.zeros(4, 128, 128, dtype=bf),
+                            w_r=torch.zeros(4, 128, dtype=bf))
+    x = torch.zeros(6, 128, dtype=bf)
+    strided, shifted = torch.zeros(6, 256, dtype=bf)[:, ::2], torch.zeros(6 * 128 + 1, dtype=bf)[1:].view(6, 128)
+    assert strided.shape == shifted.shape == x.shape and shifted.data_ptr() % 16
+    for layer, names in ((_layer(), STATE + ("drop_p", "rng_used")), (biased, ("drop_p", "rng_used", "pre", "saved"))):
+        layer.drop_p, layer.rng_used = 0.125, torch.tensor([3, 4])
+        layer.saved = layer.save_au = True
+        before = {n: getattr(layer, n) for n in names}
+        for bad in (dict(x=strided), dict(x=shifted), dict(x=x, residual=strided), dict(x=x, residual=shifted),
+                    dict(x=x, z=torch.zeros(6, 8)[:, ::2])):
+            with pytest.raises(ValueError):
+                layer.forward(**bad, dropout=0.5, rng=torch.tensor([5, 6]))
+            assert all(getattr(layer, n) is v for n, v in before.items()) and layer.rng_used.tolist() == [3, 4]
+
+
+def test_biased_layer_refuses_strided_weights():
+    from combine_grouped_gemm_amd.layer import BiasedMoELayer
+    bf = torch.bfloat16
+    good = dict(N=6, H=128, E=4, k=2, I=64, w1=torch.zeros(4, 64, 128, dtype=bf), w2=torch.zeros(4, 128, 64, dtype=bf),
+                b1=torch.zeros(4, 64), b2=torch.zeros(4, 128, dtype=bf), w_r=torch.zeros(4, 128, dtype=bf),
+                bias=torch.zeros(4))
+    BiasedMoELayer(**good)
+    for n in ("w1", "w2", "b1", "b2", "w_r", "bias"):
+        t = good[n]
+        with pytest.raises(ValueError, match=n):
+            BiasedMoELayer(**{**good, n: torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype)[..., ::2]})
