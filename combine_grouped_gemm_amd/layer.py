@@ -762,7 +762,7 @@ class BiasedMoELayer:
 
             Nw = self.w1.shape[1]
             b = dict(d_eo=new(rows, H), dg=new(N, k, dtype=torch.float32), dh=new(rows, I), dpre=new(rows, Nw),
-                     h=new(rows, I), x_perm=new(rows, H), d_perm=new(rows, H), dx=new(N, H),
+                     x_perm=new(rows, H), d_perm=new(rows, H), dx=new(N, H),
                      dw1=new(E, Nw, H, dtype=dw_dtype), dw2=new(E, H, I, dtype=dw_dtype),
                      db1=new(E, Nw, dtype=torch.float32), db2=new(E, H, dtype=torch.float32))
             for name, args in (("act_ws", (MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0)),
@@ -777,9 +777,9 @@ class BiasedMoELayer:
                                      b["dg"])
         moe_expert_act_backward(b["d_eo"], offsets=offsets, want_dz=False, db=b["db2"], ws=b["b2_ws"])
         moe_expert_dgrad(b["d_eo"], offsets, self.w2, b["dh"], b["dgrad_ws"])
-        moe_expert_act_backward(b["dh"], self.pre, offsets, self.act, self.gated, dz=b["dpre"], db=b["db1"], h=b["h"],
+        moe_expert_act_backward(b["dh"], self.pre, offsets, self.act, self.gated, dz=b["dpre"], db=b["db1"],
                                 ws=b["act_ws"])
-        moe_expert_wgrad(b["d_eo"], b["h"], offsets, dw=b["dw2"], rows=rows)
+        moe_expert_wgrad(b["d_eo"], self.h, offsets, dw=b["dw2"], rows=rows)   # (the h that w2 multiplied)
         moe_permute(x, send_pos, k, None, b["x_perm"])
         moe_expert_wgrad(b["dpre"], b["x_perm"], offsets, dw=b["dw1"], rows=rows)
         moe_expert_dgrad(b["dpre"], offsets, self.w1, b["d_perm"], b["dgrad_ws"])

@@ -252,3 +252,21 @@ def test_other_layers_with_dropout_and_residual(name, gate_in_down):
     half = 2.0 ** -24 if y.dtype == F32 else 2.0 ** -8
     assert np.all(np.abs(f64(y) - ref) <= half * np.abs(ref) + (cfg.k + 3) * 2.0 ** -23 * mag)
     assert torch.equal(layer.forward(inp["x"], inp["z"]), y0)
+
+
+@pytest.mark.parametrize("act,gated", [("gelu_tanh", False), ("silu", True), ("relu2", False)])
+def test_second_weights_gradient_takes_the_forwards_h(act, gated):
+    """dw2 is d_eo^T h of the h that w2 multiplied, to the rounding of its fp32 sums: act of the kept, rounded
+    pre-activations differs from that h in every other digit of bf16."""
+    N, H, E, k, I = 300, 256, 5, 2, 384
+    say(f"dw2 of the forward's h {act} gated={gated}")
+    layer, x, res, z = _biased(N, H, E, k, I, BF, act, gated, seed=90)
+    layer.forward(x, z, save_for_backward=True, residual=res)
+    gr = layer.backward(x, _t((N, H), 91, BF), dw_dtype=F32)
+    sync()
+    off, h, d_eo = layer.layout[1].tolist(), f64(layer.h), f64(gr["d_eo"])
+    for e in range(E):
+        s = slice(off[e], off[e + 1])
+        # products of bf16 values are exact in fp32; their sum rounds once an addition, in any order
+        lim = 2 * (off[e + 1] - off[e] + 16) * 2.0 ** -24 * (np.abs(d_eo[s]).T @ np.abs(h[s]))
+        assert np.all(np.abs(f64(gr["dw2"][e]) - d_eo[s].T @ h[s]) <= lim), e
