@@ -81,7 +81,7 @@ __device__ __forceinline__ void act8_slope(int act, float (&v)[8], float (&s)[8]
     case MOE_ACT_RELU:
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s[i] = v[i] > 0.0f ? 1.0f : 0.0f;
+        s[i] = v[i] > 0.0f ? 1.0f : (v[i] <= 0.0f ? 0.0f : v[i]);   // (NaN stays)
         v[i] = v[i] < 0.0f ? 0.0f : v[i];
       }
       break;

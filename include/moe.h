@@ -739,8 +739,8 @@ moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int
  *   dz [rows, Nw], h [rows, N] of dt out, or NULL: rows of no expert are left as they are.
  *   db        [E, Nw] of db_dt (MOE_F32 or MOE_BF16) out, or NULL; zeros for an expert without rows.
  *   ws        moe_workspace_bytes(MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0) bytes (may be 0; not read when db is NULL).
- * max(x, 0) has slope 0 at 0.  db sums the unrounded dz in fp32 in a fixed order.  Requires N % 8 ==
- * 0, N < 2^24, rows < 2^31 - 2^16; 16-byte aligned arrays.  dz, db and h not all NULL.
+ * max(x, 0) has slope 0 at 0; a NaN in z reaches its dz, db and h.  db sums the unrounded dz in fp32 in a fixed
+ * order.  Requires N % 8 == 0, N < 2^24, rows < 2^31 - 2^16; 16-byte aligned arrays.  dz, db and h not all NULL.
  */
 moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype dt, const int32_t* offsets, int E,
                                    int rows, int N, moe_act act, int gated, void* dz, void* db, moe_dtype db_dt,

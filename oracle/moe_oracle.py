@@ -660,7 +660,7 @@ ACTIVATIONS = {
 
 ACTIVATION_SLOPES = {
     "none": np.ones_like,
-    "relu": lambda x: (x > 0).astype(np.float64),
+    "relu": lambda x: np.where(np.isnan(x), x, (x > 0).astype(np.float64)),
     "relu2": lambda x: 2.0 * np.maximum(x, 0.0),
     "gelu": lambda x: _normal_cdf(x) + x * np.exp(-0.5 * x * x) / np.sqrt(2.0 * np.pi),
     "gelu_tanh": lambda x: (lambda e: 1.0 / (1.0 + e) + x * e / (1.0 + e) ** 2 * 2.0 * np.sqrt(2.0 / np.pi)

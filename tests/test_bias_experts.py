@@ -371,3 +371,9 @@ def test_biased_layer_refusals():
     fits = BiasedMoELayer(6, 128, 4, 2, 128, torch.zeros(4, 128, 128, dtype=bf), torch.zeros(4, 128, 128, dtype=bf))
     with pytest.raises(ValueError, match="save_for_backward"):
         fits.backward(x, x)
+
+
+@pytest.mark.parametrize("act", sorted(set(oracle.ACTIVATIONS) - {"none"}))
+def test_slopes_of_nan_are_nan(act):
+    x = np.array([np.nan, 1.0])
+    assert np.isnan(oracle.ACTIVATION_SLOPES[act](x)).tolist() == [True, False] and np.isnan(oracle.ACTIVATIONS[act](x[:1])).all()

@@ -452,3 +452,20 @@ def test_act_backward_of_large_calls(gated):
     mag = torch.stack([dz[:5000].abs().double().sum(dim=0), dz[5000:].abs().double().sum(dim=0)])
     # two fp32 sums of the same values in other orders: at most rows + 8 roundings of the magnitudes' sum each
     assert ((db.double() - sums).abs() <= 2 * (rows + 8) * U32 * mag).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("rows", [1, 700])
+@pytest.mark.parametrize("act", sorted(set(ACT) - {"none"}))
+def test_a_nan_pre_activation_reaches_dz_db_and_h(act, rows, dt):
+    """A NaN in z is not hidden by the slope: its element of dz and h and its column of its expert's db are NaN, nothing
+    else is."""
+    z, d = _t((rows, 24), 1, dt), torch.ones(rows, 24, dtype=dt)
+    z[rows - 1, 5] = float("nan")
+    off = torch.tensor([0, rows - 1, rows], dtype=torch.int32)
+    dz, db, h = moe.moe_expert_act_backward(d.to(DEV), z=z.to(DEV), offsets=off.to(DEV), act=ACT[act], want_h=True)
+    sync()
+    at = torch.zeros(rows, 24, dtype=torch.bool)
+    at[rows - 1, 5] = True
+    assert torch.equal(torch.isnan(dz).cpu(), at) and torch.equal(torch.isnan(h).cpu(), at)
+    assert torch.isnan(db).nonzero().tolist() == [[1, 5]]
