@@ -106,7 +106,8 @@ __device__ __forceinline__ void act8_slope(int act, float (&v)[8], float (&s)[8]
     case MOE_ACT_GELU_TANH:
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float x = v[i], x2 = x * x;
+        // (bounded: far out sg (1 - sg) is 0, and 0 times an infinity would be NaN)
+        const float x = v[i], x2 = fminf(x * x, 1e30f);
         const float sg = sigmoid_act<F32>(kGeluC * (x + kGeluB * x2 * x));
         s[i] = sg + x * sg * (1.0f - sg) * (kGeluC * (1.0f + 3.0f * kGeluB * x2));
         v[i] = x * sg;

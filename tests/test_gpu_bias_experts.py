@@ -469,3 +469,25 @@ def test_a_nan_pre_activation_reaches_dz_db_and_h(act, rows, dt):
     at[rows - 1, 5] = True
     assert torch.equal(torch.isnan(dz).cpu(), at) and torch.equal(torch.isnan(h).cpu(), at)
     assert torch.isnan(db).nonzero().tolist() == [[1, 5]]
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_large_finite_pre_activations(act, dt):
+    """Far from 0 these activations are x or 0 and their slopes 1 or 0, also where a power of x passes 2^128."""
+    v = torch.tensor([100.0, 1e10, 3e13, 2e19, 3e38, -100.0, -1e10, -3e13, -2e19, -3e38, 1e25, -1e25, 1e37, -1e37, 50.0, -50.0])
+    z, d = v.to(dt).reshape(1, 16).to(DEV), torch.full((1, 16), 0.5, dtype=dt, device=DEV)
+    dz, db, h = moe.moe_expert_act_backward(d, z=z, act=ACT[act], want_h=True)
+    u = torch.ones(1, 16, dtype=dt, device=DEV)
+    gz, gb, gh = moe.moe_expert_act_backward(d, z=torch.cat([z, u], dim=1), act=ACT[act], gated=True, want_h=True)
+    a = torch.zeros(1, 16, dtype=dt, device=DEV)
+    a[0, 0] = 1
+    w = torch.zeros(1, 16, 16, dtype=dt, device=DEV)
+    w[0, :, 0] = z[0]
+    out, _ = moe.moe_expert_linear(a, w, act=ACT[act])
+    sync()
+    up = (v > 0).reshape(1, 16)
+    for got in (dz, db, gz[:, :16], gb[:, :16]):    # 50 below 0 act is below 1e-19, its slope below 1e-17
+        assert ((got.cpu().double() - 0.5 * up).abs() <= 1e-17).all()
+    for got in (h, gh, out, gz[:, 16:].double() * 2):
+        assert torch.equal(got.cpu().double()[up], z.cpu().double()[up]) and (got.cpu().double()[~up].abs() < 1e-19).all()
