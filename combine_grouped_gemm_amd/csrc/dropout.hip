@@ -112,12 +112,15 @@ __global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int
       float d[8];
       raw_values<DY32>(rd, d);
       drop8(ds, w, d);
+      uint32_t kept[DT32 ? 8 : 4];
+      keep8<DT32>(ds, w, kept);
       if (d_shared != nullptr && j0 == 0) store_group<DT32>(d_shared, at, d);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j) {
         if (r[j] < 0) continue;
         float v[8];
         if (d_gate != nullptr) {
+          mask_raw<DT32>(b[j], kept);   // (0 times an infinity would be NaN)
           raw_values<DT32>(b[j], v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], v[i], dot[j]);

@@ -64,4 +64,20 @@ __device__ __forceinline__ void drop8(const DropState& d, uint4 w, float (&v)[8]
   }
 }
 
+// masks over 8 loaded elements (4 words of two bf16 each, or 8 of fp32): all ones where drop8 keeps one
+template <bool F32>
+__device__ __forceinline__ void keep8(const DropState& d, uint4 w, uint32_t (&m)[F32 ? 8 : 4]) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool lo = (q[j] & 0xFFFFu) >= d.cut, hi = (q[j] >> 16) >= d.cut;
+    if constexpr (F32) {
+      m[2 * j] = lo ? ~0u : 0u;
+      m[2 * j + 1] = hi ? ~0u : 0u;
+    } else {
+      m[j] = (lo ? 0xFFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
+    }
+  }
+}
+
 }  // namespace moe

@@ -74,6 +74,18 @@ __device__ __forceinline__ void raw_values(const Raw8<kEoF32>& r, float (&v)[8])
   }
 }
 
+// the loaded columns whose mask is 0 (keep8 of philox.h) become 0, whatever they held
+template <bool F32>
+__device__ __forceinline__ void mask_raw(Raw8<F32>& r, const uint32_t (&m)[F32 ? 8 : 4]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    r.w[i].x &= m[4 * i];
+    r.w[i].y &= m[4 * i + 1];
+    r.w[i].z &= m[4 * i + 2];
+    r.w[i].w &= m[4 * i + 3];
+  }
+}
+
 // 8 values (8 adjacent elements) to group i of a matrix of fp32 or bf16; NT: with the non-temporal hint (a
 // constant: of two branches that differ in the hint alone the compiler makes one, without it)
 template <bool F32, bool NT = false>

@@ -783,7 +783,8 @@ moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows
  *   expert_out, d_expert_out  [rows, H] of dt (MOE_F32 or MOE_BF16); rows that no slot names are left
  *              as they are.  expert_out may be NULL when d_gate is.
  *   topk_gate  [N, k] fp32, or NULL (1).
- *   d_gate     [N, k] fp32 out (0 for a slot without a row), or NULL.
+ *   d_gate     [N, k] fp32 out (0 for a slot without a row), or NULL.  Dropped elements do not count, whatever
+ *              expert_out holds there.
  *   d_shared   [N, H] of dt out, or NULL.
  * Dot products are fp32 in a fixed order.  Requires H % 8 == 0; 16-byte aligned arrays.
  */

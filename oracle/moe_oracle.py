@@ -755,5 +755,5 @@ def combine_dropout_backward(dy, send_pos, gates, expert_out, p, seed, offset):
             r = send_pos[t * k + j]
             if r >= 0:
                 d_eo[r] = gates[t, j] * d[t]
-                d_gate[t, j] = d[t] @ expert_out[r]
+                d_gate[t, j] = d[t] @ np.where(m[t] > 0, expert_out[r], 0.0)   # (nothing of what was dropped)
     return d_eo, d_gate, d

@@ -377,3 +377,17 @@ def test_biased_layer_refusals():
 def test_slopes_of_nan_are_nan(act):
     x = np.array([np.nan, 1.0])
     assert np.isnan(oracle.ACTIVATION_SLOPES[act](x)).tolist() == [True, False] and np.isnan(oracle.ACTIVATIONS[act](x[:1])).all()
+
+
+def test_a_dropped_expert_output_does_not_count_in_the_gates_gradient():
+    """y holds nothing of a dropped element's sum, so the gates' gradient takes nothing of what its rows held."""
+    rng = np.random.default_rng(8)
+    N, k, H = 4, 2, 32
+    eo, g, dy = rng.normal(size=(N * k, H)), rng.random((N, k)), rng.normal(size=(N, H))
+    pos = np.arange(N * k)
+    gone = (oracle.dropout_mask(0.5, 3, 4, N * H) == 0).reshape(N, H).repeat(k, axis=0)
+    bad = eo.copy()
+    bad[gone] = np.where(rng.random(gone.sum()) < 0.5, np.nan, np.inf)
+    assert np.isfinite(oracle.combine_dropout(bad, pos, g, 0.5, 3, 4)).all()
+    want, got = (oracle.combine_dropout_backward(dy, pos, g, v, 0.5, 3, 4)[1] for v in (eo, bad))
+    assert np.allclose(got, want, rtol=1e-13, atol=0)

@@ -313,3 +313,23 @@ def test_combine_of_more_columns_than_a_launch_has_lanes():
     torch.cuda.empty_cache()
     for t, row in zip(rows, got):
         assert np.array_equal(f64(row), np.where(_numbers(1, 2, t * H, H) >= 32768, 2.0 * 2 ** (t % 3), 0.0)), t
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("N,k,H", [(8, 2, 64), (5, 9, 264), (3, 4, 16392)])
+def test_dropped_expert_outputs_do_not_reach_the_gates_gradient(N, k, H, dt):
+    """Infinities and NaN where y dropped the sum: the gates' gradient is that of zeros there, bit for bit; where it did
+    not, they show."""
+    eo, g, dy = _t((N * k, H), 1, dt).to(DEV), torch.rand(N, k, device=DEV), _t((N, H), 2, dt).to(DEV)
+    pos = torch.arange(N * k, dtype=torch.int32, device=DEV)
+    gone = torch.from_numpy(oracle.dropout_mask(0.5, 3, 4, N * H) == 0).reshape(N, H).repeat_interleave(k, dim=0).to(DEV)
+    bad = torch.where(gone, torch.full_like(eo, float("inf")), eo)
+    bad[:, ::3] = torch.where(gone, torch.full_like(eo, float("nan")), eo)[:, ::3]
+    zero = torch.where(gone, torch.zeros_like(eo), eo)
+    got, want, plain = (moe.moe_combine_dropout_backward(dy, pos, g, v, 0.5, _state(3, 4)) for v in (bad, zero, eo))
+    kept = int((~gone[1]).nonzero()[0])
+    bad[1, kept] = float("nan")
+    _, dg, _ = moe.moe_combine_dropout_backward(dy, pos, g, bad, 0.5, _state(3, 4))
+    sync()
+    assert all(torch.equal(a, b) and torch.equal(b, c) for a, b, c in zip(got[:2], want[:2], plain[:2]))
+    assert torch.isnan(dg.reshape(-1)).nonzero().tolist() == [[1]]
