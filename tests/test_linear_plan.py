@@ -44,3 +44,46 @@ def test_what_fits_stays_below_the_limit():
             assert (rows // 32 + E + 1) * (N // 32 + 1) >= 2 ** 27 - 1 or p.groups * p.threads >= 2 ** 32, s
         assert p.split * 8 <= max(s[1] * (4 if s[4] else 2) / 128 + 1, 8), s   # (every part of K has stages)
     assert most > 2 ** 30
+
+
+def _sizes(test, names):
+    """The parametrized sizes of a GPU test."""
+    mark, = [m for m in test.pytestmark if m.name == "parametrize" and m.args[0] == names]
+    return mark.args[1]
+
+
+def _take(cases, gated):
+    import torch
+    return plans([(rows, K, Nw // 2 if gated else Nw, E, dt == torch.float32, gated) for rows, E, K, Nw, k, dt in cases])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_gpu_tests_of_every_kernel_take_it(gated):
+    """The sizes by which the GPU tests reach each kernel, whole K and K in parts, still do."""
+    from tests import test_gpu_bias_experts as t
+    got = [(p.kind, p.split > 1) for p in _take(_sizes(t.test_every_kernel, "rows,E,K,Nw,k,dt"), gated)]
+    assert got == [("320", False)] * 3 + [("128", False)] * 2 + [("128", True)] + [("320", True)] * 2 + [("64", True)] * 3 + [
+        ("128", False), ("128", True), ("32", False)] + [("32", True)] * 3
+    tall = _take(_sizes(t.test_every_kernel, "rows,E,K,Nw,k,dt")[:1], gated)[0]
+    assert tall.tile_rows == 192   # (320-row tiles made shorter to fill a round)
+    few = _sizes(t.test_few_rows, "rows,E,K,Nw,k,dt")
+    assert {p.kind for p in _take(few, gated)} == {"few"}
+    # 16 weight rows a workgroup up to 128 groups of 32, else 32
+    groups = [min(E, rows) * -(-Nw // 32) for rows, E, K, Nw, k, dt in few]
+    assert [n <= 128 for n in groups] == [True] * 4 + [False] * 6
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_the_small_sizes_take_64_row_tiles_whole(gated, f32):
+    """64 x 64 tiles (bf16) and 32 x 64 (fp32) with K whole are reached by the general sizes."""
+    from tests import test_gpu_bias_experts as t
+    kinds = {(p.kind, p.split) for p in plans([(rows, K, N, E, f32, gated) for rows, E, K, N in t.SIZES])}
+    assert ("32" if f32 else "64", 1) in kinds and ("few", 1) in kinds
+
+
+def test_the_gpu_tests_of_many_experts_take_tiles():
+    import torch
+    from tests import test_gpu_many_experts as t
+    got = plans([(rows, K, N, E, dt == torch.float32, gated) for rows, E, K, N, dt, gated, _, _ in t.CASES])
+    assert [(p.kind, p.split) for p in got] == [c[6:] for c in t.CASES] and all(c[1] > 64 for c in t.CASES)
