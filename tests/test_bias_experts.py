@@ -391,3 +391,27 @@ def test_a_dropped_expert_output_does_not_count_in_the_gates_gradient():
     assert np.isfinite(oracle.combine_dropout(bad, pos, g, 0.5, 3, 4)).all()
     want, got = (oracle.combine_dropout_backward(dy, pos, g, v, 0.5, 3, 4)[1] for v in (eo, bad))
     assert np.allclose(got, want, rtol=1e-13, atol=0)
+
+
+def test_a_planted_missing_scale_shows_along_the_gradient():
+    """Along a unit direction of a returned gradient the value moves by the gradient's norm; with a mask that does not
+    scale (planted here) it moves by 4/3 of it."""
+    rng = np.random.default_rng(9)
+    N, k, E, H, I = 12, 2, 3, 16, 8
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(N)])
+    _, off, pos, slot = oracle.dispatch_layout(idx, E)
+    x, g, dy = rng.normal(size=(N, H)), rng.random((N, k)), rng.normal(size=(N, H))
+    w1, w2, b2 = rng.normal(size=(E, I, H)), rng.normal(size=(E, H, I)), rng.normal(size=(E, H))
+    h, _ = oracle.expert_linear(x, off, w1, None, "silu", tokens=slot // k)
+
+    def value(b):
+        eo, _ = oracle.expert_linear(h, off, w2, b)
+        return (oracle.combine_dropout(eo, pos, g, 0.25, 5, 6) * dy).sum()
+
+    eo, _ = oracle.expert_linear(h, off, w2, b2)
+    d_eo, _, _ = oracle.combine_dropout_backward(dy, pos, g, eo, 0.25, 5, 6)
+    for scale, ratio in ((1.0, 1.0), (3 / 4, 4 / 3)):
+        db = scale * np.stack([d_eo[off[e]:off[e + 1]].sum(axis=0) for e in range(E)])
+        norm = np.linalg.norm(db)
+        want = (value(b2 + 1e-4 * db / norm) - value(b2 - 1e-4 * db / norm)) / 2e-4
+        assert abs(want / norm - ratio) < 1e-7

@@ -270,3 +270,36 @@ def test_second_weights_gradient_takes_the_forwards_h(act, gated):
         # products of bf16 values are exact in fp32; their sum rounds once an addition, in any order
         lim = 2 * (off[e + 1] - off[e] + 16) * 2.0 ** -24 * (np.abs(d_eo[s]).T @ np.abs(h[s]))
         assert np.all(np.abs(f64(gr["dw2"][e]) - d_eo[s].T @ h[s]) <= lim), e
+
+
+@pytest.mark.parametrize("act,gated,p", [("gelu_tanh", False, 0.25), ("silu", True, 0.25), ("gelu", False, 0.0)])
+def test_biased_gradients_along_themselves(act, gated, p):
+    """<dy, y> moves along each returned gradient, of b1, b2, w1, w2 and x (routes and gates held), by its square norm.
+
+    For a gradient within GRAD_BAR of the true one g in norm, <g, v> along v = got / |got| lies within GRAD_BAR |g| of
+    |got|; a missing dropout scale (4/3) or a missing part of the chain rule moves it by a quarter and more."""
+    N, H, E, k, I = 200, 128, 4, 2, 128
+    say(f"gradients along themselves {act} gated={gated} p={p}")
+    layer, x, res, z = _biased(N, H, E, k, I, BF, act, gated, w_r=False, seed=40)
+    rng = torch.tensor([8, 1], dtype=torch.int64, device=DEV)
+    dy = _t((N, H), 50, BF)
+    layer.forward(x, z, save_for_backward=True, residual=res, dropout=p, rng=rng)
+    gr = layer.backward(x, dy, dw_dtype=F32)
+    sync()
+    g = f64(layer.topk_gate)
+    _, offsets, send_pos, src_slot = oracle.dispatch_layout(layer.topk_idx.cpu().numpy(), E)
+    mask = oracle.dropout_mask(p, 8, 1, N * H).reshape(N, H)
+    at = {n: f64(t) for n, t in (("b1", layer.b1), ("b2", layer.b2), ("w1", layer.w1), ("w2", layer.w2), ("x", x))}
+
+    def value(q):
+        h, _ = oracle.expert_linear(q["x"], offsets, q["w1"], q["b1"], act, gated, tokens=src_slot // k)
+        eo, _ = oracle.expert_linear(h, offsets, q["w2"], q["b2"])
+        return (oracle.combine_dropout(eo, send_pos, g, 0.0, 0, 0) * mask * f64(dy)).sum()
+
+    for n, got in (("b1", gr["db1"]), ("b2", gr["db2"]), ("w1", gr["dw1"]), ("w2", gr["dw2"]), ("x", gr["dx"])):
+        got = f64(got).reshape(at[n].shape)
+        norm = np.linalg.norm(got)
+        step = 1e-4 / norm * got      # (a unit direction: the next term of the difference is below 1e-8 of it)
+        want = (value({**at, n: at[n] + step}) - value({**at, n: at[n] - step})) / 2e-4
+        say(f"  {n}: {want / norm:.4f}")
+        assert abs(want / norm - 1) <= GRAD_BAR / (1 - GRAD_BAR), n
