@@ -806,7 +806,9 @@ moe_status moe_dropout(const void* x, moe_dtype x_dt, int64_t n, double p, const
 /*
  * moe_workspace_bytes -- bytes of workspace `op` needs for these sizes (0 if none).
  * For MOE_OP_GROUPED_FFN and MOE_OP_EXPERT_GEMM pass the GEMMs' row count as N.
- * Arguments that an op does not use are ignored.  Returns 0 for invalid sizes.
+ * Arguments that an op does not use are ignored.  Returns 0 for invalid sizes.  The answer is for exactly these
+ * sizes and may shrink as N grows (another kernel takes over, or other ranges): a workspace that serves
+ * several sizes has the largest of their answers.  A call with less than its own returns MOE_ERR_WORKSPACE.
  */
 size_t moe_workspace_bytes(int op, int N, int H, int I, int E, int k, int a_dt);
 
