@@ -45,3 +45,29 @@ def _segments(kind, rows, E):
 def test_many_experts(rows, E, K, N, dt, gated, kernel, parts, kind):
     _run_linear(rows, E, K, N, dt, gated=gated, residual=gated, k=0 if K < 100 else 3, seed=rows,
                 offsets=_segments(kind, rows, E))
+
+
+def test_the_largest_launch_is_complete():
+    """Rows just below the refused ones (2^32 work-items): the first, the last and those between are computed."""
+    import combine_grouped_gemm_amd as moe
+    from tests.gpu_util import say, sync
+    rows = 2 ** 30 - 1024      # 2^24 - 16 tiles of 64 rows, 256 lanes each
+    say(f"linear rows={rows} K=8 N=8")
+    dev = torch.device("cuda:0")
+    at = torch.tensor([0, 63, 64, 2 ** 28 + 5, 2 ** 29, rows // 3 * 2, rows - 65, rows - 64, rows - 1], device=dev)
+    a = torch.zeros(rows, 8, dtype=BF, device=dev)
+    rand = lambda seed, *shape: torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(dev)  # noqa: E731
+    a[at] = rand(1, len(at), 8).to(BF)
+    w, b = rand(2, 1, 8, 8).to(BF), rand(3, 1, 8)
+    out, _ = moe.moe_expert_linear(a, w, bias=b)
+    want = (a[at].double() @ w[0].double().T + b.double()).float().to(BF)
+    got, plain = out[at], b.to(BF)
+    others = (out[1:63] == plain).all() & (out[-63:-1] == plain).all() & (out[2 ** 29 + 1:2 ** 29 + 10 ** 6] == plain).all()
+    sync()
+    assert others.item()
+    # 8 exact products and a bias in fp32, each addition off by 2^-24 of the magnitudes' sum at most; then a rounding on
+    # either side, half a step each
+    mag = a[at].double().abs() @ w[0].double().abs().T + b.double().abs()
+    assert ((got.double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 20 * 2.0 ** -24 * mag).all()
+    del a, out
+    torch.cuda.empty_cache()
