@@ -24,7 +24,9 @@ constexpr int kLinXcds = 8;
 //       K in 4 parts        25   25   27   43   56  109            85  108  125  256  404
 // (K 14336, 2048 rows: 320 x 256 with 256-row tiles in 2 parts, 214 where 128 x 256 takes 212 in the same
 // process.)  fp32, N 4096, K 4096: 2000 rows 32 x 64 560, 128 x 128 491, few rows 842; 512 rows 153, 257 (2
-// parts 145), 226; 200 rows 82, 257 (4 parts 77), 96.
+// parts 145), 226; 200 rows 82, 257 (4 parts 77), 96.  Gated calls run 64 x 128 and 32 x 128 tiles in place of
+// 64 x 64 and 32 x 64 (half as many, each with twice the work, fewer of them a CU); the estimate takes the plain
+// shapes' counts and constants for them, which no gated runs have been fitted to.
 enum { LIN_FEW, LIN_64, LIN_128, LIN_320, LIN_32 };   // (bf16: 64, 128, 320; fp32: 32, 128)
 struct LinPlan {
   int kind, split, tile_rows;
