@@ -76,14 +76,15 @@ __global__ __launch_bounds__(kDropThreads) void combine_dropout_kernel(
 }
 
 // One workgroup takes a token: a lane forms d for its 8 columns once and goes through the token's rows
-// in batches of KMAX (k > KMAX: d again for each batch); the rows' dot products are kept per lane and
-// summed over the workgroup at the end of a batch, in a fixed order.  8192 tokens of 7168, k 8, shared
-// rows: 398 us (5.3 TB/s) with non-temporal stores of d_expert_out, 428 without.
+// in batches of KMAX (k > KMAX: d again for each batch, so d_shared, which may be dy, is written in the
+// last one); the rows' dot products are kept per lane and summed over the workgroup at the end of a batch,
+// in a fixed order.  8192 tokens of 7168, k 8, shared rows: 398 us (5.3 TB/s) with non-temporal stores of
+// d_expert_out, 428 without.
 template <int KMAX, bool DT32, bool DY32, bool NT>
-__global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int rows, int H, int k,
+__global__ void combine_dropout_backward_kernel(const void* dy, int rows, int H, int k,
                                                 const int32_t* __restrict__ send_pos, const float* __restrict__ gate,
                                                 const void* __restrict__ eo, DropArgs drop, void* __restrict__ d_eo,
-                                                float* __restrict__ d_gate, void* __restrict__ d_shared) {
+                                                float* __restrict__ d_gate, void* d_shared) {
   __shared__ float red[16][KMAX];
   const int t = blockIdx.x;
   const DropState ds = drop_state(drop);
@@ -114,7 +115,7 @@ __global__ void combine_dropout_backward_kernel(const void* __restrict__ dy, int
       drop8(ds, w, d);
       uint32_t kept[DT32 ? 8 : 4];
       keep8<DT32>(ds, w, kept);
-      if (d_shared != nullptr && j0 == 0) store_group<DT32>(d_shared, at, d);
+      if (d_shared != nullptr && j0 + KMAX >= k) store_group<DT32>(d_shared, at, d);
 #pragma unroll
       for (int j = 0; j < KMAX; ++j) {
         if (r[j] < 0) continue;

@@ -740,7 +740,7 @@ moe_status moe_expert_linear(const void* a, moe_dtype dt, int a_nrows, const int
  *   db        [E, Nw] of db_dt (MOE_F32 or MOE_BF16) out, or NULL; zeros for an expert without rows.
  *   ws        moe_workspace_bytes(MOE_OP_ACT_BACKWARD, rows, 0, Nw, E, 0, 0) bytes (may be 0; not read when db is NULL).
  * max(x, 0) has slope 0 at 0; a NaN in z reaches its dz, db and h.  db sums the unrounded dz in fp32 in a fixed
- * order.  Requires N % 8 == 0, N < 2^24, rows < 2^31 - 2^16; 16-byte aligned arrays.  dz, db and h not all NULL.
+ * order.  dz may be z and h may be d_out; otherwise outputs overlap no other argument.  Requires N % 8 == 0, N < 2^24, rows < 2^31 - 2^16; 16-byte aligned arrays.  dz, db and h not all NULL.
  */
 moe_status moe_expert_act_backward(const void* z, const void* d_out, moe_dtype dt, const int32_t* offsets, int E,
                                    int rows, int N, moe_act act, int gated, void* dz, void* db, moe_dtype db_dt,
@@ -785,7 +785,7 @@ moe_status moe_combine_dropout(const void* expert_out, moe_dtype eo_dt, int rows
  *   topk_gate  [N, k] fp32, or NULL (1).
  *   d_gate     [N, k] fp32 out (0 for a slot without a row), or NULL.  Dropped elements do not count, whatever
  *              expert_out holds there.
- *   d_shared   [N, H] of dt out, or NULL.
+ *   d_shared   [N, H] of dt out, or NULL; may be dy (of one type).  Otherwise outputs overlap no other argument.
  * Dot products are fp32 in a fixed order.  Requires H % 8 == 0; 16-byte aligned arrays.
  */
 moe_status moe_combine_dropout_backward(const void* dy, moe_dtype dy_dt, moe_dtype dt, int rows, int N, int H, int k,

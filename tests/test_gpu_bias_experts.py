@@ -491,3 +491,17 @@ def test_large_finite_pre_activations(act, dt):
         assert ((got.cpu().double() - 0.5 * up).abs() <= 1e-17).all()
     for got in (h, gh, out, gz[:, 16:].double() * 2):
         assert torch.equal(got.cpu().double()[up], z.cpu().double()[up]) and (got.cpu().double()[~up].abs() < 1e-19).all()
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("rows,E,N,gated", [(3, 1, 8, False), (300, 4, 520, True), (300, 4, 520, False), (5000, 6, 264, True),
+                                            (70000, 3, 2056, False)])
+def test_act_backward_in_place(rows, E, N, gated, dt):
+    """dz may be z, and h d_out."""
+    off = _offsets(rows, E, 3).to(DEV)
+    z, d = _t((rows, 2 * N if gated else N), 1, dt).to(DEV), _t((rows, N), 2, dt).to(DEV)
+    kw = dict(offsets=off, act=ACT["gelu"], gated=gated)
+    want = moe.moe_expert_act_backward(d, z=z, want_h=True, **kw)
+    got = moe.moe_expert_act_backward(d, z=z, dz=z, h=d, **kw)
+    sync()
+    assert got[0] is z and got[2] is d and all(torch.equal(a, b) for a, b in zip(want, got))

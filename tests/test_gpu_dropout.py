@@ -333,3 +333,15 @@ def test_dropped_expert_outputs_do_not_reach_the_gates_gradient(N, k, H, dt):
     sync()
     assert all(torch.equal(a, b) and torch.equal(b, c) for a, b, c in zip(got[:2], want[:2], plain[:2]))
     assert torch.isnan(dg.reshape(-1)).nonzero().tolist() == [[1]]
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("N,k,H", [(6, 2, 72), (5, 9, 136), (3, 32, 2056), (2, 17, 16392)])
+def test_shared_gradient_in_place(N, k, H, dt):
+    """d_shared may be dy, also where a token's slots take several passes over it."""
+    eo, dy, g = _t((N * k, H), 1, dt).to(DEV), _t((N, H), 2, dt).to(DEV), torch.rand(N, k, device=DEV)
+    pos = torch.arange(N * k, dtype=torch.int32, device=DEV)
+    want = moe.moe_combine_dropout_backward(dy, pos, g, eo, 0.4, _state(3, 4), want_shared=True)
+    got = moe.moe_combine_dropout_backward(dy, pos, g, eo, 0.4, _state(3, 4), d_shared=dy)
+    sync()
+    assert got[2] is dy and all(torch.equal(a, b) for a, b in zip(want, got))
